@@ -16,6 +16,10 @@ fallback: if the library is missing, the first call of any binding function rais
 * ``rgdr_prefill`` / ``rgdr_prefill_gated`` -- the same recurrence over long sequences
   (T up to 65536; the page's notes hand prefill to a chunk-level operator), same arguments.
 * ``la_gate`` -- the gate front end (README "com.microsoft.LinearAttentionGate").
+* ``la_decode`` / ``la_prefill`` -- linear attention with a decay for each head (no delta
+  correction), for a few tokens and for prompts, on pools of fp32, bf16 or 8-bit states.
+* ``la_state_quantize`` / ``la_state_dequantize`` -- states into and out of 8-bit pools.
+* ``la_norm_gate`` -- the per-head norm of the outputs times the output gate.
 * ``rgdr_validate`` -- synchronous check of the index arrays.
 
 A non-OK status from the library raises ``RuntimeError`` (the page's error behaviour).
@@ -34,17 +38,27 @@ __all__ = ["rgdr_decode", "rgdr_decode_snapshots", "rgdr_decode_gated",
            "rgdr_decode_gated_snapshots", "rgdr_prefill", "rgdr_prefill_gated",
            "rgdr_prefill_ws", "rgdr_prefill_gated_ws", "rgdr_prefill_workspace_size",
            "rgdr_prefill_noalloc",
-           "recurrent_gated_delta_rule", "la_gate",
+           "recurrent_gated_delta_rule", "la_gate", "la_decode", "la_prefill",
+           "la_prefill_workspace_size", "la_state_quantize", "la_state_dequantize",
+           "la_norm_gate",
            "rgdr_validate", "VALIDATE",
            "rgdr_validate_host", "status_string", "library", "LIB_PATH", "RGDR_F32",
-           "RGDR_F16", "RGDR_BF16"]
+           "RGDR_F16", "RGDR_BF16", "RGDR_MXI8"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librgdr.so")
 
-RGDR_F32, RGDR_F16, RGDR_BF16 = 0, 1, 2
+RGDR_F32, RGDR_F16, RGDR_BF16, RGDR_MXI8 = 0, 1, 2, 3
 RGDR_NORMALIZE_QK = 1  # option bit of rgdr_decode_gated
 NORMALIZE_QK = RGDR_NORMALIZE_QK
+LA_GATE_SIGMOID = 1    # option bit of la_norm_gate
+LA_BLOCK = 32          # columns of a state row that share a scale byte in an 8-bit pool
 _DTYPE_CODE = {torch.float32: RGDR_F32, torch.float16: RGDR_F16, torch.bfloat16: RGDR_BF16}
+
+
+
+class _Strides(C.Structure):  # la_strides of include/rgdr.h
+    _fields_ = [("b", C.c_int64), ("h", C.c_int64), ("t", C.c_int64)]
+
 
 _lib = None
 VALIDATE = os.environ.get("RGDR_VALIDATE", "") == "1"
@@ -86,6 +100,21 @@ def library():
                                           + [vp] * 2 + [C.c_uint32, vp, C.c_size_t, vp])
     lib.la_gate.restype = C.c_int
     lib.la_gate.argtypes = [vp, vp, vp, vp, C.c_int, i64, i32, vp, C.c_int, vp, C.c_int, vp]
+    st = C.POINTER(_Strides)
+    lib.la_decode.restype = C.c_int
+    lib.la_decode.argtypes = ([vp, st] * 4 + [vp, vp, C.c_int] + [vp] * 3 + [f32] + [i32] * 7
+                              + [vp, st, vp, vp, vp])
+    lib.la_prefill.restype = C.c_int
+    lib.la_prefill.argtypes = lib.la_decode.argtypes[:-1] + [vp, C.c_size_t, vp]
+    lib.la_prefill_workspace_size.restype = C.c_int
+    lib.la_prefill_workspace_size.argtypes = [i32] * 5 + [C.POINTER(C.c_size_t)]
+    lib.la_state_quantize.restype = C.c_int
+    lib.la_state_quantize.argtypes = [vp, C.c_int, i32, vp, vp, vp, i32, vp] + [i32] * 4 + [vp]
+    lib.la_state_dequantize.restype = C.c_int
+    lib.la_state_dequantize.argtypes = [vp, vp, i32, vp, vp, C.c_int, i32, vp] + [i32] * 4 + [vp]
+    lib.la_norm_gate.restype = C.c_int
+    lib.la_norm_gate.argtypes = ([vp, st, vp, st, vp, i64, C.c_int, vp, f32, C.c_uint32]
+                                 + [i32] * 4 + [vp, st, vp])
     lib.rgdr_validate.restype = C.c_int
     lib.rgdr_validate.argtypes = [vp, vp, vp, i32, i32, i32, vp]
     lib.rgdr_validate_host.restype = C.c_int
@@ -495,6 +524,300 @@ def la_gate(a, dt_bias, decay_scale, b=None, *, want_beta=None, decay_dtype=None
                          _stream_handle(stream, a.device))
     _check(rc, "la_gate")
     return decay_out, beta_t
+
+
+def _rows(t, name, dtypes, ndim=4):
+    """A [B, H, T, D] operand whose D elements are contiguous; the other axes may have any
+    strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} must be on the GPU")
+    if t.dtype not in dtypes:
+        raise RuntimeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise RuntimeError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if ndim == 4 and t.shape[3] > 1 and t.stride(3) != 1:
+        raise RuntimeError(f"{name}: the last axis must be contiguous")
+    return t
+
+
+def _index(t, name, n):
+    if t is None:
+        return None
+    _dev(t, name, torch.int32, 1)
+    if t.shape[0] != n:
+        raise RuntimeError(f"{name} must have shape [{n}]")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a kernel on `stream`. The allocator hands out memory whose earlier use is
+    over on the stream it allocates for, so it is asked with that stream current."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+_STATE_TYPES = (torch.float32, torch.bfloat16, torch.int8)
+
+
+def _scales(state, scales, name):
+    """The scale bytes of an 8-bit pool, checked against its codes; None for other pools."""
+    if state.dtype != torch.int8:
+        if scales is not None:
+            raise RuntimeError(f"{name}: only an int8 pool has scales")
+        return None
+    if scales is None:
+        raise RuntimeError(f"an int8 pool needs {name}")
+    _dev(scales, name, torch.uint8, 4)
+    if state.shape[3] % LA_BLOCK or \
+            tuple(scales.shape) != (*state.shape[:3], state.shape[3] // LA_BLOCK):
+        raise RuntimeError(f"{name} must be [N_slots, H_v, D_k, D_v / {LA_BLOCK}]")
+    return scales
+
+
+def _la_call(fn, query, key, value, g, state_pool, lens, idx, nacc, scale, state_scales, out,
+             state_out, state_scales_out, stream, workspace=None):
+    lib = library()
+    _rows(query, "query", (torch.bfloat16,))
+    _rows(key, "key", (torch.bfloat16,))
+    _rows(value, "value", (torch.bfloat16,))
+    B, Hq, T, Dk = query.shape
+    Hv, Dv = value.shape[1], value.shape[3]
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        g = g[None, :, None].expand(B, g.shape[0], T)  # one decay for each head
+    _rows(g, "g", (torch.float32,), 3)
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dtype not in _STATE_TYPES:
+        raise RuntimeError("state_pool must be a float32, bfloat16 or int8 tensor")
+    _dev(state_pool, "state_pool", state_pool.dtype, 4)
+    N = state_pool.shape[0]
+    if tuple(key.shape) != (B, Hq, T, Dk) or tuple(value.shape) != (B, Hv, T, Dv) \
+            or tuple(g.shape) != (B, Hv, T) or tuple(state_pool.shape) != (N, Hv, Dk, Dv):
+        raise RuntimeError(f"{fn}: inconsistent shapes")
+    state_scales = _scales(state_pool, state_scales, "state_scales")
+    if state_out is None:
+        if state_scales_out is not None:
+            raise RuntimeError("state_scales_out goes with state_out")
+        state_out, state_scales_out = state_pool, state_scales
+    else:
+        _dev(state_out, "state_out", state_pool.dtype, 4)
+        if state_out.shape != state_pool.shape:
+            raise RuntimeError("state_out must have the pool's shape")
+        state_scales_out = _scales(state_out, state_scales_out, "state_scales_out")
+    index = {"actual_seq_lengths": lens, "ssm_state_indices": idx, "num_accepted_tokens": nacc}
+    ptrs = [_index(t, nm, B) for nm, t in index.items()]
+    if out is not None:
+        _rows(out, "out", (torch.bfloat16,))
+        if tuple(out.shape) != (B, Hv, T, Dv):
+            raise RuntimeError("out must be [B, H_v, T, D_v]")
+    _same_device(query, key=key, value=value, g=g, state_pool=state_pool, out=out,
+                 state_scales=state_scales, state_out=state_out,
+                 state_scales_out=state_scales_out, **index)
+    if out is None:
+        out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
+    with torch.cuda.device(query.device):
+        if VALIDATE and B:
+            def given(t, other):
+                return t if t is not None else torch.as_tensor(other, dtype=torch.int32,
+                                                               device=query.device)
+            n = given(lens, [T] * B)
+            _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N)
+        ws = ()
+        if fn == "la_prefill":
+            if workspace is None:
+                size = la_prefill_workspace_size(B, Hv, T, Dk, Dv, query.device)
+                if size:
+                    workspace = _empty(size, torch.uint8, query.device, stream)
+            elif workspace.dtype != torch.uint8 or not workspace.is_cuda \
+                    or not workspace.is_contiguous():
+                raise RuntimeError("workspace must be a contiguous uint8 CUDA tensor")
+            _same_device(query, workspace=workspace)
+            ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        args = []
+        for t in (query, key, value, g):
+            args += [t.data_ptr(), _Strides(*t.stride()[:3])]
+        rc = getattr(lib, fn)(
+            *args, state_pool.data_ptr(), _ptr(state_scales), _state_code(state_pool.dtype),
+            *ptrs, float(scale), B, Hq, Hv, T, Dk, Dv, N, out.data_ptr(),
+            _Strides(*out.stride()[:3]), state_out.data_ptr(), _ptr(state_scales_out), *ws,
+            _stream_handle(stream, query.device))
+    _check(rc, fn)
+    return (out, state_out) if state_scales is None else (out, state_out, state_scales_out)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _state_code(dtype):
+    return RGDR_MXI8 if dtype == torch.int8 else _DTYPE_CODE[dtype]
+
+
+def la_decode(query, key, value, g, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
+              num_accepted_tokens=None, scale=1.0, *, state_scales=None, out=None,
+              state_out=None, state_scales_out=None, stream=None):
+    """Linear attention with a decay for each head, T <= 8 tokens per entry:
+    ``S = exp(g) S + k v^T``, ``o = S^T (scale q)``; returns ``(out, state_out)``, for an int8
+    pool ``(out, state_out, state_scales_out)``.
+
+    query/key bf16 ``[B,H_q,T,D_k]``, value bf16 ``[B,H_v,T,D_v]``: any strides, the last axis
+    contiguous, rows at multiples of 8 elements (``x.transpose(1, 2)`` of a ``[B,T,H,D]``
+    projection is fine). g fp32 ``[B,H_v,T]`` of any strides (``la_gate``'s decay with its last
+    axes transposed), or ``[H_v]``: one decay for each head. state_pool float32, bfloat16 or int8
+    ``[N_slots,H_v,D_k,D_v]``; an int8 pool comes with ``state_scales``, uint8
+    ``[N_slots,H_v,D_k,D_v/32]``. The index arrays are int32 ``[B]`` as in ``rgdr_decode``; left
+    out, every token is valid, entry b is in slot b and every valid token is accepted. The state
+    is updated in place unless ``state_out`` is given.
+    """
+    return _la_call("la_decode", query, key, value, g, state_pool, actual_seq_lengths,
+                    ssm_state_indices, num_accepted_tokens, scale, state_scales, out, state_out,
+                    state_scales_out, stream)
+
+
+def la_prefill(query, key, value, g, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
+               num_accepted_tokens=None, scale=1.0, *, state_scales=None, workspace=None,
+               out=None, state_out=None, state_scales_out=None, stream=None):
+    """``la_decode`` over whole prompts (T up to 65536); arguments and results as there.
+
+    ``workspace``: a uint8 CUDA tensor of ``la_prefill_workspace_size`` bytes for calls of few
+    entries, which then work on parts of a prompt at once; allocated for the call when None."""
+    return _la_call("la_prefill", query, key, value, g, state_pool, actual_seq_lengths,
+                    ssm_state_indices, num_accepted_tokens, scale, state_scales, out, state_out,
+                    state_scales_out, stream, workspace)
+
+
+def la_prefill_workspace_size(B, H_v, T, D_k, D_v, device=None):
+    """Bytes of workspace that ``la_prefill`` uses for a call of these sizes on ``device`` (0:
+    it needs none)."""
+    lib = library()
+    n = C.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        rc = lib.la_prefill_workspace_size(B, H_v, T, D_k, D_v, C.byref(n))
+    _check(rc, "la_prefill_workspace_size")
+    return n.value
+
+
+def _slots(src_slots, dst_slots, n_src):
+    """The number of entries of a state move: the index arrays' length, or every source."""
+    for t in (src_slots, dst_slots):
+        if t is not None:
+            return t.shape[0]
+    return n_src
+
+
+def la_state_quantize(state, codes=None, scales=None, *, src_slots=None, dst_slots=None,
+                      stream=None):
+    """Slots ``src_slots`` of ``state`` (float32 or bfloat16 ``[N,H_v,D_k,D_v]``) into slots
+    ``dst_slots`` of an 8-bit pool; returns ``(codes, scales)``, int8 ``[M,H_v,D_k,D_v]`` and
+    uint8 ``[M,H_v,D_k,D_v/32]`` (value = code * 2^(scale - 127)).
+
+    The slot arrays are int32 ``[n]`` (None: entry i is slot i). Without ``codes`` and
+    ``scales``, a pool of n slots is allocated, in entry order. A source slot out of range counts
+    as a zero state, an entry whose destination is out of range is skipped."""
+    if not isinstance(state, torch.Tensor) or state.dtype not in (torch.float32, torch.bfloat16):
+        raise RuntimeError("state must be a float32 or bfloat16 tensor")
+    _dev(state, "state", state.dtype, 4)
+    N, H, Dk, Dv = state.shape
+    n = _slots(src_slots, dst_slots, N)
+    if Dv % LA_BLOCK:
+        raise RuntimeError(f"D_v must be a multiple of {LA_BLOCK}")
+    if (codes is None) != (scales is None):
+        raise RuntimeError("codes and scales go together")
+    if codes is None:
+        if dst_slots is not None:
+            raise RuntimeError("dst_slots names slots of given codes and scales")
+        codes = _empty((n, H, Dk, Dv), torch.int8, state.device, stream)
+        scales = _empty((n, H, Dk, Dv // LA_BLOCK), torch.uint8, state.device, stream)
+    return _move("la_state_quantize", state, codes, scales, src_slots, dst_slots, n, stream)
+
+
+def la_state_dequantize(codes, scales, state=None, *, dtype=torch.bfloat16, src_slots=None,
+                        dst_slots=None, stream=None):
+    """The way back: slots ``src_slots`` of the 8-bit pool into slots ``dst_slots`` of ``state``
+    (float32 or bfloat16; allocated with ``dtype``, in entry order, when None). Returns
+    ``state``. Both types hold the 8-bit values exactly. Slots as in ``la_state_quantize``."""
+    _dev(codes, "codes", torch.int8, 4)
+    n = _slots(src_slots, dst_slots, codes.shape[0])
+    if state is None:
+        if dst_slots is not None:
+            raise RuntimeError("dst_slots names slots of a given state")
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise RuntimeError("dtype must be float32 or bfloat16")
+        state = _empty((n, *codes.shape[1:]), dtype, codes.device, stream)
+    elif state.dtype not in (torch.float32, torch.bfloat16):
+        raise RuntimeError("state must be a float32 or bfloat16 tensor")
+    _move("la_state_dequantize", state, codes, scales, src_slots, dst_slots, n, stream)
+    return state
+
+
+def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
+    lib = library()
+    _dev(state, "state", state.dtype, 4)
+    _dev(codes, "codes", torch.int8, 4)
+    if codes.shape[1:] != state.shape[1:]:
+        raise RuntimeError(f"{fn}: codes and state must have the same [H_v, D_k, D_v]")
+    _scales(codes, scales, "scales")
+    src, dst = _index(src_slots, "src_slots", n), _index(dst_slots, "dst_slots", n)
+    _same_device(state, codes=codes, scales=scales, src_slots=src_slots, dst_slots=dst_slots)
+    H, Dk, Dv = state.shape[1:]
+    wide = (state.data_ptr(), _DTYPE_CODE[state.dtype])
+    packed = (codes.data_ptr(), scales.data_ptr())
+    with torch.cuda.device(state.device):
+        if n == 0:
+            return codes, scales
+        if fn == "la_state_quantize":
+            args = (*wide, state.shape[0], src, *packed, codes.shape[0], dst)
+        else:
+            args = (*packed, codes.shape[0], src, *wide, state.shape[0], dst)
+        rc = getattr(lib, fn)(*args, n, H, Dk, Dv, _stream_handle(stream, state.device))
+    _check(rc, fn)
+    return codes, scales
+
+
+def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_lengths=None,
+                 out=None, stream=None):
+    """The norm and gate behind the attention: ``weight * x / sqrt(mean(x^2) + eps) *
+    silu(gate)`` over rows of D values (``sigmoid``: sigmoid(gate) instead; no gate: the norm).
+
+    ``x`` ``[B,H,T,D]`` as ``la_decode`` and ``rgdr_decode`` return it, ``gate`` ``[B,T,H,D]``
+    as a projection gives it; float32, float16 or bfloat16, any strides with the last axis
+    contiguous and rows at multiples of 8 elements, D a multiple of 8 up to 8192. ``weight``
+    float32 ``[D]`` or ``[H,D]``. Returns ``out``, ``[B,T,H,D]`` of x's type; rows of tokens past
+    ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
+    lib = library()
+    types = tuple(_DTYPE_CODE)
+    _rows(x, "x", types)
+    B, H, T, D = x.shape
+    for nm, t in (("gate", gate), ("out", out)):
+        if t is not None:
+            _rows(t, nm, (x.dtype,))
+            if tuple(t.shape) != (B, T, H, D):
+                raise RuntimeError(f"{nm} must be [B, T, H, D]")
+    if not isinstance(weight, torch.Tensor) or tuple(weight.shape) not in ((D,), (H, D)):
+        raise RuntimeError("weight must be a [D] or [H, D] tensor")
+    _dev(weight, "weight", torch.float32)
+    lens = _index(actual_seq_lengths, "actual_seq_lengths", B)
+    _same_device(x, weight=weight, gate=gate, out=out, actual_seq_lengths=actual_seq_lengths)
+    if out is None:
+        out = _empty((B, T, H, D), x.dtype, x.device, stream)
+    if x.numel() == 0:
+        return out
+
+    def bht(t):  # the strides of a [B, T, H, D] tensor
+        return _Strides(t.stride(0), t.stride(2), t.stride(1))
+
+    with torch.cuda.device(x.device):
+        rc = lib.la_norm_gate(x.data_ptr(), _Strides(*x.stride()[:3]), _ptr(gate),
+                              None if gate is None else bht(gate), weight.data_ptr(),
+                              D if weight.dim() == 2 else 0, _DTYPE_CODE[x.dtype], lens,
+                              float(eps), LA_GATE_SIGMOID if sigmoid else 0, B, H, T, D,
+                              out.data_ptr(), bht(out), _stream_handle(stream, x.device))
+    _check(rc, "la_norm_gate")
+    return out
 
 
 def rgdr_validate(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N_slots,

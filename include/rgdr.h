@@ -1,7 +1,7 @@
 /*
  * rgdr.h -- C ABI of the gfx950 (MI355X) gated-delta-rule decode library.
  *
- * Three operations:
+ * Operations:
  *
  *   rgdr_decode  The recurrent gated-delta-rule decode step of the MindSpore Lite API page
  *                "lite_boost.ops.recurrent_gated_delta_rule" (algorithm section, parameter
@@ -23,6 +23,17 @@
  *                (Description; Inputs, Outputs, Type constraints tables):
  *                  decay = decay_scale[h] * softplus(a + dt_bias[h]),  beta = sigmoid(b),
  *                computed in fp32 and narrowed only on store.
+ *   la_decode, la_prefill
+ *                Linear attention with a decay for each head (no delta correction), the layer
+ *                that hybrid models run beside the gated delta rule: S = exp(g) S + k (x) v,
+ *                o = S^T (q * scale), for a few tokens and for whole prompts, on pools of fp32,
+ *                bf16 or 8-bit states.
+ *   la_state_quantize, la_state_dequantize
+ *                Move states between a pool of fp32 or bf16 (of either attention) and a pool
+ *                that holds them in 8 bits.
+ *   la_norm_gate The gate's other end: the per-head root-mean-square norm of the attention's
+ *                outputs times silu (or sigmoid) of a gate, written in the layout that the
+ *                output projection reads.
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers to row-major, contiguous buffers owned by
@@ -68,7 +79,9 @@ typedef enum {
                                  than the library's fixed array holds                       */
 } rgdr_status;
 
-typedef enum { RGDR_F32 = 0, RGDR_F16 = 1, RGDR_BF16 = 2 } rgdr_dtype;
+/* RGDR_MXI8 is a state type only (la_decode, la_prefill): signed 8-bit codes and, for each
+   block of 32 columns of a state row, one byte e; a value is code * 2^(e - 127). */
+typedef enum { RGDR_F32 = 0, RGDR_F16 = 1, RGDR_BF16 = 2, RGDR_MXI8 = 3 } rgdr_dtype;
 
 /* Option bits of rgdr_decode_gated. */
 enum { RGDR_NORMALIZE_QK = 1u /* L2-normalise each token's query and key head vector */ };
@@ -343,6 +356,159 @@ rgdr_status la_gate(const void *a, const float *dt_bias, const float *decay_scal
                     const void *b, rgdr_dtype ab_dtype, int64_t n_rows, int32_t H,
                     void *decay_out, rgdr_dtype decay_dtype, void *beta_out,
                     rgdr_dtype beta_dtype, hipStream_t stream);
+
+/* Element strides of a [B, H, T, D] operand whose D elements are contiguous. */
+typedef struct { int64_t b, h, t; } la_strides;
+
+/*
+ * la_decode -- linear attention with a decay for each head, T <= 8 tokens per batch entry. For
+ * every entry b, value head h and valid token t, in token order, on the state S (D_k rows,
+ * D_v columns):
+ *     S = exp(g[b,h,t]) S + k_t (x) v_t,       o_t = S^T (q_t * scale).
+ *
+ *   query, key    bf16 [B, H_q, T, D_k]; value head h reads query/key head h / (H_v / H_q).
+ *   value         bf16 [B, H_v, T, D_v].
+ *   g             fp32 [B, H_v, T] log decay (la_gate's decay; <= 0 in use, not checked). Values
+ *                 below -1024 act as -1024 (the state is forgotten either way), -infinity too.
+ *   *_strides     element strides of the four operands, or NULL for a contiguous one; 0 repeats
+ *                 an operand along that axis (a per-head decay [H_v] has strides {0, 1, 0}).
+ *                 Query, key and value rows start at multiples of 8 elements, their bases are
+ *                 16-byte aligned. Strides are not negative.
+ *   state_pool    [N_slots, H_v, D_k, D_v] of state_dtype: RGDR_F32, RGDR_BF16 or RGDR_MXI8
+ *                 (int8 codes). 16-byte aligned.
+ *   state_scales  RGDR_MXI8: uint8 [N_slots, H_v, D_k, D_v / 32], 16-byte aligned; else unused
+ *                 (may be NULL), as state_scales_out.
+ *   actual_seq_lengths, ssm_state_indices, num_accepted_tokens
+ *                 int32 [B], as in rgdr_decode; each may be NULL: all T tokens valid, entry b
+ *                 in slot b (needs N_slots >= B), every valid token accepted.
+ *   scale, B, H_q, H_v, T   as in rgdr_decode.
+ *   D_k, D_v      D_k in {64, 128, 256}; D_v a multiple of 32 up to 4096.
+ *   out           bf16 [B, H_v, T, D_v] with out_strides (NULL: contiguous; rows must not
+ *                 overlap), written entirely: rows of tokens past an entry's length, and of
+ *                 skipped entries, are +0.0. 16-byte aligned.
+ *   state_out, state_scales_out
+ *                 receive the state after the first num_accepted_tokens tokens in every slot that
+ *                 an entry names, in the pool's type; other slots are not touched. They may be
+ *                 state_pool and state_scales (in place); any other overlap is undefined.
+ *
+ * The arithmetic is fp32; the state is rounded once, when it is committed. RGDR_MXI8 commits
+ * choose for each block of 32 columns the smallest power of two with which its largest value
+ * fits +-127, and round to nearest even; a block that holds a NaN, an infinity or a magnitude
+ * above 127 * 2^121 (the last that 8 bits and fp32 both hold) becomes NaN, with byte 255.
+ * Inputs of valid tokens are taken to be finite: outputs of other tokens of the same entry may
+ * see a NaN or an infinity among them. Padded tokens and skipped entries are never read.
+ * Errors: RGDR_ERR_NULL; RGDR_ERR_SHAPE (sizes, negative strides, overlapping out rows, no
+ * slot indices with N_slots < B); RGDR_ERR_UNSUPPORTED (D_k, D_v); RGDR_ERR_DTYPE
+ * (state_dtype); RGDR_ERR_ALIGN; RGDR_ERR_HIP.
+ */
+rgdr_status la_decode(const void *query, const la_strides *query_strides, const void *key,
+                      const la_strides *key_strides, const void *value,
+                      const la_strides *value_strides, const float *g,
+                      const la_strides *g_strides, const void *state_pool,
+                      const uint8_t *state_scales, rgdr_dtype state_dtype,
+                      const int32_t *actual_seq_lengths, const int32_t *ssm_state_indices,
+                      const int32_t *num_accepted_tokens, float scale, int32_t B, int32_t H_q,
+                      int32_t H_v, int32_t T, int32_t D_k, int32_t D_v, int32_t N_slots,
+                      void *out, const la_strides *out_strides, void *state_out,
+                      uint8_t *state_scales_out, hipStream_t stream);
+
+/*
+ * la_prefill_workspace_size -- the workspace with which la_prefill runs a call of these sizes on
+ * the current device in parallel over the tokens: *bytes = 0 when it needs none.
+ * Errors: RGDR_ERR_NULL (bytes NULL), RGDR_ERR_SHAPE, RGDR_ERR_UNSUPPORTED as la_prefill;
+ * RGDR_ERR_HIP if the device cannot be queried.
+ */
+rgdr_status la_prefill_workspace_size(int32_t B, int32_t H_v, int32_t T, int32_t D_k,
+                                      int32_t D_v, size_t *bytes);
+
+/*
+ * la_prefill -- la_decode over whole prompts: the same arguments, results and errors, with
+ * 1 <= T <= 65536. The state stays in fp32 across the tokens and is rounded once, when it is
+ * committed.
+ *   workspace        device memory, 256-byte aligned, owned by the caller, written before it is
+ *                    read; used until the call completes on `stream`, so calls that share one
+ *                    must be ordered. With NULL, or fewer bytes than
+ *                    la_prefill_workspace_size says, each entry's tokens are worked through in
+ *                    order by one workgroup for each head and up to 128 columns; with it, calls
+ *                    of few entries work on parts of a prompt at once. Both hold the same
+ *                    precision, and round differently.
+ *   workspace_bytes  its size.
+ */
+rgdr_status la_prefill(const void *query, const la_strides *query_strides, const void *key,
+                       const la_strides *key_strides, const void *value,
+                       const la_strides *value_strides, const float *g,
+                       const la_strides *g_strides, const void *state_pool,
+                       const uint8_t *state_scales, rgdr_dtype state_dtype,
+                       const int32_t *actual_seq_lengths, const int32_t *ssm_state_indices,
+                       const int32_t *num_accepted_tokens, float scale, int32_t B, int32_t H_q,
+                       int32_t H_v, int32_t T, int32_t D_k, int32_t D_v, int32_t N_slots,
+                       void *out, const la_strides *out_strides, void *state_out,
+                       uint8_t *state_scales_out, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * la_state_quantize -- states of a pool into a pool that holds them in 8 bits (RGDR_MXI8), as
+ * la_decode's commits round them. For each entry i < n, slot dst_slots[i] of (codes, scales)
+ * receives slot src_slots[i] of `state`.
+ *
+ *   state      [N_src, H_v, D_k, D_v] of state_dtype (RGDR_F32 or RGDR_BF16), 16-byte aligned.
+ *   src_slots, dst_slots   int32 [n], or NULL: entry i has slot i (needs n slots). A source
+ *              outside [0, N_src) counts as a zero state; an entry whose destination is outside
+ *              [0, N_dst) is skipped. Destinations must be distinct; sources need not be.
+ *   codes      int8 [N_dst, H_v, D_k, D_v], scales uint8 [N_dst, H_v, D_k, D_v / 32]; 16-byte
+ *              aligned; slots that no entry names are not touched.
+ *   n, H_v, D_k, D_v   n >= 0 (0: nothing is read or launched); H_v, D_k >= 1; D_v a multiple
+ *              of 32.
+ * Values below 2^-127 in magnitude are rounded to multiples of 2^-127.
+ * Errors: RGDR_ERR_NULL, RGDR_ERR_SHAPE, RGDR_ERR_UNSUPPORTED (D_v), RGDR_ERR_DTYPE,
+ * RGDR_ERR_ALIGN, RGDR_ERR_HIP.
+ */
+rgdr_status la_state_quantize(const void *state, rgdr_dtype state_dtype, int32_t N_src,
+                              const int32_t *src_slots, void *codes, uint8_t *scales,
+                              int32_t N_dst, const int32_t *dst_slots, int32_t n, int32_t H_v,
+                              int32_t D_k, int32_t D_v, hipStream_t stream);
+
+/*
+ * la_state_dequantize -- the way back: slot dst_slots[i] of `state` (RGDR_F32 or RGDR_BF16)
+ * receives slot src_slots[i] of (codes, scales). Both types hold every 8-bit value exactly
+ * (bf16 down to 2^-133). Arguments, skipped entries and errors as la_state_quantize.
+ */
+rgdr_status la_state_dequantize(const void *codes, const uint8_t *scales, int32_t N_src,
+                                const int32_t *src_slots, void *state, rgdr_dtype state_dtype,
+                                int32_t N_dst, const int32_t *dst_slots, int32_t n, int32_t H_v,
+                                int32_t D_k, int32_t D_v, hipStream_t stream);
+
+/* Option bits of la_norm_gate. */
+enum { LA_GATE_SIGMOID = 1u /* the gate's function is sigmoid, not silu */ };
+
+/*
+ * la_norm_gate -- the norm and gate behind the attention. For every row x[b,h,t,:] of D values:
+ *     y = weight * x / sqrt(mean(x^2) + eps) * silu(gate[b,t,h,:])
+ * (without a gate: the norm alone), in fp32, rounded once.
+ *
+ *   x          [B, H, T, D] of dtype (RGDR_F32, RGDR_F16 or RGDR_BF16) with x_strides (NULL:
+ *              contiguous), the layout of la_decode's and rgdr_decode's out.
+ *   gate       as x with gate_strides, or NULL. NULL strides: contiguous [B, T, H, D].
+ *   weight     fp32 [D] for all heads (weight_h_stride 0), or one for each head at that element
+ *              stride. 16-byte aligned, weight_h_stride a multiple of 4.
+ *   actual_seq_lengths  int32 [B] or NULL: rows of tokens past an entry's length are written as
+ *              +0.0 and not read.
+ *   eps        >= 0.
+ *   flags      0 or LA_GATE_SIGMOID.
+ *   B, H, T, D sizes >= 0 (a zero: nothing is read or launched); D a multiple of 8 up to 8192.
+ *   out        as x with out_strides; NULL strides: contiguous [B, T, H, D]. It may be x's or
+ *              the gate's buffer if it has its strides too; any other overlap is undefined.
+ * Rows start at multiples of 8 elements, bases are 16-byte aligned.
+ * Errors: RGDR_ERR_NULL, RGDR_ERR_SHAPE (sizes, strides, overlapping out rows, eps),
+ * RGDR_ERR_UNSUPPORTED (D, an unknown option bit), RGDR_ERR_DTYPE, RGDR_ERR_ALIGN,
+ * RGDR_ERR_HIP.
+ */
+rgdr_status la_norm_gate(const void *x, const la_strides *x_strides, const void *gate,
+                         const la_strides *gate_strides, const float *weight,
+                         int64_t weight_h_stride, rgdr_dtype dtype,
+                         const int32_t *actual_seq_lengths, float eps, uint32_t flags, int32_t B,
+                         int32_t H, int32_t T, int32_t D, void *out,
+                         const la_strides *out_strides, hipStream_t stream);
 
 /*
  * rgdr_validate_host -- checks the index arrays of one rgdr_decode call, given as HOST
