@@ -71,6 +71,8 @@ struct LaArgs {
     int B, Hq, Hv, T, Dv, N_slots, group;
 };
 
+constexpr long long kMaxTokenStride = 1 << 24;  // elements from one token's row to the next's
+
 struct LaEntry {
     int L, n, slot;
     bool state;  // the slot is in range: its state is read and committed

@@ -143,6 +143,9 @@ rgdr_status la_check(LaArgs &a, int max_t, const void *query, const la_strides *
         !la_extent_ok(a.sv, B, H_v, T, D_v) || !la_extent_ok(a.sg, B, H_v, T, 1) ||
         !la_rows_distinct(a.so, B, H_v, T, D_v))
         return RGDR_ERR_SHAPE;
+    // offsets within a chunk of tokens are counted in 32 bits
+    if (T > 1 && (a.sq.t > kMaxTokenStride || a.sk.t > kMaxTokenStride || a.sv.t > kMaxTokenStride))
+        return RGDR_ERR_SHAPE;
     if (!la_strides_aligned(a.sq, B, H_q, T) || !la_strides_aligned(a.sk, B, H_q, T) ||
         !la_strides_aligned(a.sv, B, H_v, T) || !la_strides_aligned(a.so, B, H_v, T))
         return RGDR_ERR_ALIGN;
@@ -152,6 +155,7 @@ rgdr_status la_check(LaArgs &a, int max_t, const void *query, const la_strides *
     if (mx && (!aligned(state_scales, 16) || !aligned(state_scales_out, 16))) return RGDR_ERR_ALIGN;
     if ((lens && !aligned(lens, 4)) || (idx && !aligned(idx, 4)) || (nacc && !aligned(nacc, 4)))
         return RGDR_ERR_ALIGN;
+    if (T == 1) a.sq.t = a.sk.t = a.sv.t = a.sg.t = a.so.t = 0;
     a.q = static_cast<const uint16_t *>(query);
     a.k = static_cast<const uint16_t *>(key);
     a.v = static_cast<const uint16_t *>(value);

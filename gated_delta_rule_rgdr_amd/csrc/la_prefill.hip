@@ -1,8 +1,572 @@
 // la_prefill.hip -- linear attention with a decay for each head, over whole prompts.
+//
+// For tokens 0..C-1 of a chunk with the incoming state S, G_t the running sum of the log decays
+// and G the chunk's whole sum:
+//     o_t = scale e^{G_t} S^T q_t + sum_{s <= t} scale e^{G_t - G_s} (q_t . k_s) v_s
+//     S'  = e^G S + sum_s k_s (e^{G - G_s} v_s)^T
+// which is the recurrence, regrouped into four dense products for the matrix cores. Exponents are
+// differences of sums held in fp64, so a chunk may decay by any amount.
+//
+// Precision: q, k and v are bf16 and enter the products as they are. What is computed enters as a
+// sum of bf16 numbers: the state and the scores as two (2^-16 of each, far below the output's
+// bf16 rounding), the scaled v of the state's update as three (2^-24: the state is kept in fp32
+// over the whole prompt, so its update is not rounded further).
 #include "la_common.h"
 
 namespace rgdr {
+
 constexpr int kLaMaxPrompt = 65536;
+constexpr int kChunk = 64;    // tokens
+constexpr int kCols = 128;    // columns of one workgroup: 32 for each of its 4 waves
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+struct LaPlan {
+    int state_dtype, tiles, seg_len, nseg;
+    float *seg_state;  // [nseg][B*H_v][D_v/32][D_k/32][4][64][4]: accumulator layout
+    float *seg_decay;  // [nseg][B*H_v]
+};
+
+enum { kWhole = 0, kSegState = 1, kSegOut = 2 };
+
+// 16-byte pieces of LDS rows are permuted within each row, so that both kinds of reads spread over
+// the banks: 16 lanes at the same piece of 16 rows, and 4 rows times 4 neighbouring pieces.
+template <int PIECES>
+__device__ __forceinline__ int swz(int row) {
+    if constexpr (PIECES == 8)
+        return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    else
+        return ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
+template <int PIECES>
+__device__ __forceinline__ int lds_at(int row, int piece) {
+    return row * (PIECES * 16) + ((piece ^ swz<PIECES>(row)) << 4);
+}
+
+__device__ __forceinline__ bf16x8 lds_read(const char *p) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
+}
+
+// Eight rows (tokens) of one column for each lane: lane l gets column map32(l % 32) of its
+// 32-column group, rows 8 * (l / 32) .. + 7 of the 16 at `row0`. The hardware transposes 4 rows
+// by 16 columns for each 16 lanes, which read them as 4-column pieces; lane l's piece is
+// chosen so that consecutive accumulator registers hold consecutive rows (see map32).
+template <int PIECES>
+__device__ __forceinline__ bf16x8 lds_read_tr(char *m, int row0, int group, int lane) {
+    const int n = lane & 15, row = row0 + ((lane >> 5) << 3) + (n >> 2);
+    const int piece = group * 4 + ((lane >> 4) & 1) * 2 + (n & 1), half = (n & 2) << 2;
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(m + lds_at<PIECES>(row, piece) + half));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(m + lds_at<PIECES>(row + 4, piece) + half));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The column (or row) that position n of a 32-wide matrix operand read by lds_read_tr stands for:
+// groups of four in the order 0, 2, 1, 3. An accumulator lane holds positions 8 m + 4 (l / 32) + 0..3
+// in registers 4 m + 0..3, which are then the 8 consecutive rows 16 (m / 2) + 8 (l / 32) + 0..7
+// in registers 8 (m / 2) + 0..7: what a matrix operand's lane holds, and 16 bytes of output.
+__device__ __forceinline__ int map32(int n) {
+    return (n & 16) | ((n & 4) << 1) | ((n & 8) >> 1) | (n & 3);
+}
+
+// x = hi + lo (+ lo2) in bf16, for eight values.
+__device__ __forceinline__ void split2(const float (&x)[8], u32x4 &hi, u32x4 &lo, float (&rest)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        rest[2 * i] = x[2 * i] - bf16_lo(hi[i]);
+        rest[2 * i + 1] = x[2 * i + 1] - bf16_hi(hi[i]);
+        lo[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
+    }
+}
+
+__device__ __forceinline__ f32x16 mfma(u32x4 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b, c, 0, 0, 0);
+}
+
+// One wave's 32 columns of a state, D_k rows: register r = 8 kb + e of tile `it` is row
+// 32 it + 16 kb + 8 (lane / 32) + e, column map32(lane % 32).
+// `base`: the element of the wave's first column in the state's first row.
+template <int DK, int ST>
+__device__ __forceinline__ void load_state(f32x16 (&S)[DK / 32], const void *pool,
+                                           const uint8_t *scales, long long base, int Dv, int lane) {
+    constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
+    const char *p = static_cast<const char *>(pool) + base * kSize;
+    const uint8_t *sc = scales + base / kMxBlock;
+    const uint32_t at = (uint32_t)((lane >> 5) * 8 * Dv + map32(lane & 31)) * kSize;
+    const uint32_t sat = (uint32_t)((lane >> 5) * 8 * (Dv / kMxBlock));
+#pragma unroll
+    for (int it = 0; it < DK / 32; ++it) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = it * 32 + (r >> 3) * 16 + (r & 7);
+            const char *x = p + (uint32_t)(row * Dv) * kSize;
+            if constexpr (ST == RGDR_F32)
+                S[it][r] = *reinterpret_cast<const float *>(x + at);
+            else if constexpr (ST == RGDR_BF16)
+                S[it][r] = bf16_to_f32(*reinterpret_cast<const uint16_t *>(x + at));
+            else
+                S[it][r] = static_cast<float>(*reinterpret_cast<const int8_t *>(x + at)) *
+                           mx_scale((sc + row * (Dv / kMxBlock))[sat]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int DK, int ST>
+__device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *pool,
+                                            uint8_t *scales, long long base, int Dv, int lane) {
+    constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
+    char *p = static_cast<char *>(pool) + base * kSize;
+    uint8_t *sc = scales + base / kMxBlock;
+    asm volatile("" : "+v"(lane));  // the rows' addresses are formed here, not kept from the prompt's start
+    const uint32_t at = (uint32_t)((lane >> 5) * 8 * Dv + map32(lane & 31)) * kSize;
+    const uint32_t sat = (uint32_t)((lane >> 5) * 8 * (Dv / kMxBlock));
+#pragma unroll
+    for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = it * 32 + (r >> 3) * 16 + (r & 7);
+            char *x = p + (uint32_t)(row * Dv) * kSize;
+            const float y = S[it][r];
+            if constexpr (ST == RGDR_F32) {
+                *reinterpret_cast<float *>(x + at) = y;
+            } else if constexpr (ST == RGDR_BF16) {
+                *reinterpret_cast<uint16_t *>(x + at) = f32_to_bf16(y);
+            } else {
+                uint32_t top = __float_as_uint(y) & 0x7FFFFFFFu;  // as whole numbers NaN is the largest
+#pragma unroll
+                for (int m = 16; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+                const uint32_t eb = mx_exponent(top);
+                *reinterpret_cast<uint8_t *>(x + at) = (uint8_t)mx_code_bits(y, mx_inverse(eb));
+                if ((lane & 31) == 0) (sc + row * (Dv / kMxBlock))[sat] = (uint8_t)eb;
+            }
+            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few rows at a time: registers
+        }
+}
+
+// A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
+// one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
+// chunk's q, k and v lie in LDS, and three waves compute a 32 x 32 tile of the scores each while
+// the fourth sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
+template <int DK, int MODE>
+__global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const LaArgs a, const LaPlan p) {
+    constexpr int KP = DK / 8;                 // 16-byte pieces of a q or k row
+    constexpr int NR = kChunk * KP / 256;      // of them in each thread's hands
+    constexpr int NV = kChunk * 16 / 256;
+    constexpr bool kOut = MODE != kSegState;
+    __shared__ __align__(256) char lq[kOut ? kChunk * DK * 2 : 256];
+    __shared__ __align__(256) char lk[kChunk * DK * 2];
+    __shared__ __align__(256) char lv[kChunk * kCols * 2];
+    __shared__ __align__(256) char lp[kOut ? 2 : 1][kOut ? kChunk * kChunk * 2 : 256];
+    // Of each token of this chunk and the next: the log2 decay sum in two floats, what a later
+    // state keeps of it, and what it keeps of the incoming state (with the scale).
+    __shared__ __align__(16) float g_hi[2][kChunk], g_lo[2][kChunk], keep[2][kChunk], carry[2][kChunk];
+    __shared__ float whole[2];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int item = xcd_item(blockIdx.x, gridDim.x);
+    const int tile = item % p.tiles;
+    item /= p.tiles;
+    const int h = item % a.Hv;
+    item /= a.Hv;
+    const int seg = MODE == kWhole ? 0 : item % p.nseg;
+    const int b = MODE == kWhole ? item : item / p.nseg;
+    const LaEntry en = la_entry(a, b);
+    const int t_begin = MODE == kWhole ? 0 : seg * p.seg_len;
+    const int t_stop = MODE == kWhole ? a.T : min(a.T, t_begin + p.seg_len);
+    const int t_end = min(en.L, t_stop);
+    if (MODE == kSegState && t_begin + p.seg_len >= en.L) return;  // no later segment needs it
+    const int hq = h / a.group, bh = b * a.Hv + h;
+    const int col0 = tile * kCols + wave * 32;
+    const bool mine = col0 < a.Dv;  // this wave has columns
+    const int vpieces = min(16, (a.Dv - tile * kCols) / 8);
+
+    const uint16_t *gq = a.q + b * a.sq.b + hq * a.sq.h;
+    const uint16_t *gk = a.k + b * a.sk.b + hq * a.sk.h;
+    const uint16_t *gv = a.v + b * a.sv.b + h * a.sv.h + tile * kCols;
+    const float *gg = a.g + b * a.sg.b + h * a.sg.h;
+    uint16_t *go = a.out + b * a.so.b + h * a.so.h + col0;
+
+    // rows of tokens past the entry's length
+    if (kOut) {
+        const int from = max(t_begin, t_end);
+        for (int j = tid; j < (t_stop - from) * vpieces; j += 256)
+            *reinterpret_cast<u32x4 *>(a.out + b * a.so.b + h * a.so.h + tile * kCols +
+                                       (from + j / vpieces) * a.so.t + (j % vpieces) * 8) = u32x4{0, 0, 0, 0};
+    }
+    if (!en.state) return;
+    if (t_begin >= t_end && !(kOut && t_begin == 0)) return;
+
+    f32x16 S[DK / 32];
+    const long long base = ((long long)__builtin_amdgcn_readfirstlane(en.slot) * a.Hv + h) * DK * a.Dv + col0;
+    float *const ws = MODE == kWhole ? nullptr
+                                     : p.seg_state + (((long long)seg * a.B * a.Hv + bh) * (a.Dv / 32) +
+                                                      tile * 4 + wave) * (DK * 32);
+    if (mine) {
+        if (MODE == kWhole) {
+            if (p.state_dtype == RGDR_F32)
+                load_state<DK, RGDR_F32>(S, a.pool, a.scales, base, a.Dv, lane);
+            else if (p.state_dtype == RGDR_BF16)
+                load_state<DK, RGDR_BF16>(S, a.pool, a.scales, base, a.Dv, lane);
+            else
+                load_state<DK, RGDR_MXI8>(S, a.pool, a.scales, base, a.Dv, lane);
+        } else if (MODE == kSegOut) {
+#pragma unroll
+            for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const f32x4 x = *reinterpret_cast<const f32x4 *>(ws + ((it * 4 + m) * 64 + lane) * 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[it][m * 4 + e] = x[e];
+                }
+        } else {
+#pragma unroll
+            for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S[it][r] = 0.f;
+        }
+    }
+    auto commit = [&]() {
+        if (!mine) return;
+        if (p.state_dtype == RGDR_F32)
+            store_state<DK, RGDR_F32>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+        else if (p.state_dtype == RGDR_BF16)
+            store_state<DK, RGDR_BF16>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+        else
+            store_state<DK, RGDR_MXI8>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+    };
+    if (kOut && t_begin == 0 && en.n == 0) commit();
+    if (t_begin >= t_end) return;
+
+    // A chunk ends after 64 tokens, at the accepted count (whose state is committed) or at the end.
+    auto chunk_end = [&](int t) { return min(min(t + kChunk, t_end), kOut && t < en.n ? en.n : t_end); };
+
+    u32x4 rq[kOut ? NR : 1], rk[NR], rv[NV];
+    // Rows past the chunk repeat its last row: they are not padding's (never read), and their
+    // weights are zero.
+    auto fetch = [&](int t0, int n, int tid) {
+        const char *q = reinterpret_cast<const char *>(gq + t0 * a.sq.t);
+        const char *k = reinterpret_cast<const char *>(gk + t0 * a.sk.t);
+        const char *v = reinterpret_cast<const char *>(gv + t0 * a.sv.t);
+        const uint32_t qt = (uint32_t)a.sq.t * 2, kt = (uint32_t)a.sk.t * 2, vt = (uint32_t)a.sv.t * 2;
+#pragma unroll
+        for (int m = 0; m < NR; ++m) {
+            const uint32_t j = m * 256 + tid, t = min(j / KP, (uint32_t)n - 1), c = j % KP * 16;
+            if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (t * qt + c));
+            rk[m] = *reinterpret_cast<const u32x4 *>(k + (t * kt + c));
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const uint32_t j = m * 256 + tid, t = min(j / 16, (uint32_t)n - 1);
+            rv[m] = *reinterpret_cast<const u32x4 *>(v + (t * vt + min(j % 16, (uint32_t)vpieces - 1) * 16));
+        }
+    };
+    auto stage = [&](int tid) {
+#pragma unroll
+        for (int m = 0; m < NR; ++m) {
+            const int j = m * 256 + tid, at = lds_at<KP>(j / KP, j % KP);
+            if (kOut) *reinterpret_cast<u32x4 *>(lq + at) = rq[m];
+            *reinterpret_cast<u32x4 *>(lk + at) = rk[m];
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int j = m * 256 + tid;
+            *reinterpret_cast<u32x4 *>(lv + lds_at<16>(j / 16, j % 16)) = rv[m];
+        }
+    };
+    auto fetch_g = [&](int t0, int n) { return gg[(long long)(t0 + min(lane, n - 1)) * a.sg.t]; };
+    // One lane for each token: decay sums of a chunk of n tokens, into buffer `to`.
+    auto decays = [&](float x, int n, int to) {
+        constexpr double kLog2e = 1.4426950408889634;
+        double G = lane < n ? (double)la_log_decay(x) * kLog2e : 0.0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const double y = __shfl_up(G, m);
+            if (lane >= m) G += y;
+        }
+        const double end = __shfl(G, 63);
+        const float hi = (float)G;
+        g_hi[to][lane] = hi;
+        g_lo[to][lane] = (float)(G - (double)hi);
+        keep[to][lane] = lane < n ? __builtin_amdgcn_exp2f((float)(end - G)) : 0.f;
+        carry[to][lane] = __builtin_amdgcn_exp2f(hi) * a.scale;
+        if (lane == 0) whole[to] = __builtin_amdgcn_exp2f((float)end);
+    };
+
+    int t0 = t_begin, t1 = chunk_end(t0), buf = 0;
+    float g_next = 0.f, seg_keep = 1.f;
+    fetch(t0, t1 - t0, tid);
+    if (wave == 3) {
+        decays(fetch_g(t0, t1 - t0), t1 - t0, 0);
+        if (t1 < t_end) g_next = fetch_g(t1, chunk_end(t1) - t1);
+    }
+    while (true) {
+        const int n = t1 - t0;
+        const int t2 = t1 < t_end ? chunk_end(t1) : t1;
+        // The lane's number, as if new in each round: the many addresses made of it are cheap to
+        // form again, and would not fit the registers if they were kept over the loop.
+        int now = tid;
+        asm volatile("" : "+v"(now));
+        const int lane = now & 63, col = lane & 31, hf = lane >> 5;
+        stage(now);
+        __syncthreads();
+        if (t2 > t1) fetch(t1, t2 - t1, now);
+        if (wave == 3) {
+            if (t2 > t1) {
+                decays(g_next, t2 - t1, buf ^ 1);
+                if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
+            }
+        } else if (kOut) {
+            // scores of tokens t (lanes) and s (registers): tiles (0,0), (1,0) and (1,1)
+            const int tt = wave > 0, st = wave > 1;
+            f32x16 x = {};
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c)
+                x = mfma(__builtin_bit_cast(u32x4, lds_read(lk + lds_at<KP>(st * 32 + col, c * 2 + hf))),
+                         lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf)), x);
+            const int t = tt * 32 + col;
+            const float th = g_hi[buf][t], tl = g_lo[buf][t];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int s = st * 32 + m * 8 + hf * 4;
+                const f32x4 sh = *reinterpret_cast<const f32x4 *>(&g_hi[buf][s]);
+                const f32x4 sl = *reinterpret_cast<const f32x4 *>(&g_lo[buf][s]);
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float w = __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) * a.scale;
+                    y[e] = s + e <= t && t < n ? x[m * 4 + e] * w : 0.f;
+                }
+                u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+                u32x2 lo = {pack_bf16x2(y[0] - bf16_lo(hi[0]), y[1] - bf16_hi(hi[0])),
+                            pack_bf16x2(y[2] - bf16_lo(hi[1]), y[3] - bf16_hi(hi[1]))};
+                const int at = lds_at<8>(t, st * 4 + m) + hf * 8;
+                *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
+                *reinterpret_cast<u32x2 *>(lp[kOut ? 1 : 0] + at) = lo;
+            }
+        }
+        bf16x8 vf[4];
+        f32x16 o[2] = {};
+        if (mine) {
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16>(lv, kb * 16, wave, lane);
+            if (kOut) {
+#pragma unroll
+                for (int c = 0; c < DK / 16; ++c) {
+                    float x[8], rest[8];
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
+                    split2(x, hi, lo, rest);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) {
+                        const bf16x8 q = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
+                        o[tt] = mfma(hi, q, o[tt]);
+                        o[tt] = mfma(lo, q, o[tt]);
+                    }
+                }
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) {
+                    const float c = carry[buf][tt * 32 + col];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[tt][r] *= c;
+                }
+            }
+        }
+        if (kOut) __syncthreads();
+        if (mine) {
+            if (kOut) {
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int kb = 0; kb < 2 + 2 * tt; ++kb)
+#pragma unroll
+                        for (int pl = 0; pl < 2; ++pl)
+                            o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]),
+                                         lds_read(lp[kOut ? pl : 0] + lds_at<8>(tt * 32 + col, kb * 2 + hf)), o[tt]);
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+                    if (tt * 32 + col < n) {
+                        uint16_t *row = go + (t0 + tt * 32 + col) * a.so.t + hf * 8;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            u32x4 y;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = pack_bf16x2(o[tt][m * 8 + 2 * e], o[tt][m * 8 + 2 * e + 1]);
+                            *reinterpret_cast<u32x4 *>(row + m * 16) = y;
+                        }
+                    }
+            }
+            if (t1 < t_end || MODE == kSegState || t1 == en.n) {
+                const float d = whole[buf];
+                if (MODE == kSegState) seg_keep *= d;
+#pragma unroll
+                for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) S[it][r] *= d;
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb) {
+                    float x[8], r1[8], r2[8];
+                    u32x4 hi, lo, lo2;
+                    const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
+                    const float *w = &keep[buf][kb * 16 + hf * 8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = bf16_lo(v[e]) * w[2 * e];
+                        x[2 * e + 1] = bf16_hi(v[e]) * w[2 * e + 1];
+                    }
+                    split2(x, hi, lo, r1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        r2[2 * e] = r1[2 * e] - bf16_lo(lo[e]);
+                        r2[2 * e + 1] = r1[2 * e + 1] - bf16_hi(lo[e]);
+                        lo2[e] = pack_bf16x2(r2[2 * e], r2[2 * e + 1]);
+                    }
+#pragma unroll
+                    for (int it = 0; it < DK / 32; ++it) {
+                        const u32x4 k = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, kb * 16, it, lane));
+                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, lo2), S[it]);
+                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, lo), S[it]);
+                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, hi), S[it]);
+                    }
+                }
+            }
+        }
+        if (kOut && t1 == en.n) commit();
+        if (t2 == t1) break;
+        __syncthreads();
+        t0 = t1;
+        t1 = t2;
+        buf ^= 1;
+    }
+    if (MODE == kSegState && mine) {
+#pragma unroll
+        for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                *reinterpret_cast<f32x4 *>(ws + ((it * 4 + m) * 64 + lane) * 4) =
+                    f32x4{S[it][m * 4], S[it][m * 4 + 1], S[it][m * 4 + 2], S[it][m * 4 + 3]};
+        if (tile == 0 && tid == 0) p.seg_decay[(long long)seg * a.B * a.Hv + bh] = seg_keep;
+    }
+}
+
+// Segments' own contributions into their incoming states, in place: one thread for four rows of a
+// column. The states in the pool are read here and committed by the next kernel, since a slot may
+// be updated in place.
+template <int ST>
+__global__ __launch_bounds__(256) void la_scan_kernel(const LaArgs a, const LaPlan p, int DK) {
+    const int per = a.Dv * DK / 4;  // threads for each (entry, head)
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int bh = (int)(id / per), x = (int)(id % per);
+    if (bh >= a.B * a.Hv) return;
+    const int b = bh / a.Hv, h = bh % a.Hv;
+    const LaEntry en = la_entry(a, b);
+    if (!en.state) return;
+    const int lane = x & 63, m = (x >> 6) & 3, it = (x >> 8) % (DK / 32), cb = (x >> 8) / (DK / 32);
+    const int row = it * 32 + (m >> 1) * 16 + (lane >> 5) * 8 + (m & 1) * 4;
+    const long long e = ((long long)en.slot * a.Hv + h) * DK * a.Dv + (long long)row * a.Dv + cb * 32 +
+                        map32(lane & 31);
+    f32x4 S;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long at = e + (long long)i * a.Dv;
+        if constexpr (ST == RGDR_F32)
+            S[i] = static_cast<const float *>(a.pool)[at];
+        else if constexpr (ST == RGDR_BF16)
+            S[i] = bf16_to_f32(static_cast<const uint16_t *>(a.pool)[at]);
+        else
+            S[i] = static_cast<float>(static_cast<const int8_t *>(a.pool)[at]) * mx_scale(a.scales[at / kMxBlock]);
+    }
+    const int last = max(0, (en.L + p.seg_len - 1) / p.seg_len - 1);
+    const long long step = (long long)a.B * a.Hv * per;
+    f32x4 *ws = reinterpret_cast<f32x4 *>(p.seg_state) + (long long)bh * per + x;
+    const float *decay = p.seg_decay + bh;
+    constexpr int U = 8;  // segments whose contributions are in flight together
+    for (int s0 = 0; s0 < last; s0 += U) {
+        f32x4 own[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = min(s0 + u, last - 1);
+            own[u] = ws[s * step];
+            d[u] = decay[(long long)s * a.B * a.Hv];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u < last) {
+                ws[(s0 + u) * step] = S;
+                S = S * d[u] + own[u];
+            }
+    }
+    ws[last * step] = S;
+}
+
+static int cu_count() {
+    static int known[64];  // zero: not asked yet; every writer writes the same number
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED))) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+    return n;
+}
+
+// How many segments: as many as fill the device's resident workgroups (two on a compute unit, one
+// with D_k = 256), of at least two chunks. Two segments would do one and a half times the work in
+// half the length each, plus two launches, so a call is cut into three or more, or not at all.
+static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, size_t &bytes) {
+    bytes = 0;
+    p.nseg = 1;
+    p.seg_len = T;
+    const int cus = cu_count();
+    if (cus <= 0) return false;
+    const long long tiles = (D_v + kCols - 1) / kCols;
+    const long long items = (long long)B * H_v * tiles;
+    const long long slots = (long long)cus * (D_k == 256 ? 1 : 2);
+    const int chunks = (T + kChunk - 1) / kChunk;
+    if (items <= 0) return true;
+    const long long most = slots / items < chunks / 2 ? slots / items : chunks / 2;
+    if (most < 3) return true;
+    const int seg_chunks = (int)((chunks + most - 1) / most);
+    const int nseg = (chunks + seg_chunks - 1) / seg_chunks;
+    if (nseg < 3) return true;
+    p.nseg = nseg;
+    p.seg_len = seg_chunks * kChunk;
+    const size_t bh = (size_t)B * H_v;
+    bytes = (size_t)nseg * bh * (size_t)D_k * D_v * 4 + ((size_t)nseg * bh * 4 + 255) / 256 * 256;
+    return true;
+}
+
+template <int DK>
+static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream) {
+    p.tiles = (a.Dv + kCols - 1) / kCols;
+    const unsigned items = (unsigned)((long long)a.B * a.Hv * p.tiles);
+    const dim3 block(256);
+    if (p.nseg == 1) {
+        hipLaunchKernelGGL((la_chunk_kernel<DK, kWhole>), dim3(items), block, 0, stream, a, p);
+        return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+    }
+    const unsigned scan = (unsigned)(((long long)a.B * a.Hv * (a.Dv * DK / 4) + 255) / 256);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState>), dim3(items * p.nseg), block, 0, stream, a, p);
+    if (p.state_dtype == RGDR_F32)
+        hipLaunchKernelGGL(la_scan_kernel<RGDR_F32>, dim3(scan), block, 0, stream, a, p, DK);
+    else if (p.state_dtype == RGDR_BF16)
+        hipLaunchKernelGGL(la_scan_kernel<RGDR_BF16>, dim3(scan), block, 0, stream, a, p, DK);
+    else
+        hipLaunchKernelGGL(la_scan_kernel<RGDR_MXI8>, dim3(scan), block, 0, stream, a, p, DK);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut>), dim3(items * p.nseg), block, 0, stream, a, p);
+    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+}
+
 }  // namespace rgdr
 
 extern "C" rgdr_status la_prefill_workspace_size(int32_t B, int32_t H_v, int32_t T, int32_t D_k,
@@ -11,7 +575,9 @@ extern "C" rgdr_status la_prefill_workspace_size(int32_t B, int32_t H_v, int32_t
     if (!bytes) return RGDR_ERR_NULL;
     if (const rgdr_status st = la_check_sizes(kLaMaxPrompt, B, H_v, T, D_k, D_v)) return st;
     *bytes = 0;
-    return RGDR_OK;
+    if (B == 0) return RGDR_OK;
+    LaPlan p;
+    return plan_segments(B, H_v, T, D_k, D_v, p, *bytes) ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 extern "C" rgdr_status la_prefill(const void *query, const la_strides *query_strides,
@@ -36,6 +602,19 @@ extern "C" rgdr_status la_prefill(const void *query, const la_strides *query_str
         return st;
     if (B == 0) return RGDR_OK;
     if (workspace && !aligned(workspace, 256)) return RGDR_ERR_ALIGN;
-    (void)workspace_bytes;
-    return la_launch_recurrent(a, state_dtype, D_k, stream);
+    LaPlan p = {};
+    size_t need = 0;
+    if (!plan_segments(B, H_v, T, D_k, D_v, p, need)) return RGDR_ERR_HIP;
+    if (!workspace || workspace_bytes < need) {
+        p.nseg = 1;
+        p.seg_len = T;
+    }
+    p.state_dtype = state_dtype;
+    if (p.nseg > 1) {
+        p.seg_state = static_cast<float *>(workspace);
+        p.seg_decay = p.seg_state + (size_t)p.nseg * B * H_v * D_k * D_v;
+    }
+    if (D_k == 64) return launch_prefill<64>(a, p, stream);
+    if (D_k == 128) return launch_prefill<128>(a, p, stream);
+    return launch_prefill<256>(a, p, stream);
 }

@@ -52,6 +52,7 @@ BAD_ATTENTION = [
     (dict(vs=(1 << 20, 4, 128)), ALIGN),
     (dict(qs=(1 << 20, 1 << 10, -128)), SHAPE),
     (dict(gs=(-4, 4, 1)), SHAPE),
+    (dict(ks=(1 << 30, 128, (1 << 24) + 8)), SHAPE),
     (dict(os=(1 << 20, 1 << 10, 64)), SHAPE),   # out rows on top of each other
     (dict(os=(0, 1 << 10, 128)), SHAPE),
     (dict(os=(2048, 128, 256)), SHAPE),         # head 2 of token 0 is head 0 of token 1
