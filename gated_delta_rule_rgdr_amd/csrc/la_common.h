@@ -46,10 +46,15 @@ __device__ __forceinline__ uint32_t mx_pack4(uint32_t a, uint32_t b, uint32_t c,
     const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
     return lo | hi;
 }
-// Code i of a word of four.
+// Code i of a word of four (one instruction: the conversion selects the byte).
 __device__ __forceinline__ float mx_code(uint32_t w, int i) {
-    return static_cast<float>(static_cast<int32_t>(w << (24 - 8 * i)) >> 24);
+    return static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
 }
+// The larger magnitude, or NaN if either is (three-operand instruction: two values each).
+__device__ __forceinline__ float mx_larger(float top, float x) {
+    return __builtin_elementwise_maximum(top, __builtin_fabsf(x));
+}
+__device__ __forceinline__ uint32_t mx_top_bits(float top) { return __float_as_uint(top) & 0x7FFFFFFFu; }
 
 // ---- linear attention: arguments ------------------------------------------------------------
 
@@ -142,8 +147,5 @@ rgdr_status la_check(LaArgs &a, int max_t, const void *query, const la_strides *
                      int32_t N_slots, void *out, const la_strides *out_strides, void *state_out,
                      uint8_t *state_scales_out);
 rgdr_status la_check_sizes(int max_t, int32_t B, int32_t H_v, int32_t T, int32_t D_k, int32_t D_v);
-
-// Tokens in order, one workgroup for each (entry, head, 32 columns); any T.
-rgdr_status la_launch_recurrent(const LaArgs &a, int state_dtype, int D_k, hipStream_t stream);
 
 }  // namespace rgdr

@@ -1,108 +1,519 @@
 // la_decode.hip -- linear attention with a decay for each head, a few tokens at a time.
 //
-// Per (entry, value head) and valid token, on S (D_k x D_v, fp32 while the call works on it):
-//     S = exp(g) S + k v^T,     o = S^T (scale q).
-#include "la_common.h"
+// Per (entry, value head) and valid token, on S (D_k x D_v):  S = exp(g) S + k v^T,
+// o = S^T (scale q). With G_t the running sum of the log decays and S0 the stored state, that is
+//     o_t = S0^T (scale e^{G_t} q_t) + sum_{s <= t} scale e^{G_t - G_s} (q_t . k_s) v_s
+//     S_n = e^{G_n} S0 + sum_{s < n} (e^{G_n - G_s} k_s) v_s^T
+// so every state element is read once, multiplied by T query rows and T key rows, and written once,
+// with nothing carried from token to token. Bound: the state's bytes (2 T + 1 multiply-adds for
+// each of its elements, 2 to 8 bytes).
+#include "la_mfma.h"
 
 namespace rgdr {
 
-// Loads and stores of one state element at column c of a row, by 32 lanes (c = lane % 32).
+// How one lane holds a piece of a state row: 16 bytes of it.
 template <int ST>
-__device__ __forceinline__ float la_load1(const void *pool, const uint8_t *scales, long long e) {
-    if constexpr (ST == RGDR_F32)
-        return static_cast<const float *>(pool)[e];
-    else if constexpr (ST == RGDR_BF16)
-        return bf16_to_f32(static_cast<const uint16_t *>(pool)[e]);
-    else
-        return static_cast<float>(static_cast<const int8_t *>(pool)[e]) *
-               mx_scale(scales[e / kMxBlock]);
-}
+struct Piece {
+    static constexpr int N = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 8 : 16;  // columns
+    // Value c; of an 8-bit state its code.
+    static __device__ __forceinline__ float get(const u32x4 &w, int c) {
+        if constexpr (ST == RGDR_F32)
+            return __uint_as_float(w[c]);
+        else if constexpr (ST == RGDR_BF16)
+            return c & 1 ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2]);
+        else
+            return mx_code(w[c / 4], c % 4);
+    }
+};
+
+// Rounds a lane's piece of a row. Two neighbouring lanes hold an 8-bit block; every lane of the
+// wave calls this.
 template <int ST>
-__device__ __forceinline__ void la_store1(void *pool, uint8_t *scales, long long e, float x) {
+__device__ __forceinline__ u32x4 round_piece(const float (&x)[Piece<ST>::N], uint32_t &eb) {
+    u32x4 w;
     if constexpr (ST == RGDR_F32) {
-        static_cast<float *>(pool)[e] = x;
-    } else if constexpr (ST == RGDR_BF16) {
-        static_cast<uint16_t *>(pool)[e] = f32_to_bf16(x);
-    } else {
-        uint32_t top = __float_as_uint(x) & 0x7FFFFFFFu;  // as whole numbers NaN is the largest
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-        const uint32_t eb = mx_exponent(top);
-        static_cast<uint8_t *>(pool)[e] = (uint8_t)mx_code_bits(x, mx_inverse(eb));
-        if (e % kMxBlock == 0) scales[e / kMxBlock] = (uint8_t)eb;
+        for (int c = 0; c < 4; ++c) w[c] = __float_as_uint(x[c]);
+    } else if constexpr (ST == RGDR_BF16) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+    } else {
+        float most = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) most = mx_larger(most, x[c]);
+        uint32_t top = mx_top_bits(most);  // as whole numbers NaN is the largest
+        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false));  // lane ^ 1
+        eb = mx_exponent(top);
+        const float inv = mx_inverse(eb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            w[c] = mx_pack4(mx_code_bits(x[4 * c], inv), mx_code_bits(x[4 * c + 1], inv),
+                            mx_code_bits(x[4 * c + 2], inv), mx_code_bits(x[4 * c + 3], inv));
+    }
+    return w;
+}
+
+template <int ST, int DK, int TV>
+struct StepShape {
+    static constexpr int CPL = Piece<ST>::N;                       // columns of a lane
+    static constexpr int LPR = TV / CPL;                           // lanes across a row of the tile
+    static constexpr int NT = DK * LPR < 256 ? DK * LPR : 256;     // threads
+    static constexpr int RPP = NT / LPR;                           // rows in one pass of them
+    static constexpr int R = DK / RPP;                             // rows of a thread
+    static constexpr int NW = NT / 64;
+    static_assert(NT % 64 == 0 && NT >= DK && 64 % LPR == 0 && DK % RPP == 0, "tile shape");
+};
+
+// Sum over the lanes of the wave that hold the same columns, LPR apart; every lane gets it.
+template <int LPR>
+__device__ __forceinline__ float row_lanes_sum(float x) {
+#pragma unroll
+    for (int m = LPR; m < 64; m <<= 1) x += __shfl_xor(x, m);
+    return x;
+}
+
+// N bf16 values of a row, in fp32; p is aligned to their 2 N bytes or to 16.
+template <int N>
+__device__ __forceinline__ void load_bf16(float (&x)[N], const uint16_t *p) {
+    if constexpr (N == 4) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            x[2 * e] = bf16_lo(v[e]);
+            x[2 * e + 1] = bf16_hi(v[e]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + j * 8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[j * 8 + 2 * e] = bf16_lo(v[e]);
+                x[j * 8 + 2 * e + 1] = bf16_hi(v[e]);
+            }
+        }
     }
 }
 
-// The plainest form: thread (c, r) holds rows r, r + 8, ... of column c.
-template <int ST, int DK>
-__global__ __launch_bounds__(256) void la_recurrent_kernel(const LaArgs a, int tiles) {
-    constexpr int R = DK / 8;
-    __shared__ float ks[DK], qs[DK], red[8][32];
-    const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
-    const int h = bh % a.Hv, b = bh / a.Hv, hq = h / a.group;
-    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+// One token: one workgroup for each (entry, value head, TV columns). A lane holds 16 bytes of each
+// of its rows, so the state moves in whole lines. The operands' loads go out before the state's,
+// whose answers are waited for last.
+template <int ST, int DK, int TV>
+__global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles) {
+    using Sh = StepShape<ST, DK, TV>;
+    constexpr int CPL = Sh::CPL, LPR = Sh::LPR, R = Sh::R, NT = Sh::NT, NW = Sh::NW;
+    __shared__ f32x2_t qk[DK];
+    __shared__ float red[NW][TV];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int item = xcd_item(blockIdx.x, gridDim.x);
+    const int tile = item % tiles;
+    item /= tiles;
+    const int h = item % a.Hv, b = item / a.Hv, hq = h / a.group;
     const LaEntry en = la_entry(a, b);
-    const long long base = ((long long)en.slot * a.Hv + h) * DK * a.Dv + tile * 32 + c;
-    float S[R];
-    if (en.state)
-#pragma unroll
-        for (int m = 0; m < R; ++m)
-            S[m] = la_load1<ST>(a.pool, a.scales, base + (long long)(r + 8 * m) * a.Dv);
-    auto commit = [&]() {
-#pragma unroll
-        for (int m = 0; m < R; ++m)
-            la_store1<ST>(a.pool_out, a.scales_out, base + (long long)(r + 8 * m) * a.Dv, S[m]);
-    };
-    if (en.state && en.n == 0) commit();
-    const uint16_t *q = a.q + b * a.sq.b + hq * a.sq.h;
-    const uint16_t *k = a.k + b * a.sk.b + hq * a.sk.h;
-    const uint16_t *v = a.v + b * a.sv.b + h * a.sv.h + tile * 32 + c;
-    const float *g = a.g + b * a.sg.b + h * a.sg.h;
-    uint16_t *o = a.out + b * a.so.b + h * a.so.h + tile * 32 + c;
-    for (int t = 0; t < en.L; ++t) {
-        if (threadIdx.x < DK) {
-            ks[threadIdx.x] = bf16_to_f32(k[t * a.sk.t + threadIdx.x]);
-            qs[threadIdx.x] = bf16_to_f32(q[t * a.sq.t + threadIdx.x]) * a.scale;
-        }
-        const float vt = bf16_to_f32(v[t * a.sv.t]);
-        const float d = expf(la_log_decay(g[t * a.sg.t]));
-        __syncthreads();
-        float o_part = 0.f;
-#pragma unroll
-        for (int m = 0; m < R; ++m) {
-            S[m] = d * S[m] + ks[r + 8 * m] * vt;
-            o_part += qs[r + 8 * m] * S[m];
-        }
-        red[r][c] = o_part;
-        __syncthreads();
-        if (r == 0) {
-            float x = 0.f;
-            for (int m = 0; m < 8; ++m) x += red[m][c];
-            o[t * a.so.t] = f32_to_bf16(x);
-        }
-        if (t + 1 == en.n) commit();
+    uint16_t *go = a.out + b * a.so.b + h * a.so.h + tile * TV;
+    if (!en.state || (en.L == 0 && a.pool == a.pool_out)) {  // nothing to read, nothing new to write
+        for (int c = tid; c < TV; c += NT) go[c] = 0;
+        return;
     }
-    if (r == 0)
-        for (int t = en.L; t < a.T; ++t) o[t * a.so.t] = 0;
+
+    // this thread's columns, and its first row
+    const int c0 = tid % LPR * CPL, r0 = tid / LPR;
+    const long long first = (((long long)en.slot * a.Hv + h) * DK + r0) * a.Dv + tile * TV + c0;
+    constexpr int kSize = 16 / CPL;
+    const long long row_bytes = (long long)Sh::RPP * a.Dv * kSize;
+    const char *in = static_cast<const char *>(a.pool) + first * kSize;
+    const uint8_t *sin = ST == RGDR_MXI8 ? a.scales + first / kMxBlock : nullptr;
+    const int srow = Sh::RPP * (a.Dv / kMxBlock);
+
+    float q0 = 0.f, k0 = 0.f, g0 = 0.f, vt[CPL] = {};
+    if (en.L) {
+        if (tid < DK) {
+            q0 = bf16_to_f32(a.q[b * a.sq.b + hq * a.sq.h + tid]) * a.scale;
+            k0 = bf16_to_f32(a.k[b * a.sk.b + hq * a.sk.h + tid]);
+        }
+        load_bf16<CPL>(vt, a.v + b * a.sv.b + h * a.sv.h + tile * TV + c0);
+        g0 = a.g[b * a.sg.b + h * a.sg.h];
+    }
+    u32x4 w[R];
+    uint32_t eb[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(in + r * row_bytes));
+        if constexpr (ST == RGDR_MXI8) eb[r] = sin[r * srow];
+    }
+    if (tid < DK) qk[tid] = f32x2_t{q0, k0};
+    const float keep = en.L ? expf(la_log_decay(g0)) : 1.f;
+    __syncthreads();
+
+    char *const o_state = static_cast<char *>(a.pool_out) + first * kSize;
+    uint8_t *const o_scale = ST == RGDR_MXI8 ? a.scales_out + first / kMxBlock : nullptr;
+    float acc[CPL] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const f32x2_t op = qk[r0 + r * Sh::RPP];
+        const float sc = ST == RGDR_MXI8 ? mx_scale(eb[r]) * keep : keep;  // a power of two: exact
+        float x[CPL];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            x[c] = __builtin_fmaf(op[1], vt[c], sc * Piece<ST>::get(w[r], c));
+            acc[c] = __builtin_fmaf(op[0], x[c], acc[c]);
+        }
+        if (en.n) w[r] = round_piece<ST>(x, eb[r]);  // else the token is rejected: the bytes as they were
+        __builtin_nontemporal_store(w[r], reinterpret_cast<u32x4 *>(o_state + r * row_bytes));
+        if constexpr (ST == RGDR_MXI8)
+            if ((lane & 1) == 0) o_scale[r * srow] = (uint8_t)eb[r];
+    }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        const float x = row_lanes_sum<LPR>(acc[c]);
+        if (lane < LPR) red[wave][c0 + c] = x;
+    }
+    __syncthreads();
+    for (int c = tid; c < TV; c += NT) {
+        float x = 0.f;
+#pragma unroll
+        for (int m = 0; m < NW; ++m) x += red[m][c];
+        go[c] = f32_to_bf16(x);  // 0 where the entry has no token: its q, k and v are zero
+    }
+}
+
+// 2 to 8 tokens, on the matrix cores: one workgroup for each (entry, value head, 128 columns), CB
+// blocks of 32 columns for each wave. A wave moves 32 rows at a time, in whole lines (16 bytes for
+// each lane, up to 128 for each row), through LDS into the layout of the products' results,
+// transposed (lanes: rows i, registers: columns j), and back; as bf16 they become an operand of
+// S^T q on the way. The tokens are a quarter of the products' 32 columns; the products are far
+// from bounding the call all the same (30 of them, under 0.5 us, for 4096 elements, whose bytes
+// take a compute unit 0.4 to 1.6 us).
+template <int ST, int DK, int CB>
+__global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int tiles) {
+    constexpr int KP = DK / 8;                          // 16-byte pieces of a q or k row
+    constexpr int NI = DK / 32;                         // tiles of 32 rows
+    constexpr int NT = 256 / CB, NW = 4 / CB;
+    constexpr int PL = ST == RGDR_F32 ? 2 : 1;          // bf16 and 8-bit states are whole bf16 numbers
+    constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
+    constexpr int WP = 2 * kSize;                       // words of 8 columns
+    constexpr int PC = CB * 2 * kSize;                  // 16-byte pieces of the wave's part of a row
+    constexpr int NM = 32 * PC / 64;                    // of a tile, in each lane's hands
+    static_assert(PC <= 8 && NM >= 1, "a wave moves up to 128 bytes of a row");
+    __shared__ __align__(256) char lq[kMaxT * DK * 2], lk[kMaxT * DK * 2], lv[kMaxT * 256];
+    __shared__ __align__(256) char ls[NW][PL][32 * 64], lw[NW][32 * PC * 16];
+
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hf = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int item = xcd_item(blockIdx.x, gridDim.x);
+    const int tile = item % tiles;
+    item /= tiles;
+    const int h = item % a.Hv, b = item / a.Hv, hq = h / a.group;
+    const LaEntry en = la_entry(a, b);
+    const int L = en.L, n = en.n;
+    const int col0 = tile * 128 + wave * CB * 32;  // the wave's first column
+    const bool mine = col0 < a.Dv;                 // CB divides D_v / 32
+    const int vpieces = min(16, (a.Dv - tile * 128) / 8);
+    uint16_t *const go = a.out + b * a.so.b + h * a.so.h + tile * 128;
+    for (int j = tid; j < (a.T - L) * vpieces; j += NT)
+        *reinterpret_cast<u32x4 *>(go + (L + j / vpieces) * a.so.t + j % vpieces * 8) = u32x4{0, 0, 0, 0};
+    if (!en.state || (L == 0 && a.pool == a.pool_out)) return;
+
+    // operands: eight rows of q, k and v (the last token's again behind it: those have no weight)
+    constexpr int QN = (DK + NT - 1) / NT, VN = (kMaxT * 16 + NT - 1) / NT;
+    u32x4 rq[QN] = {}, rk[QN] = {}, rv[VN] = {};
+    double G = 0.0;
+    const int tg = lane & 7;
+    if (L) {
+#pragma unroll
+        for (int m = 0; m < QN; ++m) {
+            const int j = m * NT + tid, t = min(j / KP, L - 1), c = j % KP * 8;
+            if (j < DK) {
+                rq[m] = *reinterpret_cast<const u32x4 *>(a.q + b * a.sq.b + hq * a.sq.h + t * a.sq.t + c);
+                rk[m] = *reinterpret_cast<const u32x4 *>(a.k + b * a.sk.b + hq * a.sk.h + t * a.sk.t + c);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < VN; ++m) {
+            const int j = m * NT + tid, t = min(j / 16, L - 1), c = min(j % 16, vpieces - 1) * 8;
+            if (j < kMaxT * 16)
+                rv[m] = *reinterpret_cast<const u32x4 *>(a.v + b * a.sv.b + h * a.sv.h + t * a.sv.t + tile * 128 + c);
+        }
+        if (tg < L) G = (double)la_log_decay(a.g[b * a.sg.b + h * a.sg.h + tg * a.sg.t]);
+    }
+    // the state: lane by lane along its rows' pieces
+    const long long head = ((long long)en.slot * a.Hv + h) * DK * a.Dv + col0;
+    const int row_l = lane / PC, piece_l = lane % PC;
+    const long long lane_off = (long long)row_l * a.Dv * kSize + piece_l * 16;
+    const long long move = (long long)(64 / PC) * a.Dv * kSize;  // rows of one instruction
+    u32x4 w[NI][NM];
+    uint32_t eb[NI];  // CB scale bytes of row 32 it + map32(lane % 32)
+    const long long se = (head + (long long)map32(col) * a.Dv) / kMxBlock;
+    if (mine)
+#pragma unroll
+        for (int it = 0; it < NI; ++it) {
+            const char *p = static_cast<const char *>(a.pool) + (head + (long long)it * 32 * a.Dv) * kSize + lane_off;
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+                w[it][m] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + m * move));
+            if constexpr (ST == RGDR_MXI8) {
+                const uint8_t *sp = a.scales + se + (long long)it * 32 * (a.Dv / kMxBlock);
+                eb[it] = CB == 1 ? *sp : *reinterpret_cast<const uint16_t *>(sp);
+            }
+        }
+#pragma unroll
+    for (int m = 0; m < QN; ++m) {
+        const int j = m * NT + tid;
+        if (j < DK) {
+            *reinterpret_cast<u32x4 *>(lq + lds_at<KP>(j / KP, j % KP)) = rq[m];
+            *reinterpret_cast<u32x4 *>(lk + lds_at<KP>(j / KP, j % KP)) = rk[m];
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < VN; ++m) {
+        const int j = m * NT + tid;
+        if (j < kMaxT * 16) *reinterpret_cast<u32x4 *>(lv + lds_at<16>(j / 16, j % 16)) = rv[m];
+    }
+    // decay sums in fp64 (a token that forgets all leaves a large sum under the later ones'
+    // differences), the same in every group of eight lanes
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) {
+        const double y = __shfl_up(G, m);
+        if (tg >= m) G += y;
+    }
+    const double G_n = n ? __shfl(G, n - 1) : 0.0, G_t = __shfl(G, col & 7);
+    const float keep = expf((float)G_n);
+    const float wk1 = tg < n ? expf((float)(G_n - G)) : 0.f;  // what S_n keeps of token tg
+    const float carry = expf((float)G_t) * a.scale;
+    float gap[4];  // decay from token s = 4 hf + r to token t = lane % 32
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const double d = G_t - __shfl(G, hf * 4 + r);
+        gap[r] = hf * 4 + r <= col && col < L ? expf((float)d) * a.scale : 0.f;
+    }
+    __syncthreads();
+    if (!mine) return;
+
+    // scores: lanes t, registers s = 4 hf + 0..3; then s = 0..7 in the lower lanes
+    f32x16 x = {};
+#pragma unroll
+    for (int c = 0; c < DK / 16; ++c)
+        x = mfma(__builtin_bit_cast(u32x4, lds_read(lk + lds_at<KP>(col & 7, c * 2 + hf))),
+                 lds_read(lq + lds_at<KP>(col & 7, c * 2 + hf)), x);
+    float y[8], rest[8];
+    u32x4 p_hi, p_lo;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t z = __float_as_uint(gap[r] != 0.f ? x[r] * gap[r] : 0.f);
+        const auto sw = __builtin_amdgcn_permlane32_swap(z, z, false, false);
+        y[r] = hf ? 0.f : __uint_as_float(sw[0]);
+        y[r + 4] = hf ? 0.f : __uint_as_float(sw[1]);
+    }
+    split2(y, p_hi, p_lo, rest);
+    // values: lanes j, eight tokens in each lane (the upper lanes' have no weight), and the same
+    // weighted for the state
+    u32x4 vf[CB], v_hi[CB], v_lo[CB], v_lo2[CB];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+        vf[cb] = __builtin_bit_cast(u32x4, lds_read_tr<16>(lv, 0, wave * CB + cb, col));
+        float r1[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float wk = __shfl(wk1, e);
+            y[e] = hf ? 0.f : (e & 1 ? bf16_hi(vf[cb][e / 2]) : bf16_lo(vf[cb][e / 2])) * wk;
+        }
+        split2(y, v_hi[cb], v_lo[cb], r1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v_lo2[cb][e] = pack_bf16x2(r1[2 * e] - bf16_lo(v_lo[cb][e]), r1[2 * e + 1] - bf16_hi(v_lo[cb][e]));
+    }
+
+    f32x16 o[CB] = {};
+    const bool store = n || a.pool != a.pool_out;
+    char *const raw = lw[wave];
+    // The wave's own pieces, read back across its lanes: LDS serves a wave's accesses in order, and
+    // the compiler is kept from reordering them.
+    auto in_order = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            *reinterpret_cast<u32x4 *>(raw + lds_at<PC>(m * (64 / PC) + row_l, piece_l)) = w[it][m];
+        in_order();
+        const bf16x8 k = lds_read_tr<KP>(lk, 0, it, col);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            // row map32(lane % 32) of the tile, columns 32 cb + 16 kb + 8 hf .. + 7
+            float s[2][8];
+            const float sc = ST == RGDR_MXI8 ? mx_scale((eb[it] >> (8 * cb)) & 255) : 1.f;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int at = (cb * 32 + kb * 16 + hf * 8) * kSize;  // bytes into the row
+                u32x4 hi, lo;
+                uint32_t u[WP];
+                if constexpr (ST == RGDR_MXI8) {
+                    const u32x2 z = *reinterpret_cast<const u32x2 *>(raw + lds_at<PC>(map32(col), at / 16) + at % 16);
+                    u[0] = z[0];
+                    u[1] = z[1];
+                } else {
+#pragma unroll
+                    for (int m = 0; m < WP / 4; ++m) {
+                        const u32x4 z = *reinterpret_cast<const u32x4 *>(raw + lds_at<PC>(map32(col), at / 16 + m));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[m * 4 + e] = z[e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (ST == RGDR_F32)
+                        s[kb][e] = __uint_as_float(u[e]);
+                    else if constexpr (ST == RGDR_BF16)
+                        s[kb][e] = e & 1 ? bf16_hi(u[e / 2]) : bf16_lo(u[e / 2]);
+                    else
+                        s[kb][e] = mx_code(u[e / 4], e % 4) * sc;
+                }
+                const int pa = lds_at<4>(map32(col), kb * 2 + hf);
+                if constexpr (ST == RGDR_F32) {
+                    split2(s[kb], hi, lo, rest);
+                    *reinterpret_cast<u32x4 *>(ls[wave][PL - 1] + pa) = lo;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        hi[e] = ST == RGDR_BF16 ? u[e % WP] : pack_bf16x2(s[kb][2 * e], s[kb][2 * e + 1]);
+                }
+                *reinterpret_cast<u32x4 *>(ls[wave][0] + pa) = hi;
+            }
+            in_order();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const bf16x8 q = lds_read(lq + lds_at<KP>(col & 7, (it * 2 + c) * 2 + hf));
+#pragma unroll
+                for (int pl = PL - 1; pl >= 0; --pl)
+                    o[cb] = mfma(__builtin_bit_cast(u32x4, lds_read_tr<4>(ls[wave][pl], c * 16, 0, lane)), q, o[cb]);
+            }
+            in_order();
+            if (!n) continue;
+            f32x16 z;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z[r] = s[r / 8][r % 8] * keep;
+            z = mfma(v_lo2[cb], k, z);
+            z = mfma(v_lo[cb], k, z);
+            z = mfma(v_hi[cb], k, z);
+            float inv = 0.f;
+            if constexpr (ST == RGDR_MXI8) {
+                float most = 0.f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) most = mx_larger(most, z[r]);
+                const uint32_t top = mx_top_bits(most);  // as whole numbers NaN is the largest
+                const auto sw = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+                const uint32_t e = mx_exponent(max(sw[0], sw[1]));
+                inv = mx_inverse(e);
+                eb[it] = (eb[it] & ~(255u << (8 * cb))) | e << (8 * cb);
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int at = (cb * 32 + kb * 16 + hf * 8) * kSize;
+                if constexpr (ST == RGDR_MXI8) {
+                    u32x2 u;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        u[m] = mx_pack4(mx_code_bits(z[kb * 8 + m * 4], inv), mx_code_bits(z[kb * 8 + m * 4 + 1], inv),
+                                        mx_code_bits(z[kb * 8 + m * 4 + 2], inv), mx_code_bits(z[kb * 8 + m * 4 + 3], inv));
+                    *reinterpret_cast<u32x2 *>(raw + lds_at<PC>(map32(col), at / 16) + at % 16) = u;
+                } else {
+#pragma unroll
+                    for (int m = 0; m < WP / 4; ++m) {
+                        u32x4 u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = ST == RGDR_F32 ? __float_as_uint(z[kb * 8 + m * 4 + e])
+                                                  : pack_bf16x2(z[kb * 8 + 2 * e], z[kb * 8 + 2 * e + 1]);
+                        *reinterpret_cast<u32x4 *>(raw + lds_at<PC>(map32(col), at / 16 + m)) = u;
+                    }
+                }
+            }
+        }
+        in_order();
+        if (store) {
+            char *p = static_cast<char *>(a.pool_out) + (head + (long long)it * 32 * a.Dv) * kSize + lane_off;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + lds_at<PC>(m * (64 / PC) + row_l, piece_l));
+                __builtin_nontemporal_store(u, reinterpret_cast<u32x4 *>(p + m * move));
+            }
+            if constexpr (ST == RGDR_MXI8)
+                if (hf == 0) {
+                    uint8_t *sp = a.scales_out + se + (long long)it * 32 * (a.Dv / kMxBlock);
+                    if constexpr (CB == 1)
+                        *sp = (uint8_t)eb[it];
+                    else
+                        *reinterpret_cast<uint16_t *>(sp) = (uint16_t)eb[it];
+                }
+        }
+        in_order();
+    }
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[cb][r] *= carry;
+        o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_lo), o[cb]);
+        o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_hi), o[cb]);
+        if (col < L) {
+            uint16_t *row = go + col * a.so.t + (wave * CB + cb) * 32 + hf * 8;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                u32x4 z;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = pack_bf16x2(o[cb][m * 8 + 2 * e], o[cb][m * 8 + 2 * e + 1]);
+                *reinterpret_cast<u32x4 *>(row + m * 16) = z;
+            }
+        }
+    }
+}
+
+template <int ST, int DK, int CB>
+static void launch_tokens(const LaArgs &a, hipStream_t stream) {
+    const int tiles = (a.Dv + 127) / 128;
+    const dim3 grid((unsigned)((long long)a.B * a.Hv * tiles));
+    hipLaunchKernelGGL((la_tokens_kernel<ST, DK, CB>), grid, dim3(256 / CB), 0, stream, a, tiles);
+}
+
+template <int ST, int DK, int TV>
+static void launch_step_tv(const LaArgs &a, hipStream_t stream) {
+    const int tiles = a.Dv / TV;
+    const dim3 grid((unsigned)((long long)a.B * a.Hv * tiles)), block(StepShape<ST, DK, TV>::NT);
+    hipLaunchKernelGGL((la_step_kernel<ST, DK, TV>), grid, block, 0, stream, a, tiles);
+}
+
+template <int ST, int DK>
+static void launch_dk(const LaArgs &a, hipStream_t stream) {
+    if (a.T > 1) {
+        // Two blocks of 32 columns for each wave move 16-bit and 8-bit states in longer runs, once
+        // that leaves every SIMD two waves (T = 4, H_v = 32, D = 128; two blocks against one: bf16
+        // B = 16 11.8 against 10.8 us, B = 32 15.8 against 20.5; 8 bits 12.6 against 10.3 and 15.5
+        // against 19.3).
+        if constexpr (ST != RGDR_F32) {
+            if (a.Dv % 64 == 0 && (long long)a.B * a.Hv * (a.Dv / 64) >= 2048)
+                return launch_tokens<ST, DK, 2>(a, stream);
+        }
+        launch_tokens<ST, DK, 1>(a, stream);
+    } else if (a.Dv % 128 == 0 && (long long)a.B * a.Hv * (a.Dv / 128) >= 512) {
+        launch_step_tv<ST, DK, 128>(a, stream);
+    } else if (a.Dv % 64 == 0) {
+        launch_step_tv<ST, DK, 64>(a, stream);
+    } else {
+        launch_step_tv<ST, DK, 32>(a, stream);
+    }
 }
 
 template <int ST>
-static rgdr_status launch_recurrent_st(const LaArgs &a, int D_k, hipStream_t stream) {
-    const int tiles = a.Dv / 32;
-    const dim3 grid((unsigned)((long long)a.B * a.Hv * tiles)), block(256);
+static rgdr_status launch_decode(const LaArgs &a, int D_k, hipStream_t stream) {
     if (D_k == 64)
-        hipLaunchKernelGGL((la_recurrent_kernel<ST, 64>), grid, block, 0, stream, a, tiles);
+        launch_dk<ST, 64>(a, stream);
     else if (D_k == 128)
-        hipLaunchKernelGGL((la_recurrent_kernel<ST, 128>), grid, block, 0, stream, a, tiles);
+        launch_dk<ST, 128>(a, stream);
     else
-        hipLaunchKernelGGL((la_recurrent_kernel<ST, 256>), grid, block, 0, stream, a, tiles);
+        launch_dk<ST, 256>(a, stream);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
-}
-
-rgdr_status la_launch_recurrent(const LaArgs &a, int state_dtype, int D_k, hipStream_t stream) {
-    if (state_dtype == RGDR_F32) return launch_recurrent_st<RGDR_F32>(a, D_k, stream);
-    if (state_dtype == RGDR_BF16) return launch_recurrent_st<RGDR_BF16>(a, D_k, stream);
-    return launch_recurrent_st<RGDR_MXI8>(a, D_k, stream);
 }
 
 rgdr_status la_check_sizes(int max_t, int32_t B, int32_t H_v, int32_t T, int32_t D_k, int32_t D_v) {
@@ -201,5 +612,7 @@ extern "C" rgdr_status la_decode(const void *query, const la_strides *query_stri
             state_out, state_scales_out))
         return st;
     if (B == 0) return RGDR_OK;
-    return la_launch_recurrent(a, state_dtype, D_k, stream);
+    if (state_dtype == RGDR_F32) return launch_decode<RGDR_F32>(a, D_k, stream);
+    if (state_dtype == RGDR_BF16) return launch_decode<RGDR_BF16>(a, D_k, stream);
+    return launch_decode<RGDR_MXI8>(a, D_k, stream);
 }

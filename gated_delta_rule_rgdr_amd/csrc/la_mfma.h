@@ -1,0 +1,80 @@
+// la_mfma.h -- matrix-core helpers of the linear-attention kernels: operands from LDS, bf16 splits.
+// Not part of the C ABI.
+//
+// v_mfma_f32_32x32x16_bf16: operand A's lane l holds row l % 32, B's column l % 32, both the 8
+// products 8 (l / 32) .. + 7; register r of the result's lane l is row 8 (r / 4) + 4 (l / 32) +
+// r % 4 of column l % 32.
+#pragma once
+
+#include "la_common.h"
+
+namespace rgdr {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// 16-byte pieces of LDS rows are permuted within each row, so that both kinds of reads spread over
+// the banks: 16 lanes at the same piece of 16 rows, and 4 rows times 4 neighbouring pieces.
+template <int PIECES>
+__device__ __forceinline__ int swz(int row) {
+    if constexpr (PIECES == 2)
+        return (row >> 3) & 1;
+    else if constexpr (PIECES == 4)
+        return (row >> 2) & 3;
+    else if constexpr (PIECES == 8)
+        return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    else
+        return ((row & 3) << 2) | ((row >> 2) & 3);
+}
+
+template <int PIECES>
+__device__ __forceinline__ int lds_at(int row, int piece) {
+    return row * (PIECES * 16) + ((piece ^ swz<PIECES>(row)) << 4);
+}
+
+__device__ __forceinline__ bf16x8 lds_read(const char *p) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
+}
+
+// Eight rows (tokens) of one column for each lane: lane l gets column map32(l % 32) of its
+// 32-column group, rows 8 * (l / 32) .. + 7 of the 16 at `row0`. The hardware transposes 4 rows
+// by 16 columns for each 16 lanes, which read them as 4-column pieces; lane l's piece is
+// chosen so that consecutive accumulator registers hold consecutive rows (see map32).
+template <int PIECES>
+__device__ __forceinline__ bf16x8 lds_read_tr(char *m, int row0, int group, int lane) {
+    const int n = lane & 15, row = row0 + ((lane >> 5) << 3) + (n >> 2);
+    const int piece = group * 4 + ((lane >> 4) & 1) * 2 + (n & 1), half = (n & 2) << 2;
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(m + lds_at<PIECES>(row, piece) + half));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_ptr)(m + lds_at<PIECES>(row + 4, piece) + half));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The column (or row) that position n of a 32-wide matrix operand read by lds_read_tr stands for:
+// groups of four in the order 0, 2, 1, 3. An accumulator lane holds positions 8 m + 4 (l / 32) + 0..3
+// in registers 4 m + 0..3, which are then the 8 consecutive rows 16 (m / 2) + 8 (l / 32) + 0..7
+// in registers 8 (m / 2) + 0..7: what a matrix operand's lane holds, and 16 bytes of output.
+__device__ __forceinline__ int map32(int n) {
+    return (n & 16) | ((n & 4) << 1) | ((n & 8) >> 1) | (n & 3);
+}
+
+// x = hi + lo (+ lo2) in bf16, for eight values.
+__device__ __forceinline__ void split2(const float (&x)[8], u32x4 &hi, u32x4 &lo, float (&rest)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        rest[2 * i] = x[2 * i] - bf16_lo(hi[i]);
+        rest[2 * i + 1] = x[2 * i + 1] - bf16_hi(hi[i]);
+        lo[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
+    }
+}
+
+__device__ __forceinline__ f32x16 mfma(u32x4 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b, c, 0, 0, 0);
+}
+
+}  // namespace rgdr

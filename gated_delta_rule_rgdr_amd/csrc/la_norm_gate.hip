@@ -16,55 +16,132 @@ struct NormArgs {
     int B, H, T, D, sigmoid;
 };
 
+// 16 bytes of a row as fp32 values, and back.
 template <typename E>
-__device__ __forceinline__ float norm_load(const void *p, long long e) {
-    if constexpr (sizeof(E) == 2 && !__is_same(E, _Float16))
-        return bf16_to_f32(static_cast<const uint16_t *>(p)[e]);
-    else
-        return static_cast<float>(static_cast<const E *>(p)[e]);
-}
-template <typename E>
-__device__ __forceinline__ void norm_store(void *p, long long e, float x) {
-    if constexpr (sizeof(E) == 2 && !__is_same(E, _Float16))
-        static_cast<uint16_t *>(p)[e] = f32_to_bf16(x);
-    else
-        static_cast<E *>(p)[e] = static_cast<E>(x);
-}
-
-// One wave for each row.
-template <typename E>
-__global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a) {
-    const long long rows = (long long)a.B * a.T * a.H;
-    const long long stride = (long long)gridDim.x * 4;
-    const int lane = threadIdx.x & 63;
-    for (long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += stride) {
-        const int h = (int)(r % a.H);
-        const long long bt = r / a.H;
-        const int t = (int)(bt % a.T), b = (int)(bt / a.T);
-        const long long eo = b * a.so.b + h * a.so.h + t * a.so.t;
-        if (a.lens && t >= a.lens[b]) {
-            for (int d = lane; d < a.D; d += 64) norm_store<E>(a.out, eo + d, 0.f);
-            continue;
-        }
-        const long long ex = b * a.sx.b + h * a.sx.h + t * a.sx.t;
-        const long long eg = b * a.sg.b + h * a.sg.h + t * a.sg.t;
-        float ss = 0.f;
-        for (int d = lane; d < a.D; d += 64) {
-            const float x = norm_load<E>(a.x, ex + d);
-            ss += x * x;
-        }
+struct NormVec {
+    static constexpr int N = 16 / sizeof(E);
+    static __device__ __forceinline__ void get(float (&x)[N], const u32x4 &w) {
 #pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) ss += __shfl_xor(ss, m);
-        const float r_rms = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-        for (int d = lane; d < a.D; d += 64) {
-            float y = norm_load<E>(a.x, ex + d) * r_rms * a.weight[h * a.sw + d];
-            if (a.gate) {
-                const float z = norm_load<E>(a.gate, eg + d);
-                y *= a.sigmoid ? sigmoid_f32(z) : z * sigmoid_f32(z);
-            }
-            norm_store<E>(a.out, eo + d, y);
+        for (int c = 0; c < N; ++c) {
+            if constexpr (sizeof(E) == 4)
+                x[c] = __uint_as_float(w[c]);
+            else if constexpr (__is_same(E, _Float16))
+                x[c] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[c / 2] >> (c % 2 * 16))));
+            else
+                x[c] = c & 1 ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2]);
         }
     }
+    static __device__ __forceinline__ u32x4 put(const float (&x)[N]) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 4)
+                w[i] = __float_as_uint(x[i]);
+            else if constexpr (__is_same(E, _Float16))
+                w[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i])) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i + 1])) << 16;
+            else
+                w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        }
+        return w;
+    }
+};
+
+// LPR lanes for each row, NV pieces of 16 bytes in each lane: the row stays in registers between the
+// sum and the product, so x and the gate are read once. Rows are taken in out's order (heads
+// fastest). Bound: the bytes.
+template <typename E, int LPR, int NV>
+__global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a) {
+    using V = NormVec<E>;
+    constexpr int ROWS = 256 / LPR;
+    const long long r0 = (long long)blockIdx.x * ROWS, bt0 = r0 / a.H;
+    const uint32_t hh = (uint32_t)(r0 - bt0 * a.H) + threadIdx.x / LPR, dt = hh / (uint32_t)a.H;
+    const int h = (int)(hh - dt * a.H);
+    const int b0 = (int)(bt0 / a.T);
+    const uint32_t tt = (uint32_t)(bt0 - (long long)b0 * a.T) + dt, db = tt / (uint32_t)a.T;
+    const int t = (int)(tt - db * a.T), b = b0 + (int)db;
+    if (b >= a.B) return;
+    const int c0 = threadIdx.x % LPR * V::N;
+    E *out = static_cast<E *>(a.out) + b * a.so.b + h * a.so.h + t * a.so.t;
+    if (a.lens && t >= a.lens[b]) {
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+            if (c0 + m * LPR * V::N < a.D)
+                *reinterpret_cast<u32x4 *>(out + c0 + m * LPR * V::N) = u32x4{0, 0, 0, 0};
+        return;
+    }
+    const E *x = static_cast<const E *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
+    const E *z = static_cast<const E *>(a.gate) + b * a.sg.b + h * a.sg.h + t * a.sg.t;
+    const float *w = a.weight + h * a.sw;
+    u32x4 wx[NV], wz[NV];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int c = c0 + m * LPR * V::N;
+        wx[m] = wz[m] = u32x4{0, 0, 0, 0};
+        if (c < a.D) {
+            wx[m] = *reinterpret_cast<const u32x4 *>(x + c);
+            if (a.gate) wz[m] = *reinterpret_cast<const u32x4 *>(z + c);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        float v[V::N];
+        V::get(v, wx[m]);
+#pragma unroll
+        for (int c = 0; c < V::N; ++c) ss = __builtin_fmaf(v[c], v[c], ss);
+    }
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor(ss, m);
+    const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int c = c0 + m * LPR * V::N;
+        if (c >= a.D) continue;
+        float v[V::N], g[V::N];
+        V::get(v, wx[m]);
+        V::get(g, wz[m]);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) {
+            v[i] *= r * w[c + i];
+            if (a.gate) v[i] *= a.sigmoid ? sigmoid_fast(g[i]) : g[i] * sigmoid_fast(g[i]);
+        }
+        *reinterpret_cast<u32x4 *>(out + c) = V::put(v);
+    }
+}
+
+template <typename E, int LPR, int NV>
+static void launch_norm_lanes(const NormArgs &a, unsigned grid, hipStream_t stream) {
+    hipLaunchKernelGGL((la_norm_gate_kernel<E, LPR, NV>), dim3(grid), dim3(256), 0, stream, a);
+}
+
+// The fewest lanes that hold a row in one piece each; of long rows a wave holds several.
+template <typename E>
+static rgdr_status launch_norm(const NormArgs &a, hipStream_t stream) {
+    const int pieces = a.D / NormVec<E>::N;
+    const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
+    const __int128 rows = (__int128)a.B * a.T * a.H, want = (rows + 256 / lanes - 1) / (256 / lanes);
+    if (want > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
+    const unsigned grid = (unsigned)want;
+    if (pieces <= 8)
+        launch_norm_lanes<E, 8, 1>(a, grid, stream);
+    else if (pieces <= 16)
+        launch_norm_lanes<E, 16, 1>(a, grid, stream);
+    else if (pieces <= 32)
+        launch_norm_lanes<E, 32, 1>(a, grid, stream);
+    else if (pieces <= 64)
+        launch_norm_lanes<E, 64, 1>(a, grid, stream);
+    else if (pieces <= 128)
+        launch_norm_lanes<E, 64, 2>(a, grid, stream);
+    else if (pieces <= 256)
+        launch_norm_lanes<E, 64, 4>(a, grid, stream);
+    else if (pieces <= 512)
+        launch_norm_lanes<E, 64, 8>(a, grid, stream);
+    else if (pieces <= 1024)
+        launch_norm_lanes<E, 64, 16>(a, grid, stream);
+    else
+        launch_norm_lanes<E, 64, 32>(a, grid, stream);
+    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 }  // namespace rgdr
@@ -108,13 +185,7 @@ extern "C" rgdr_status la_norm_gate(const void *x, const la_strides *x_strides, 
     a.T = T;
     a.D = D;
     a.sigmoid = (flags & LA_GATE_SIGMOID) != 0;
-    const __int128 rows = (__int128)B * T * H, want = (rows + 3) / 4;
-    const dim3 grid((unsigned)(want < 65536 ? want : 65536)), block(256);
-    if (dtype == RGDR_F32)
-        hipLaunchKernelGGL(la_norm_gate_kernel<float>, grid, block, 0, stream, a);
-    else if (dtype == RGDR_F16)
-        hipLaunchKernelGGL(la_norm_gate_kernel<_Float16>, grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL(la_norm_gate_kernel<uint16_t>, grid, block, 0, stream, a);
-    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+    if (dtype == RGDR_F32) return launch_norm<float>(a, stream);
+    if (dtype == RGDR_F16) return launch_norm<_Float16>(a, stream);
+    return launch_norm<uint16_t>(a, stream);
 }

@@ -25,67 +25,97 @@ __device__ __forceinline__ bool move_slots(const StateMove &m, int i, int &s, in
     return d >= 0 && d < m.N_dst;
 }
 
-// One thread for each block of 32 columns.
+// A lane holds 16 bytes of the wide pool, so both pools are read and written in whole lines: 4
+// columns in fp32 (8 lanes for a block), 8 in bf16 (4 lanes). U such units are in flight.
 template <bool BF16>
+struct Unit {
+    static constexpr int N = BF16 ? 8 : 4;            // columns
+    static constexpr int LANES = kMxBlock / N;        // lanes of a block
+    static constexpr int W = N / 4;                   // words of codes
+};
+
+// The largest of the magnitudes' bits over a block's lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false));  // lane ^ 1
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false));  // lane ^ 2
+    if constexpr (LANES == 8)
+        x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false));  // other quad of 8
+    return x;
+}
+
+template <bool BF16, int U>
 __global__ __launch_bounds__(256) void la_quantize_kernel(const StateMove m) {
-    const int i = blockIdx.x / m.parts;
+    using T = Unit<BF16>;
     int s, d;
-    if (!move_slots(m, i, s, d)) return;
+    if (!move_slots(m, blockIdx.x / m.parts, s, d)) return;
     const bool have = s >= 0 && s < m.N_src;
-    for (long long j = (long long)(blockIdx.x % m.parts) * 256 + threadIdx.x; j < m.blocks;
-         j += (long long)m.parts * 256) {
-        float x[kMxBlock];
-        const long long e = ((long long)s * m.blocks + j) * kMxBlock;
+    const long long units = m.blocks * T::LANES;
+    const long long j0 = (long long)(blockIdx.x % m.parts) * (256 * U) + threadIdx.x;
+    const u32x4 *in = reinterpret_cast<const u32x4 *>(m.in) + (have ? s : 0) * units;
+    uint32_t *out = reinterpret_cast<uint32_t *>(m.out) + d * units * T::W;
+    uint8_t *scales = m.scales_out + d * m.blocks;
+    u32x4 w[U];
 #pragma unroll
-        for (int c = 0; c < kMxBlock; ++c)
-            x[c] = !have  ? 0.f
-                   : BF16 ? bf16_to_f32(static_cast<const uint16_t *>(m.in)[e + c])
-                          : static_cast<const float *>(m.in)[e + c];
-        uint32_t top = 0;
+    for (int u = 0; u < U; ++u) {
+        const long long j = j0 + u * 256;
+        w[u] = u32x4{0, 0, 0, 0};
+        if (have && j < units) w[u] = __builtin_nontemporal_load(in + j);
+    }
 #pragma unroll
-        for (int c = 0; c < kMxBlock; ++c) top = max(top, __float_as_uint(x[c]) & 0x7FFFFFFFu);
-        const uint32_t eb = mx_exponent(top);
+    for (int u = 0; u < U; ++u) {
+        const long long j = j0 + u * 256;
+        float x[T::N], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < T::N; ++c) {
+            x[c] = !BF16 ? __uint_as_float(w[u][c]) : c & 1 ? bf16_hi(w[u][c / 2]) : bf16_lo(w[u][c / 2]);
+            top = mx_larger(top, x[c]);
+        }
+        const uint32_t eb = mx_exponent(block_max<T::LANES>(mx_top_bits(top)));
         const float inv = mx_inverse(eb);
-        uint32_t w[8];
+        if (j < units) {  // the units are whole blocks
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            w[c] = mx_pack4(mx_code_bits(x[4 * c], inv), mx_code_bits(x[4 * c + 1], inv),
-                            mx_code_bits(x[4 * c + 2], inv), mx_code_bits(x[4 * c + 3], inv));
-        u32x4 *o = reinterpret_cast<u32x4 *>(static_cast<char *>(m.out) +
-                                             ((long long)d * m.blocks + j) * kMxBlock);
-        o[0] = u32x4{w[0], w[1], w[2], w[3]};
-        o[1] = u32x4{w[4], w[5], w[6], w[7]};
-        m.scales_out[(long long)d * m.blocks + j] = (uint8_t)eb;
+            for (int c = 0; c < T::W; ++c)
+                out[j * T::W + c] = mx_pack4(mx_code_bits(x[4 * c], inv), mx_code_bits(x[4 * c + 1], inv),
+                                             mx_code_bits(x[4 * c + 2], inv), mx_code_bits(x[4 * c + 3], inv));
+            if (threadIdx.x % T::LANES == 0) scales[j / T::LANES] = (uint8_t)eb;
+        }
     }
 }
 
-template <bool BF16>
+template <bool BF16, int U>
 __global__ __launch_bounds__(256) void la_dequantize_kernel(const StateMove m) {
-    const int i = blockIdx.x / m.parts;
+    using T = Unit<BF16>;
     int s, d;
-    if (!move_slots(m, i, s, d)) return;
+    if (!move_slots(m, blockIdx.x / m.parts, s, d)) return;
     const bool have = s >= 0 && s < m.N_src;
-    for (long long j = (long long)(blockIdx.x % m.parts) * 256 + threadIdx.x; j < m.blocks;
-         j += (long long)m.parts * 256) {
-        const long long e = (long long)s * m.blocks + j;
-        u32x4 w[2] = {};
-        float sc = 0.f;
-        if (have) {
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const char *>(m.in) +
-                                                             e * kMxBlock);
-            w[0] = p[0];
-            w[1] = p[1];
-            sc = mx_scale(m.scales_in[e]);
-        }
-        const long long o = ((long long)d * m.blocks + j) * kMxBlock;
+    const long long units = m.blocks * T::LANES;
+    const long long j0 = (long long)(blockIdx.x % m.parts) * (256 * U) + threadIdx.x;
+    const uint32_t *in = reinterpret_cast<const uint32_t *>(m.in) + (have ? s : 0) * units * T::W;
+    const uint8_t *scales = m.scales_in + (have ? s : 0) * m.blocks;
+    u32x4 *out = reinterpret_cast<u32x4 *>(m.out) + d * units;
+    uint32_t w[U][T::W] = {}, eb[U] = {};
 #pragma unroll
-        for (int c = 0; c < kMxBlock; ++c) {
-            const float x = mx_code(w[c / 16][c / 4 % 4], c % 4) * sc;
-            if (BF16)
-                static_cast<uint16_t *>(m.out)[o + c] = f32_to_bf16(x);
-            else
-                static_cast<float *>(m.out)[o + c] = x;
+    for (int u = 0; u < U; ++u) {
+        const long long j = j0 + u * 256;
+        if (have && j < units) {
+#pragma unroll
+            for (int c = 0; c < T::W; ++c) w[u][c] = in[j * T::W + c];
+            eb[u] = scales[j / T::LANES];
         }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long long j = j0 + u * 256;
+        const float sc = mx_scale(eb[u]);
+        float x[T::N];
+#pragma unroll
+        for (int c = 0; c < T::N; ++c) x[c] = mx_code(w[u][c / 4], c % 4) * sc;
+        u32x4 y;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            y[c] = BF16 ? pack_bf16x2(x[2 * c % T::N], x[(2 * c + 1) % T::N]) : __float_as_uint(x[c]);
+        if (j < units) __builtin_nontemporal_store(y, out + j);
     }
 }
 
@@ -111,10 +141,23 @@ static rgdr_status move_check(const void *wide, int state_dtype, const void *cod
     m.N_src = N_src;
     m.N_dst = N_dst;
     m.blocks = (long long)blocks;
-    const long long full = (m.blocks + 255) / 256;
-    const long long most = 0x7FFFFFFFLL / n;  // the grid is counted in an int
-    m.parts = (unsigned)(full < most ? full : most);
     return RGDR_OK;
+}
+
+// Four units for each thread where that still gives every compute unit several workgroups, else one.
+template <bool BF16, bool BACK>
+static rgdr_status launch_move(StateMove &m, int n, hipStream_t stream) {
+    const long long groups = (m.blocks * Unit<BF16>::LANES + 255) / 256;
+    const bool four = groups / 4 * n >= 1024;
+    const long long parts = four ? (groups + 3) / 4 : groups;
+    if (parts * n > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
+    m.parts = (unsigned)parts;
+    const dim3 grid((unsigned)(parts * n)), block(256);
+    if (four)
+        hipLaunchKernelGGL((BACK ? la_dequantize_kernel<BF16, 4> : la_quantize_kernel<BF16, 4>), grid, block, 0, stream, m);
+    else
+        hipLaunchKernelGGL((BACK ? la_dequantize_kernel<BF16, 1> : la_quantize_kernel<BF16, 1>), grid, block, 0, stream, m);
+    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 }  // namespace rgdr
@@ -133,12 +176,8 @@ extern "C" rgdr_status la_state_quantize(const void *state, rgdr_dtype state_dty
     m.in = state;
     m.out = codes;
     m.scales_out = scales;
-    const dim3 grid((unsigned)n * m.parts), block(256);
-    if (state_dtype == RGDR_BF16)
-        hipLaunchKernelGGL(la_quantize_kernel<true>, grid, block, 0, stream, m);
-    else
-        hipLaunchKernelGGL(la_quantize_kernel<false>, grid, block, 0, stream, m);
-    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+    return state_dtype == RGDR_BF16 ? launch_move<true, false>(m, n, stream)
+                                    : launch_move<false, false>(m, n, stream);
 }
 
 extern "C" rgdr_status la_state_dequantize(const void *codes, const uint8_t *scales,
@@ -155,10 +194,6 @@ extern "C" rgdr_status la_state_dequantize(const void *codes, const uint8_t *sca
     m.in = codes;
     m.scales_in = scales;
     m.out = state;
-    const dim3 grid((unsigned)n * m.parts), block(256);
-    if (state_dtype == RGDR_BF16)
-        hipLaunchKernelGGL(la_dequantize_kernel<true>, grid, block, 0, stream, m);
-    else
-        hipLaunchKernelGGL(la_dequantize_kernel<false>, grid, block, 0, stream, m);
-    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+    return state_dtype == RGDR_BF16 ? launch_move<true, true>(m, n, stream)
+                                    : launch_move<false, true>(m, n, stream);
 }
