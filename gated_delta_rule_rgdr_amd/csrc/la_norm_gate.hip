@@ -48,100 +48,134 @@ struct NormVec {
 };
 
 // LPR lanes for each row, NV pieces of 16 bytes in each lane: the row stays in registers between the
-// sum and the product, so x and the gate are read once. Rows are taken in out's order (heads
-// fastest). Bound: the bytes.
-template <typename E, int LPR, int NV>
-__global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a) {
+// sum and the product, so x and the gate are read once. A workgroup's 256 / LPR groups of lanes
+// take HR heads (2^hr_log) times TR = 256 / LPR / HR tokens, and U such sets of tokens one after
+// the other with all their loads in flight: runs of several rows on both sides of the transposition
+// (x keeps a head's tokens together, out a token's heads). Bound: the bytes.
+template <typename E, int LPR, int NV, int U, bool GATED>
+__global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a, int hr_log, int h_blocks, int t_blocks) {
     using V = NormVec<E>;
-    constexpr int ROWS = 256 / LPR;
-    const long long r0 = (long long)blockIdx.x * ROWS, bt0 = r0 / a.H;
-    const uint32_t hh = (uint32_t)(r0 - bt0 * a.H) + threadIdx.x / LPR, dt = hh / (uint32_t)a.H;
-    const int h = (int)(hh - dt * a.H);
-    const int b0 = (int)(bt0 / a.T);
-    const uint32_t tt = (uint32_t)(bt0 - (long long)b0 * a.T) + dt, db = tt / (uint32_t)a.T;
-    const int t = (int)(tt - db * a.T), b = b0 + (int)db;
-    if (b >= a.B) return;
+    const int hb = blockIdx.x % h_blocks, tb = blockIdx.x / h_blocks % t_blocks;
+    const int b = blockIdx.x / h_blocks / t_blocks;
+    const int group = threadIdx.x / LPR, tr = (256 / LPR) >> hr_log;
+    const int h = (hb << hr_log) + (group & ((1 << hr_log) - 1));
+    const int t0 = tb * tr * U + (group >> hr_log);
+    if (h >= a.H) return;
+    const int L = a.lens ? min(a.lens[b], a.T) : a.T;
     const int c0 = threadIdx.x % LPR * V::N;
-    E *out = static_cast<E *>(a.out) + b * a.so.b + h * a.so.h + t * a.so.t;
-    if (a.lens && t >= a.lens[b]) {
-#pragma unroll
-        for (int m = 0; m < NV; ++m)
-            if (c0 + m * LPR * V::N < a.D)
-                *reinterpret_cast<u32x4 *>(out + c0 + m * LPR * V::N) = u32x4{0, 0, 0, 0};
-        return;
-    }
-    const E *x = static_cast<const E *>(a.x) + b * a.sx.b + h * a.sx.h + t * a.sx.t;
-    const E *z = static_cast<const E *>(a.gate) + b * a.sg.b + h * a.sg.h + t * a.sg.t;
+    const E *x = static_cast<const E *>(a.x) + b * a.sx.b + h * a.sx.h;
+    const E *z = static_cast<const E *>(a.gate) + b * a.sg.b + h * a.sg.h;
+    E *out = static_cast<E *>(a.out) + b * a.so.b + h * a.so.h;
     const float *w = a.weight + h * a.sw;
-    u32x4 wx[NV], wz[NV];
+    u32x4 wx[U][NV], wz[U][GATED ? NV : 1];
 #pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        const int c = c0 + m * LPR * V::N;
-        wx[m] = wz[m] = u32x4{0, 0, 0, 0};
-        if (c < a.D) {
-            wx[m] = *reinterpret_cast<const u32x4 *>(x + c);
-            if (a.gate) wz[m] = *reinterpret_cast<const u32x4 *>(z + c);
+    for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * tr;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) wx[u][m] = wz[u][GATED ? m : 0] = u32x4{0, 0, 0, 0};
+        if (t < L && c0 < a.D) {
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                // a lane whose further pieces lie past the row's end reads its last piece, and
+                // leaves it out below
+                const int c = m ? min(c0 + m * LPR * V::N, a.D - V::N) : c0;
+                wx[u][m] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + t * a.sx.t + c));
+                if (GATED) wz[u][m] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(z + t * a.sg.t + c));
+            }
         }
     }
-    float ss = 0.f;
 #pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        float v[V::N];
-        V::get(v, wx[m]);
+    for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * tr;
+        float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < V::N; ++c) ss = __builtin_fmaf(v[c], v[c], ss);
-    }
+        for (int m = 0; m < NV; ++m) {
+            float v[V::N], s1 = 0.f;
+            V::get(v, wx[u][m]);
 #pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor(ss, m);
-    const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
-#pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        const int c = c0 + m * LPR * V::N;
-        if (c >= a.D) continue;
-        float v[V::N], g[V::N];
-        V::get(v, wx[m]);
-        V::get(g, wz[m]);
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) {
-            v[i] *= r * w[c + i];
-            if (a.gate) v[i] *= a.sigmoid ? sigmoid_fast(g[i]) : g[i] * sigmoid_fast(g[i]);
+            for (int c = 0; c < V::N; ++c) s1 = __builtin_fmaf(v[c], v[c], s1);
+            ss += m == 0 || c0 + m * LPR * V::N < a.D ? s1 : 0.f;
         }
-        *reinterpret_cast<u32x4 *>(out + c) = V::put(v);
+#pragma unroll
+        for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor(ss, m);
+        const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
+        if (t >= a.T) continue;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int c = c0 + m * LPR * V::N;
+            if (c >= a.D) continue;
+            float v[V::N], g[V::N];
+            V::get(v, wx[u][m]);
+            V::get(g, wz[u][GATED ? m : 0]);
+#pragma unroll
+            for (int j = 0; j < V::N / 4; ++j) {
+                const f32x4 w4 = *reinterpret_cast<const f32x4 *>(w + c + j * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float &y = v[j * 4 + i];
+                    const float z1 = g[j * 4 + i];
+                    y *= r * w4[i];
+                    if (GATED) y *= (a.sigmoid ? 1.f : z1) * sigmoid_fast(z1);
+                    y = t < L ? y : 0.f;
+                }
+            }
+            __builtin_nontemporal_store(V::put(v), reinterpret_cast<u32x4 *>(out + t * a.so.t + c));
+        }
     }
 }
 
-template <typename E, int LPR, int NV>
-static void launch_norm_lanes(const NormArgs &a, unsigned grid, hipStream_t stream) {
-    hipLaunchKernelGGL((la_norm_gate_kernel<E, LPR, NV>), dim3(grid), dim3(256), 0, stream, a);
+template <typename E, int LPR, int NV, int U>
+static rgdr_status launch_norm_rows(const NormArgs &a, hipStream_t stream) {
+    constexpr int ROWS = 256 / LPR;
+    // the split of a workgroup's rows into heads and tokens that leaves the fewest idle; of equal
+    // ones the most heads
+    int hr_log = 0;
+    double best = 0;
+    for (int k = 0; (1 << k) <= ROWS; ++k) {
+        const int hr = 1 << k, tu = ROWS / hr * U;
+        const double use = (double)a.H / ((a.H + (long long)hr - 1) / hr * hr) * a.T /
+                           ((a.T + (long long)tu - 1) / tu * tu);
+        if (use >= best) {
+            best = use;
+            hr_log = k;
+        }
+    }
+    const int tu = (ROWS >> hr_log) * U;
+    const long long h_blocks = ((long long)a.H + (1 << hr_log) - 1) >> hr_log;
+    const long long t_blocks = ((long long)a.T + tu - 1) / tu;
+    if ((__int128)h_blocks * t_blocks * a.B > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
+    const dim3 grid((unsigned)(h_blocks * t_blocks * a.B)), block(256);
+    if (a.gate)
+        hipLaunchKernelGGL((la_norm_gate_kernel<E, LPR, NV, U, true>), grid, block, 0, stream, a, hr_log,
+                           (int)h_blocks, (int)t_blocks);
+    else
+        hipLaunchKernelGGL((la_norm_gate_kernel<E, LPR, NV, U, false>), grid, block, 0, stream, a, hr_log,
+                           (int)h_blocks, (int)t_blocks);
+    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+}
+
+// Two rows for each group of lanes where that still gives every compute unit four workgroups (B=16,
+// T=1024, H=32, D=128, bf16, against one and four: 55.7 us, 59.8, 58.4).
+template <typename E, int LPR>
+static rgdr_status launch_norm_lanes(const NormArgs &a, hipStream_t stream) {
+    if (a.T >= 2 && (__int128)a.B * a.T * a.H >= 2 * 1024 * (256 / LPR)) return launch_norm_rows<E, LPR, 1, 2>(a, stream);
+    return launch_norm_rows<E, LPR, 1, 1>(a, stream);
 }
 
 // The fewest lanes that hold a row in one piece each; of long rows a wave holds several.
 template <typename E>
 static rgdr_status launch_norm(const NormArgs &a, hipStream_t stream) {
     const int pieces = a.D / NormVec<E>::N;
-    const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
-    const __int128 rows = (__int128)a.B * a.T * a.H, want = (rows + 256 / lanes - 1) / (256 / lanes);
-    if (want > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
-    const unsigned grid = (unsigned)want;
-    if (pieces <= 8)
-        launch_norm_lanes<E, 8, 1>(a, grid, stream);
-    else if (pieces <= 16)
-        launch_norm_lanes<E, 16, 1>(a, grid, stream);
-    else if (pieces <= 32)
-        launch_norm_lanes<E, 32, 1>(a, grid, stream);
-    else if (pieces <= 64)
-        launch_norm_lanes<E, 64, 1>(a, grid, stream);
-    else if (pieces <= 128)
-        launch_norm_lanes<E, 64, 2>(a, grid, stream);
-    else if (pieces <= 256)
-        launch_norm_lanes<E, 64, 4>(a, grid, stream);
-    else if (pieces <= 512)
-        launch_norm_lanes<E, 64, 8>(a, grid, stream);
-    else if (pieces <= 1024)
-        launch_norm_lanes<E, 64, 16>(a, grid, stream);
-    else
-        launch_norm_lanes<E, 64, 32>(a, grid, stream);
-    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+    if (pieces <= 8) return launch_norm_lanes<E, 8>(a, stream);
+    if (pieces <= 16) return launch_norm_lanes<E, 16>(a, stream);
+    if (pieces <= 32) return launch_norm_lanes<E, 32>(a, stream);
+    if (pieces <= 64) return launch_norm_lanes<E, 64>(a, stream);
+    if (pieces <= 128) return launch_norm_rows<E, 64, 2, 1>(a, stream);
+    if (pieces <= 256) return launch_norm_rows<E, 64, 4, 1>(a, stream);
+    if (pieces <= 512) return launch_norm_rows<E, 64, 8, 1>(a, stream);
+    if constexpr (sizeof(E) == 4)
+        if (pieces > 1024) return launch_norm_rows<E, 64, 32, 1>(a, stream);
+    return launch_norm_rows<E, 64, 16, 1>(a, stream);
 }
 
 }  // namespace rgdr
