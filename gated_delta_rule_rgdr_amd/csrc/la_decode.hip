@@ -196,8 +196,9 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     constexpr int PC = CB * 2 * kSize;                  // 16-byte pieces of the wave's part of a row
     constexpr int NM = 32 * PC / 64;                    // of a tile, in each lane's hands
     static_assert(PC <= 8 && NM >= 1, "a wave moves up to 128 bytes of a row");
-    __shared__ __align__(256) char lq[kMaxT * DK * 2], lk[kMaxT * DK * 2], lv[kMaxT * 256];
-    __shared__ __align__(256) char ls[NW][PL][32 * 64], lw[NW][32 * PC * 16];
+    __shared__ __align__(256) char lq[kMaxT * lds_row_bytes<KP>()], lk[kMaxT * lds_row_bytes<KP>()];
+    __shared__ __align__(256) char lv[kMaxT * lds_row_bytes<16>()];
+    __shared__ __align__(256) char ls[NW][PL][32 * 64], lw[NW][32 * lds_row_bytes<PC>()];
 
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, hf = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -4,6 +4,8 @@
 // v_mfma_f32_32x32x16_bf16: operand A's lane l holds row l % 32, B's column l % 32, both the 8
 // products 8 (l / 32) .. + 7; register r of the result's lane l is row 8 (r / 4) + 4 (l / 32) +
 // r % 4 of column l % 32.
+// v_mfma_f32_16x16x32_bf16: rows and columns l % 16, products 8 (l / 16) .. + 7; the result's
+// register r is row 4 (l / 16) + r of column l % 16.
 #pragma once
 
 #include "la_common.h"
@@ -15,23 +17,22 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 16-byte pieces of LDS rows are permuted within each row, so that both kinds of reads spread over
-// the banks: 16 lanes at the same piece of 16 rows, and 4 rows times 4 neighbouring pieces.
+// 16-byte pieces of LDS rows of PIECES such pieces. A spare piece behind each row (where rows are
+// 128 bytes or more) puts the same piece of 16 rows on different banks; the reads that transpose take
+// four rows of 64 bytes, which then overlap on some banks, but every address is a lane's base plus
+// a constant. Permuting the pieces in each row instead spreads both kinds of reads, and cost
+// the prompt kernel a tenth of its vector instructions for addresses; it serves the short rows.
 template <int PIECES>
-__device__ __forceinline__ int swz(int row) {
-    if constexpr (PIECES == 2)
-        return (row >> 3) & 1;
-    else if constexpr (PIECES == 4)
-        return (row >> 2) & 3;
-    else if constexpr (PIECES == 8)
-        return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-    else
-        return ((row & 3) << 2) | ((row >> 2) & 3);
+__device__ __forceinline__ constexpr int lds_row_bytes() {
+    return PIECES >= 8 ? PIECES * 16 + 16 : PIECES * 16;
 }
-
 template <int PIECES>
 __device__ __forceinline__ int lds_at(int row, int piece) {
-    return row * (PIECES * 16) + ((piece ^ swz<PIECES>(row)) << 4);
+    if constexpr (PIECES == 2)
+        piece ^= (row >> 3) & 1;
+    else if constexpr (PIECES == 4)
+        piece ^= (row >> 2) & 3;
+    return row * lds_row_bytes<PIECES>() + piece * 16;
 }
 
 __device__ __forceinline__ bf16x8 lds_read(const char *p) {
@@ -44,13 +45,20 @@ __device__ __forceinline__ bf16x8 lds_read(const char *p) {
 // chosen so that consecutive accumulator registers hold consecutive rows (see map32).
 template <int PIECES>
 __device__ __forceinline__ bf16x8 lds_read_tr(char *m, int row0, int group, int lane) {
-    const int n = lane & 15, row = row0 + ((lane >> 5) << 3) + (n >> 2);
-    const int piece = group * 4 + ((lane >> 4) & 1) * 2 + (n & 1), half = (n & 2) << 2;
+    const int n = lane & 15, row = ((lane >> 5) << 3) + (n >> 2);
+    const int piece = ((lane >> 4) & 1) * 2 + (n & 1), half = (n & 2) << 2;
     typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(m + lds_at<PIECES>(row, piece) + half));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_ptr)(m + lds_at<PIECES>(row + 4, piece) + half));
+    s16x4 lo, hi;
+    if constexpr (PIECES >= 8) {
+        char *const p = m + lds_at<PIECES>(row, piece) + half + lds_at<PIECES>(row0, group * 4);
+        lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+        hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * lds_row_bytes<PIECES>()));
+    } else {
+        lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_ptr)(m + lds_at<PIECES>(row0 + row, group * 4 + piece) + half));
+        hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_ptr)(m + lds_at<PIECES>(row0 + row + 4, group * 4 + piece) + half));
+    }
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -71,6 +79,10 @@ __device__ __forceinline__ void split2(const float (&x)[8], u32x4 &hi, u32x4 &lo
         rest[2 * i + 1] = x[2 * i + 1] - bf16_hi(hi[i]);
         lo[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
     }
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ f32x16 mfma(u32x4 a, bf16x8 b, f32x16 c) {

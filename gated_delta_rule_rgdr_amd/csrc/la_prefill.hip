@@ -9,8 +9,8 @@
 //
 // Precision: q, k and v are bf16 and enter the products as they are. What is computed enters as a
 // sum of bf16 numbers: the state and the scores as two (2^-16 of each, far below the output's
-// bf16 rounding), the scaled v of the state's update as three (2^-24: the state is kept in fp32
-// over the whole prompt, so its update is not rounded further).
+// bf16 rounding), the scaled v of the state's update as two as well, and as three (2^-24) where the
+// state leaves in fp32 and nothing coarser follows. The state is kept in fp32 over the whole prompt.
 #include "la_mfma.h"
 
 namespace rgdr {
@@ -90,18 +90,19 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
 
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
-// chunk's q, k and v lie in LDS, and three waves compute a 32 x 32 tile of the scores each while
-// the fourth sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
+// chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
+// each; one with two also sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
 template <int DK, int MODE>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8;                 // 16-byte pieces of a q or k row
     constexpr int NR = kChunk * KP / 256;      // of them in each thread's hands
     constexpr int NV = kChunk * 16 / 256;
     constexpr bool kOut = MODE != kSegState;
-    __shared__ __align__(256) char lq[kOut ? kChunk * DK * 2 : 256];
-    __shared__ __align__(256) char lk[kChunk * DK * 2];
-    __shared__ __align__(256) char lv[kChunk * kCols * 2];
-    __shared__ __align__(256) char lp[kOut ? 2 : 1][kOut ? kChunk * kChunk * 2 : 256];
+    constexpr int RQ = lds_row_bytes<KP>(), RV = lds_row_bytes<16>(), RP = lds_row_bytes<8>();
+    __shared__ __align__(256) char lq[kOut ? kChunk * RQ : 256];
+    __shared__ __align__(256) char lk[kChunk * RQ];
+    __shared__ __align__(256) char lv[kChunk * RV];
+    __shared__ __align__(256) char lp[kOut ? 2 : 1][kOut ? kChunk * RP : 256];
     // Of each token of this chunk and the next: the log2 decay sum in two floats, what a later
     // state keeps of it, and what it keeps of the incoming state (with the scale).
     __shared__ __align__(16) float g_hi[2][kChunk], g_lo[2][kChunk], keep[2][kChunk], carry[2][kChunk];
@@ -187,23 +188,34 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     auto chunk_end = [&](int t) { return min(min(t + kChunk, t_end), kOut && t < en.n ? en.n : t_end); };
 
     u32x4 rq[kOut ? NR : 1], rk[NR], rv[NV];
-    // Rows past the chunk repeat its last row: they are not padding's (never read), and their
-    // weights are zero.
-    auto fetch = [&](int t0, int n, int tid) {
+    // One row of a token for each 16 (or D_k / 8) threads. Rows past the chunk repeat its last row:
+    // they are not padding's (never read), and their weights are zero.
+    const uint32_t qt = (uint32_t)a.sq.t * 2, kt = (uint32_t)a.sk.t * 2, vt = (uint32_t)a.sv.t * 2;
+    const uint32_t qk_row = tid / KP, qk_at = tid % KP * 16, v_row = tid / 16;
+    const uint32_t v_at = min(tid % 16, vpieces - 1) * 16;
+    auto fetch = [&](int t0, int n) {
         const char *q = reinterpret_cast<const char *>(gq + t0 * a.sq.t);
         const char *k = reinterpret_cast<const char *>(gk + t0 * a.sk.t);
         const char *v = reinterpret_cast<const char *>(gv + t0 * a.sv.t);
-        const uint32_t qt = (uint32_t)a.sq.t * 2, kt = (uint32_t)a.sk.t * 2, vt = (uint32_t)a.sv.t * 2;
+        if (n == kChunk) {  // a lane's offsets are the same for every set of rows
+            const uint32_t q0 = qk_row * qt + qk_at, k0 = qk_row * kt + qk_at, v0 = v_row * vt + v_at;
 #pragma unroll
-        for (int m = 0; m < NR; ++m) {
-            const uint32_t j = m * 256 + tid, t = min(j / KP, (uint32_t)n - 1), c = j % KP * 16;
-            if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (t * qt + c));
-            rk[m] = *reinterpret_cast<const u32x4 *>(k + (t * kt + c));
-        }
+            for (int m = 0; m < NR; ++m) {
+                if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (uint64_t)(m * (256 / KP)) * qt + q0);
+                rk[m] = *reinterpret_cast<const u32x4 *>(k + (uint64_t)(m * (256 / KP)) * kt + k0);
+            }
 #pragma unroll
-        for (int m = 0; m < NV; ++m) {
-            const uint32_t j = m * 256 + tid, t = min(j / 16, (uint32_t)n - 1);
-            rv[m] = *reinterpret_cast<const u32x4 *>(v + (t * vt + min(j % 16, (uint32_t)vpieces - 1) * 16));
+            for (int m = 0; m < NV; ++m) rv[m] = *reinterpret_cast<const u32x4 *>(v + (uint64_t)(m * 16) * vt + v0);
+        } else {
+#pragma unroll
+            for (int m = 0; m < NR; ++m) {
+                const uint32_t t = min(m * (256 / KP) + qk_row, (uint32_t)n - 1);
+                if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (t * qt + qk_at));
+                rk[m] = *reinterpret_cast<const u32x4 *>(k + (t * kt + qk_at));
+            }
+#pragma unroll
+            for (int m = 0; m < NV; ++m)
+                rv[m] = *reinterpret_cast<const u32x4 *>(v + (min(m * 16 + v_row, (uint32_t)n - 1) * vt + v_at));
         }
     };
     auto stage = [&](int tid) {
@@ -238,9 +250,18 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         if (lane == 0) whole[to] = __builtin_amdgcn_exp2f((float)end);
     };
 
+    // The two tiles above the diagonal that the products of 32 tokens by 32 read: zero for good.
+    if (kOut)
+        for (int j = tid; j < 2 * 2 * 16 * 2; j += 256) {
+            const int plane = j >> 6, half = j >> 5 & 1, row = j >> 1 & 15, piece = j & 1;
+            *reinterpret_cast<u32x4 *>(lp[kOut ? plane : 0] + (half * 32 + row) * RP + (half * 4 + 2 + piece) * 16) =
+                u32x4{0, 0, 0, 0};
+        }
+
+    const bool three = p.state_dtype == RGDR_F32;
     int t0 = t_begin, t1 = chunk_end(t0), buf = 0;
     float g_next = 0.f, seg_keep = 1.f;
-    fetch(t0, t1 - t0, tid);
+    fetch(t0, t1 - t0);
     if (wave == 3) {
         decays(fetch_g(t0, t1 - t0), t1 - t0, 0);
         if (t1 < t_end) g_next = fetch_g(t1, chunk_end(t1) - t1);
@@ -255,40 +276,40 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         const int lane = now & 63, col = lane & 31, hf = lane >> 5;
         stage(now);
         __syncthreads();
-        if (t2 > t1) fetch(t1, t2 - t1, now);
-        if (wave == 3) {
-            if (t2 > t1) {
-                decays(g_next, t2 - t1, buf ^ 1);
-                if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
-            }
-        } else if (kOut) {
-            // scores of tokens t (lanes) and s (registers): tiles (0,0), (1,0) and (1,1)
-            const int tt = wave > 0, st = wave > 1;
-            f32x16 x = {};
+        if (t2 > t1) fetch(t1, t2 - t1);
+        if (kOut) {
+            // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal
 #pragma unroll
-            for (int c = 0; c < DK / 16; ++c)
-                x = mfma(__builtin_bit_cast(u32x4, lds_read(lk + lds_at<KP>(st * 32 + col, c * 2 + hf))),
-                         lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf)), x);
-            const int t = tt * 32 + col;
-            const float th = g_hi[buf][t], tl = g_lo[buf][t];
+            for (int j = 0; j < 3; ++j) {
+                const int i = wave + 4 * j;
+                const int tt = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, st = i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0;
+                if (i > 9 || tt * 16 >= n) continue;
+                const int l16 = lane & 15, l4 = lane >> 4, t = tt * 16 + l16, s = st * 16 + l4 * 4;
+                f32x4 x = {};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int s = st * 32 + m * 8 + hf * 4;
+                for (int c = 0; c < DK / 32; ++c)
+                    x = mfma16(lds_read(lk + lds_at<KP>(st * 16 + l16, c * 4 + l4)),
+                               lds_read(lq + lds_at<KP>(t, c * 4 + l4)), x);
+                const float th = g_hi[buf][t], tl = g_lo[buf][t];
                 const f32x4 sh = *reinterpret_cast<const f32x4 *>(&g_hi[buf][s]);
                 const f32x4 sl = *reinterpret_cast<const f32x4 *>(&g_lo[buf][s]);
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float w = __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) * a.scale;
-                    y[e] = s + e <= t && t < n ? x[m * 4 + e] * w : 0.f;
+                    y[e] = s + e <= t && t < n ? x[e] * w : 0.f;
                 }
                 u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
                 u32x2 lo = {pack_bf16x2(y[0] - bf16_lo(hi[0]), y[1] - bf16_hi(hi[0])),
                             pack_bf16x2(y[2] - bf16_lo(hi[1]), y[3] - bf16_hi(hi[1]))};
-                const int at = lds_at<8>(t, st * 4 + m) + hf * 8;
+                const int at = t * RP + s * 2;
                 *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
                 *reinterpret_cast<u32x2 *>(lp[kOut ? 1 : 0] + at) = lo;
             }
+        }
+        if (wave == 3 && t2 > t1) {
+            decays(g_next, t2 - t1, buf ^ 1);
+            if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
         }
         bf16x8 vf[4];
         f32x16 o[2] = {};
@@ -352,7 +373,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     for (int r = 0; r < 16; ++r) S[it][r] *= d;
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb) {
-                    float x[8], r1[8], r2[8];
+                    float x[8], r1[8];
                     u32x4 hi, lo, lo2;
                     const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
                     const float *w = &keep[buf][kb * 16 + hf * 8];
@@ -362,19 +383,24 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                         x[2 * e + 1] = bf16_hi(v[e]) * w[2 * e + 1];
                     }
                     split2(x, hi, lo, r1);
+                    u32x4 k[DK / 32];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r2[2 * e] = r1[2 * e] - bf16_lo(lo[e]);
-                        r2[2 * e + 1] = r1[2 * e + 1] - bf16_hi(lo[e]);
-                        lo2[e] = pack_bf16x2(r2[2 * e], r2[2 * e + 1]);
+                    for (int it = 0; it < DK / 32; ++it)
+                        k[it] = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, kb * 16, it, lane));
+                    if (three) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            lo2[e] = pack_bf16x2(r1[2 * e] - bf16_lo(lo[e]), r1[2 * e + 1] - bf16_hi(lo[e]));
+#pragma unroll
+                        for (int it = 0; it < DK / 32; ++it)
+                            S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, lo2), S[it]);
                     }
 #pragma unroll
-                    for (int it = 0; it < DK / 32; ++it) {
-                        const u32x4 k = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, kb * 16, it, lane));
-                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, lo2), S[it]);
-                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, lo), S[it]);
-                        S[it] = mfma(k, __builtin_bit_cast(bf16x8, hi), S[it]);
-                    }
+                    for (int it = 0; it < DK / 32; ++it)
+                        S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, lo), S[it]);
+#pragma unroll
+                    for (int it = 0; it < DK / 32; ++it)
+                        S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, hi), S[it]);
                 }
             }
         }
