@@ -297,7 +297,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     for (int c = 0; c < DK / 16; ++c)
         x = mfma(__builtin_bit_cast(u32x4, lds_read(lk + lds_at<KP>(col & 7, c * 2 + hf))),
                  lds_read(lq + lds_at<KP>(col & 7, c * 2 + hf)), x);
-    float y[8], rest[8];
+    float y[8];
     u32x4 p_hi, p_lo;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -306,23 +306,20 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         y[r] = hf ? 0.f : __uint_as_float(sw[0]);
         y[r + 4] = hf ? 0.f : __uint_as_float(sw[1]);
     }
-    split2(y, p_hi, p_lo, rest);
+    split2(y, p_hi, p_lo);
     // values: lanes j, eight tokens in each lane (the upper lanes' have no weight), and the same
     // weighted for the state
     u32x4 vf[CB], v_hi[CB], v_lo[CB], v_lo2[CB];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
         vf[cb] = __builtin_bit_cast(u32x4, lds_read_tr<16>(lv, 0, wave * CB + cb, col));
-        float r1[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float wk = __shfl(wk1, e);
             y[e] = hf ? 0.f : (e & 1 ? bf16_hi(vf[cb][e / 2]) : bf16_lo(vf[cb][e / 2])) * wk;
         }
-        split2(y, v_hi[cb], v_lo[cb], r1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v_lo2[cb][e] = pack_bf16x2(r1[2 * e] - bf16_lo(v_lo[cb][e]), r1[2 * e + 1] - bf16_hi(v_lo[cb][e]));
+        split2(y, v_hi[cb], v_lo[cb]);
+        v_lo2[cb] = split_rest(y, v_lo[cb]);
     }
 
     f32x16 o[CB] = {};
@@ -374,7 +371,10 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
                 }
                 const int pa = lds_at<4>(map32(col), kb * 2 + hf);
                 if constexpr (ST == RGDR_F32) {
-                    split2(s[kb], hi, lo, rest);
+                    float rest[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rest[e] = s[kb][e];
+                    split2(rest, hi, lo);
                     *reinterpret_cast<u32x4 *>(ls[wave][PL - 1] + pa) = lo;
                 } else {
 #pragma unroll
@@ -556,7 +556,8 @@ rgdr_status la_check(LaArgs &a, int max_t, const void *query, const la_strides *
         !la_rows_distinct(a.so, B, H_v, T, D_v))
         return RGDR_ERR_SHAPE;
     // offsets within a chunk of tokens are counted in 32 bits
-    if (T > 1 && (a.sq.t > kMaxTokenStride || a.sk.t > kMaxTokenStride || a.sv.t > kMaxTokenStride))
+    if (T > 1 && (a.sq.t > kMaxTokenStride || a.sk.t > kMaxTokenStride || a.sv.t > kMaxTokenStride ||
+                  a.sg.t > kMaxTokenStride || a.so.t > kMaxTokenStride))
         return RGDR_ERR_SHAPE;
     if (!la_strides_aligned(a.sq, B, H_q, T) || !la_strides_aligned(a.sk, B, H_q, T) ||
         !la_strides_aligned(a.sv, B, H_v, T) || !la_strides_aligned(a.so, B, H_v, T))

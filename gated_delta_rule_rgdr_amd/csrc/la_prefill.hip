@@ -92,15 +92,20 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
 // each; one with two also sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
-template <int DK, int MODE>
+//
+// FULL: D_v is a multiple of 128, so every wave has columns. THREE: the state leaves in fp32. Both are
+// template arguments so that a chunk is a few long stretches of code without branches, in which
+// the products and the vector work around them can be interleaved.
+template <int DK, int MODE, bool FULL, bool THREE>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8;                 // 16-byte pieces of a q or k row
     constexpr int NR = kChunk * KP / 256;      // of them in each thread's hands
     constexpr int NV = kChunk * 16 / 256;
     constexpr bool kOut = MODE != kSegState;
-    constexpr int RQ = lds_row_bytes<KP>(), RV = lds_row_bytes<16>(), RP = lds_row_bytes<8>();
+    constexpr int RQ = lds_row_bytes<KP>(), RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>(),
+                  RP = lds_row_bytes<8>();
     __shared__ __align__(256) char lq[kOut ? kChunk * RQ : 256];
-    __shared__ __align__(256) char lk[kChunk * RQ];
+    __shared__ __align__(256) char lk[kChunk * RK];
     __shared__ __align__(256) char lv[kChunk * RV];
     __shared__ __align__(256) char lp[kOut ? 2 : 1][kOut ? kChunk * RP : 256];
     // Of each token of this chunk and the next: the log2 decay sum in two floats, what a later
@@ -124,8 +129,8 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     if (MODE == kSegState && t_begin + p.seg_len >= en.L) return;  // no later segment needs it
     const int hq = h / a.group, bh = b * a.Hv + h;
     const int col0 = tile * kCols + wave * 32;
-    const bool mine = col0 < a.Dv;  // this wave has columns
-    const int vpieces = min(16, (a.Dv - tile * kCols) / 8);
+    const bool mine = FULL || col0 < a.Dv;  // this wave has columns
+    const int vpieces = FULL ? 16 : min(16, (a.Dv - tile * kCols) / 8);
 
     const uint16_t *gq = a.q + b * a.sq.b + hq * a.sq.h;
     const uint16_t *gk = a.k + b * a.sk.b + hq * a.sk.h;
@@ -221,27 +226,22 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     auto stage = [&](int tid) {
 #pragma unroll
         for (int m = 0; m < NR; ++m) {
-            const int j = m * 256 + tid, at = lds_at<KP>(j / KP, j % KP);
-            if (kOut) *reinterpret_cast<u32x4 *>(lq + at) = rq[m];
-            *reinterpret_cast<u32x4 *>(lk + at) = rk[m];
+            const int j = m * 256 + tid;
+            if (kOut) *reinterpret_cast<u32x4 *>(lq + lds_at<KP>(j / KP, j % KP)) = rq[m];
+            *reinterpret_cast<u32x4 *>(lk + lds_at<KP, kTrPad>(j / KP, j % KP)) = rk[m];
         }
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int j = m * 256 + tid;
-            *reinterpret_cast<u32x4 *>(lv + lds_at<16>(j / 16, j % 16)) = rv[m];
+            *reinterpret_cast<u32x4 *>(lv + lds_at<16, kTrPad>(j / 16, j % 16)) = rv[m];
         }
     };
-    auto fetch_g = [&](int t0, int n) { return gg[(long long)(t0 + min(lane, n - 1)) * a.sg.t]; };
+    const uint32_t g_at = (uint32_t)a.sg.t, out_at = (uint32_t)(lane & 31) * (uint32_t)a.so.t * 2 + (lane >> 5) * 16;
+    auto fetch_g = [&](int t0, int n) { return (gg + (long long)t0 * a.sg.t)[(uint32_t)min(lane, n - 1) * g_at]; };
     // One lane for each token: decay sums of a chunk of n tokens, into buffer `to`.
     auto decays = [&](float x, int n, int to) {
         constexpr double kLog2e = 1.4426950408889634;
-        double G = lane < n ? (double)la_log_decay(x) * kLog2e : 0.0;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const double y = __shfl_up(G, m);
-            if (lane >= m) G += y;
-        }
-        const double end = __shfl(G, 63);
+        const double G = wave_scan(lane < n ? (double)la_log_decay(x) * kLog2e : 0.0), end = wave_last(G);
         const float hi = (float)G;
         g_hi[to][lane] = hi;
         g_lo[to][lane] = (float)(G - (double)hi);
@@ -258,7 +258,6 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 u32x4{0, 0, 0, 0};
         }
 
-    const bool three = p.state_dtype == RGDR_F32;
     int t0 = t_begin, t1 = chunk_end(t0), buf = 0;
     float g_next = 0.f, seg_keep = 1.f;
     fetch(t0, t1 - t0);
@@ -277,19 +276,31 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         stage(now);
         __syncthreads();
         if (t2 > t1) fetch(t1, t2 - t1);
+        if (wave == 3 && t2 > t1) {
+            decays(g_next, t2 - t1, buf ^ 1);
+            if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
+        }
         if (kOut) {
-            // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal
+            // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal: (3,0..3),
+            // (2,0..2), (1,0..1), (0,0). The last two waves' third tile is another wave's.
+            const int l16 = lane & 15, l4 = lane >> 4;
+            f32x4 x[3] = {};
+            int ts[3], ss[3];
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
-                const int i = wave + 4 * j;
-                const int tt = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, st = i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0;
-                if (i > 9 || tt * 16 >= n) continue;
-                const int l16 = lane & 15, l4 = lane >> 4, t = tt * 16 + l16, s = st * 16 + l4 * 4;
-                f32x4 x = {};
+                const int i = min(wave + 4 * j, 9);
+                ts[j] = (i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0) * 16 + l16;
+                ss[j] = (i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0) * 16;
+            }
 #pragma unroll
-                for (int c = 0; c < DK / 32; ++c)
-                    x = mfma16(lds_read(lk + lds_at<KP>(st * 16 + l16, c * 4 + l4)),
-                               lds_read(lq + lds_at<KP>(t, c * 4 + l4)), x);
+            for (int c = 0; c < DK / 32; ++c)
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    x[j] = mfma16(lds_read(lk + lds_at<KP, kTrPad>(ss[j] + l16, c * 4 + l4)),
+                                  lds_read(lq + lds_at<KP>(ts[j], c * 4 + l4)), x[j]);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int t = ts[j], s = ss[j] + l4 * 4;
                 const float th = g_hi[buf][t], tl = g_lo[buf][t];
                 const f32x4 sh = *reinterpret_cast<const f32x4 *>(&g_hi[buf][s]);
                 const f32x4 sl = *reinterpret_cast<const f32x4 *>(&g_lo[buf][s]);
@@ -297,33 +308,30 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float w = __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) * a.scale;
-                    y[e] = s + e <= t && t < n ? x[e] * w : 0.f;
+                    y[e] = s + e <= t && t < n ? x[j][e] * w : 0.f;
                 }
                 u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-                u32x2 lo = {pack_bf16x2(y[0] - bf16_lo(hi[0]), y[1] - bf16_hi(hi[0])),
-                            pack_bf16x2(y[2] - bf16_lo(hi[1]), y[3] - bf16_hi(hi[1]))};
+                bf16_rest(hi[0], y[0], y[1]);
+                bf16_rest(hi[1], y[2], y[3]);
+                u32x2 lo = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
                 const int at = t * RP + s * 2;
                 *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
                 *reinterpret_cast<u32x2 *>(lp[kOut ? 1 : 0] + at) = lo;
             }
         }
-        if (wave == 3 && t2 > t1) {
-            decays(g_next, t2 - t1, buf ^ 1);
-            if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
-        }
         bf16x8 vf[4];
         f32x16 o[2] = {};
         if (mine) {
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16>(lv, kb * 16, wave, lane);
+            for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
             if (kOut) {
 #pragma unroll
                 for (int c = 0; c < DK / 16; ++c) {
-                    float x[8], rest[8];
+                    float x[8];
                     u32x4 hi, lo;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
-                    split2(x, hi, lo, rest);
+                    split2(x, hi, lo);
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
                         const bf16x8 q = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
@@ -353,14 +361,14 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt)
                     if (tt * 32 + col < n) {
-                        uint16_t *row = go + (t0 + tt * 32 + col) * a.so.t + hf * 8;
+                        char *row = reinterpret_cast<char *>(go + (long long)(t0 + tt * 32) * a.so.t) + out_at;
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             u32x4 y;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 y[e] = pack_bf16x2(o[tt][m * 8 + 2 * e], o[tt][m * 8 + 2 * e + 1]);
-                            *reinterpret_cast<u32x4 *>(row + m * 16) = y;
+                            *reinterpret_cast<u32x4 *>(row + m * 32) = y;
                         }
                     }
             }
@@ -373,7 +381,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     for (int r = 0; r < 16; ++r) S[it][r] *= d;
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb) {
-                    float x[8], r1[8];
+                    float x[8];
                     u32x4 hi, lo, lo2;
                     const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
                     const float *w = &keep[buf][kb * 16 + hf * 8];
@@ -382,15 +390,13 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                         x[2 * e] = bf16_lo(v[e]) * w[2 * e];
                         x[2 * e + 1] = bf16_hi(v[e]) * w[2 * e + 1];
                     }
-                    split2(x, hi, lo, r1);
+                    split2(x, hi, lo);
                     u32x4 k[DK / 32];
 #pragma unroll
                     for (int it = 0; it < DK / 32; ++it)
-                        k[it] = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, kb * 16, it, lane));
-                    if (three) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            lo2[e] = pack_bf16x2(r1[2 * e] - bf16_lo(lo[e]), r1[2 * e + 1] - bf16_hi(lo[e]));
+                        k[it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
+                    if constexpr (THREE) {
+                        lo2 = split_rest(x, lo);
 #pragma unroll
                         for (int it = 0; it < DK / 32; ++it)
                             S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, lo2), S[it]);
@@ -509,25 +515,33 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
     return true;
 }
 
-template <int DK>
+template <int DK, bool FULL, bool THREE>
 static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream) {
     p.tiles = (a.Dv + kCols - 1) / kCols;
     const unsigned items = (unsigned)((long long)a.B * a.Hv * p.tiles);
     const dim3 block(256);
     if (p.nseg == 1) {
-        hipLaunchKernelGGL((la_chunk_kernel<DK, kWhole>), dim3(items), block, 0, stream, a, p);
+        hipLaunchKernelGGL((la_chunk_kernel<DK, kWhole, FULL, THREE>), dim3(items), block, 0, stream, a, p);
         return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
     }
     const unsigned scan = (unsigned)(((long long)a.B * a.Hv * (a.Dv * DK / 4) + 255) / 256);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState>), dim3(items * p.nseg), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState, FULL, THREE>), dim3(items * p.nseg), block, 0, stream, a, p);
     if (p.state_dtype == RGDR_F32)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_F32>, dim3(scan), block, 0, stream, a, p, DK);
     else if (p.state_dtype == RGDR_BF16)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_BF16>, dim3(scan), block, 0, stream, a, p, DK);
     else
         hipLaunchKernelGGL(la_scan_kernel<RGDR_MXI8>, dim3(scan), block, 0, stream, a, p, DK);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut>), dim3(items * p.nseg), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut, FULL, THREE>), dim3(items * p.nseg), block, 0, stream, a, p);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+}
+
+template <int DK>
+static rgdr_status launch_prefill_dk(const LaArgs &a, const LaPlan &p, hipStream_t stream) {
+    const bool three = p.state_dtype == RGDR_F32;
+    if (a.Dv % kCols == 0)
+        return three ? launch_prefill<DK, true, true>(a, p, stream) : launch_prefill<DK, true, false>(a, p, stream);
+    return three ? launch_prefill<DK, false, true>(a, p, stream) : launch_prefill<DK, false, false>(a, p, stream);
 }
 
 }  // namespace rgdr
@@ -577,7 +591,7 @@ extern "C" rgdr_status la_prefill(const void *query, const la_strides *query_str
         p.seg_state = static_cast<float *>(workspace);
         p.seg_decay = p.seg_state + (size_t)p.nseg * B * H_v * D_k * D_v;
     }
-    if (D_k == 64) return launch_prefill<64>(a, p, stream);
-    if (D_k == 128) return launch_prefill<128>(a, p, stream);
-    return launch_prefill<256>(a, p, stream);
+    if (D_k == 64) return launch_prefill_dk<64>(a, p, stream);
+    if (D_k == 128) return launch_prefill_dk<128>(a, p, stream);
+    return launch_prefill_dk<256>(a, p, stream);
 }

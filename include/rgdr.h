@@ -373,8 +373,8 @@ typedef struct { int64_t b, h, t; } la_strides;
  *   *_strides     element strides of the four operands, or NULL for a contiguous one; 0 repeats
  *                 an operand along that axis (a per-head decay [H_v] has strides {0, 1, 0}).
  *                 Query, key and value rows start at multiples of 8 elements, their bases are
- *                 16-byte aligned. Strides are not negative, and those of their
- *                 tokens at most 2^24.
+ *                 16-byte aligned. Strides are not negative, and those of the
+ *                 tokens (out's too) at most 2^24.
  *   state_pool    [N_slots, H_v, D_k, D_v] of state_dtype: RGDR_F32, RGDR_BF16 or RGDR_MXI8
  *                 (int8 codes). 16-byte aligned.
  *   state_scales  RGDR_MXI8: uint8 [N_slots, H_v, D_k, D_v / 32], 16-byte aligned; else unused
