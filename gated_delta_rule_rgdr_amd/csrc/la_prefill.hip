@@ -292,22 +292,40 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 ts[j] = (i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0) * 16 + l16;
                 ss[j] = (i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0) * 16;
             }
+            bf16x8 kf[2][3], qf[2][3];
+            auto load = [&](int c) {
 #pragma unroll
-            for (int c = 0; c < DK / 32; ++c)
+                for (int j = 0; j < 3; ++j) {
+                    kf[c & 1][j] = lds_read(lk + lds_at<KP, kTrPad>(ss[j] + l16, c * 4 + l4));
+                    qf[c & 1][j] = lds_read(lq + lds_at<KP>(ts[j], c * 4 + l4));
+                }
+            };
+            load(0);
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
-                    x[j] = mfma16(lds_read(lk + lds_at<KP, kTrPad>(ss[j] + l16, c * 4 + l4)),
-                                  lds_read(lq + lds_at<KP>(ts[j], c * 4 + l4)), x[j]);
+            for (int c = 0; c < DK / 32; ++c) {
+                if (c + 1 < DK / 32) load(c + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) x[j] = mfma16(kf[c & 1][j], qf[c & 1][j], x[j]);
+            }
+            float th[3], tl[3];
+            f32x4 sh[3], sl[3];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                th[j] = g_hi[buf][ts[j]];
+                tl[j] = g_lo[buf][ts[j]];
+                sh[j] = *reinterpret_cast<const f32x4 *>(&g_hi[buf][ss[j] + l4 * 4]);
+                sl[j] = *reinterpret_cast<const f32x4 *>(&g_lo[buf][ss[j] + l4 * 4]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
                 const int t = ts[j], s = ss[j] + l4 * 4;
-                const float th = g_hi[buf][t], tl = g_lo[buf][t];
-                const f32x4 sh = *reinterpret_cast<const f32x4 *>(&g_hi[buf][s]);
-                const f32x4 sl = *reinterpret_cast<const f32x4 *>(&g_lo[buf][s]);
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float w = __builtin_amdgcn_exp2f((th - sh[e]) + (tl - sl[e])) * a.scale;
+                    float w = __builtin_amdgcn_exp2f((th[j] - sh[j][e]) + (tl[j] - sl[j][e])) * a.scale;
+                    asm volatile("" : "+v"(w));  // formed for every lane: no branch around it
                     y[e] = s + e <= t && t < n ? x[j][e] * w : 0.f;
                 }
                 u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
@@ -325,19 +343,25 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
             if (kOut) {
+                bf16x8 qf[2][2];
+                auto load = [&](int c) {
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) qf[c & 1][tt] = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
+                };
+                load(0);
 #pragma unroll
                 for (int c = 0; c < DK / 16; ++c) {
+                    if (c + 1 < DK / 16) load(c + 1);
+                    __builtin_amdgcn_sched_barrier(0);
                     float x[8];
                     u32x4 hi, lo;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
                     split2(x, hi, lo);
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) {
-                        const bf16x8 q = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
-                        o[tt] = mfma(hi, q, o[tt]);
-                        o[tt] = mfma(lo, q, o[tt]);
-                    }
+                    for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi, qf[c & 1][tt], o[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo, qf[c & 1][tt], o[tt]);
                 }
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) {
@@ -350,14 +374,27 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         if (kOut) __syncthreads();
         if (mine) {
             if (kOut) {
+                // (second tokens, s block 3), (2), then both halves for blocks 1 and 0
+                bf16x8 pf[2][4];
+                auto load = [&](int kb) {
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                    for (int kb = 0; kb < 2 + 2 * tt; ++kb)
+                    for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
 #pragma unroll
                         for (int pl = 0; pl < 2; ++pl)
-                            o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]),
-                                         lds_read(lp[kOut ? pl : 0] + lds_at<8>(tt * 32 + col, kb * 2 + hf)), o[tt]);
+                            pf[kb & 1][tt * 2 + pl] =
+                                lds_read(lp[kOut ? pl : 0] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
+                };
+                load(3);
+#pragma unroll
+                for (int kb = 3; kb >= 0; --kb) {
+                    if (kb > 0) load(kb - 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+                        for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
+                            o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 2 + pl], o[tt]);
+                }
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt)
                     if (tt * 32 + col < n) {
@@ -375,38 +412,47 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
             if (t1 < t_end || MODE == kSegState || t1 == en.n) {
                 const float d = whole[buf];
                 if (MODE == kSegState) seg_keep *= d;
+                u32x4 kf[2][DK / 32];
+                f32x4 wf[2][2];
+                auto load = [&](int kb) {
+#pragma unroll
+                    for (int it = 0; it < DK / 32; ++it)
+                        kf[kb & 1][it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        wf[kb & 1][i] = *reinterpret_cast<const f32x4 *>(&keep[buf][kb * 16 + hf * 8 + i * 4]);
+                };
+                load(0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int it = 0; it < DK / 32; ++it)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) S[it][r] *= d;
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb) {
+                    if (kb < 3) load(kb + 1);
+                    __builtin_amdgcn_sched_barrier(0);
                     float x[8];
                     u32x4 hi, lo, lo2;
                     const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
-                    const float *w = &keep[buf][kb * 16 + hf * 8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = bf16_lo(v[e]) * w[2 * e];
-                        x[2 * e + 1] = bf16_hi(v[e]) * w[2 * e + 1];
+                        x[2 * e] = bf16_lo(v[e]) * wf[kb & 1][e / 2][2 * e % 4];
+                        x[2 * e + 1] = bf16_hi(v[e]) * wf[kb & 1][e / 2][2 * e % 4 + 1];
                     }
                     split2(x, hi, lo);
-                    u32x4 k[DK / 32];
-#pragma unroll
-                    for (int it = 0; it < DK / 32; ++it)
-                        k[it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
                     if constexpr (THREE) {
                         lo2 = split_rest(x, lo);
 #pragma unroll
                         for (int it = 0; it < DK / 32; ++it)
-                            S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, lo2), S[it]);
+                            S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2), S[it]);
                     }
 #pragma unroll
                     for (int it = 0; it < DK / 32; ++it)
-                        S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, lo), S[it]);
+                        S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo), S[it]);
 #pragma unroll
                     for (int it = 0; it < DK / 32; ++it)
-                        S[it] = mfma(k[it], __builtin_bit_cast(bf16x8, hi), S[it]);
+                        S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi), S[it]);
                 }
             }
         }
