@@ -223,18 +223,17 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 rv[m] = *reinterpret_cast<const u32x4 *>(v + (min(m * 16 + v_row, (uint32_t)n - 1) * vt + v_at));
         }
     };
-    auto stage = [&](int tid) {
+    const int q_to = lds_at<KP>(tid / KP, tid % KP), k_to = lds_at<KP, kTrPad>(tid / KP, tid % KP);
+    const int v_to = lds_at<16, kTrPad>(tid / 16, tid % 16);
+    auto stage = [&]() {
 #pragma unroll
         for (int m = 0; m < NR; ++m) {
-            const int j = m * 256 + tid;
-            if (kOut) *reinterpret_cast<u32x4 *>(lq + lds_at<KP>(j / KP, j % KP)) = rq[m];
-            *reinterpret_cast<u32x4 *>(lk + lds_at<KP, kTrPad>(j / KP, j % KP)) = rk[m];
+            const int set = m * (256 / KP);  // rows of one set of pieces
+            if (kOut) *reinterpret_cast<u32x4 *>(lq + q_to + set * RQ) = rq[m];
+            *reinterpret_cast<u32x4 *>(lk + k_to + set * RK) = rk[m];
         }
 #pragma unroll
-        for (int m = 0; m < NV; ++m) {
-            const int j = m * 256 + tid;
-            *reinterpret_cast<u32x4 *>(lv + lds_at<16, kTrPad>(j / 16, j % 16)) = rv[m];
-        }
+        for (int m = 0; m < NV; ++m) *reinterpret_cast<u32x4 *>(lv + v_to + m * 16 * RV) = rv[m];
     };
     const uint32_t g_at = (uint32_t)a.sg.t, out_at = (uint32_t)(lane & 31) * (uint32_t)a.so.t * 2 + (lane >> 5) * 16;
     auto fetch_g = [&](int t0, int n) { return (gg + (long long)t0 * a.sg.t)[(uint32_t)min(lane, n - 1) * g_at]; };
@@ -273,7 +272,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         int now = tid;
         asm volatile("" : "+v"(now));
         const int lane = now & 63, col = lane & 31, hf = lane >> 5;
-        stage(now);
+        stage();
         __syncthreads();
         if (t2 > t1) fetch(t1, t2 - t1);
         if (wave == 3 && t2 > t1) {
@@ -326,7 +325,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 for (int e = 0; e < 4; ++e) {
                     float w = __builtin_amdgcn_exp2f((th[j] - sh[j][e]) + (tl[j] - sl[j][e])) * a.scale;
                     asm volatile("" : "+v"(w));  // formed for every lane: no branch around it
-                    y[e] = s + e <= t && t < n ? x[j][e] * w : 0.f;
+                    y[e] = s + e <= t ? x[j][e] * w : 0.f;  // columns t past the chunk are not stored
                 }
                 u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
                 bf16_rest(hi[0], y[0], y[1]);
