@@ -17,6 +17,7 @@ namespace rgdr {
 
 constexpr int kLaMaxPrompt = 65536;
 constexpr int kChunk = 64;    // tokens
+constexpr int kXcds = 8;      // of the device, each with its own L2
 constexpr int kCols = 128;    // columns of one workgroup: 32 for each of its 4 waves
 
 struct LaPlan {
@@ -88,6 +89,44 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
         }
 }
 
+// Which (entry, segment, value head, columns) a workgroup works on. A unit is what shares a query/key
+// head: its value heads and their columns, which run on one XCD, so that q and k meet in its
+// L2. Units go round the XCDs (workgroup ids do), those of the longest entries first: with
+// ragged lengths every XCD, and every compute unit's two places, then get long and short ones.
+// (B=16, H=16/32, D=128, lengths from 0 to 1024: XCD_UNSORTED us with an XCD's units contiguous.)
+struct LaItem {
+    int b, seg, h, tile;
+    bool live;
+};
+
+__device__ __forceinline__ int entry_of_rank(const LaArgs &a, int rank) {
+    if (!a.lens || a.B < 2 || a.B > 64) return rank;
+    const int lane = threadIdx.x & 63;
+    const int L = lane < a.B ? min(max(a.lens[lane], 0), a.T) : -1;
+    int r = 0;  // of this lane's entry: how many are longer, or as long and before it
+    for (int j = 0; j < a.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(L, j);
+        r += other > L || (other == L && j < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < a.B && r == rank));
+}
+
+template <bool SEGMENTS>
+__device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
+    const int per = a.group * p.tiles, local = blockIdx.x / kXcds;
+    int unit = local / per * kXcds + blockIdx.x % kXcds;
+    LaItem m;
+    m.tile = local % per % p.tiles;
+    const int in_group = local % per / p.tiles;
+    m.live = unit < a.B * a.Hq * (SEGMENTS ? p.nseg : 1);
+    const int hq = unit % a.Hq;
+    unit /= a.Hq;
+    m.seg = SEGMENTS ? unit % p.nseg : 0;
+    m.b = entry_of_rank(a, m.live ? (SEGMENTS ? unit / p.nseg : unit) : 0);
+    m.h = hq * a.group + in_group;
+    return m;
+}
+
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
@@ -115,13 +154,9 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int item = xcd_item(blockIdx.x, gridDim.x);
-    const int tile = item % p.tiles;
-    item /= p.tiles;
-    const int h = item % a.Hv;
-    item /= a.Hv;
-    const int seg = MODE == kWhole ? 0 : item % p.nseg;
-    const int b = MODE == kWhole ? item : item / p.nseg;
+    const LaItem item = la_item<MODE != kWhole>(a, p);
+    if (!item.live) return;
+    const int tile = item.tile, h = item.h, seg = item.seg, b = item.b;
     const LaEntry en = la_entry(a, b);
     const int t_begin = MODE == kWhole ? 0 : seg * p.seg_len;
     const int t_stop = MODE == kWhole ? a.T : min(a.T, t_begin + p.seg_len);
@@ -563,21 +598,24 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
 template <int DK, bool FULL, bool THREE>
 static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream) {
     p.tiles = (a.Dv + kCols - 1) / kCols;
-    const unsigned items = (unsigned)((long long)a.B * a.Hv * p.tiles);
+    // whole rounds of units over the XCDs
+    const long long units = ((long long)a.B * a.Hq * p.nseg + kXcds - 1) / kXcds * kXcds;
+    if (units * a.group * p.tiles > 0x7FFFFFFF) return RGDR_ERR_SHAPE;
+    const unsigned items = (unsigned)(units * a.group * p.tiles);
     const dim3 block(256);
     if (p.nseg == 1) {
         hipLaunchKernelGGL((la_chunk_kernel<DK, kWhole, FULL, THREE>), dim3(items), block, 0, stream, a, p);
         return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
     }
     const unsigned scan = (unsigned)(((long long)a.B * a.Hv * (a.Dv * DK / 4) + 255) / 256);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState, FULL, THREE>), dim3(items * p.nseg), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState, FULL, THREE>), dim3(items), block, 0, stream, a, p);
     if (p.state_dtype == RGDR_F32)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_F32>, dim3(scan), block, 0, stream, a, p, DK);
     else if (p.state_dtype == RGDR_BF16)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_BF16>, dim3(scan), block, 0, stream, a, p, DK);
     else
         hipLaunchKernelGGL(la_scan_kernel<RGDR_MXI8>, dim3(scan), block, 0, stream, a, p, DK);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut, FULL, THREE>), dim3(items * p.nseg), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut, FULL, THREE>), dim3(items), block, 0, stream, a, p);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
