@@ -26,8 +26,6 @@ struct LaPlan {
     float *seg_decay;  // [nseg][B*H_v]
 };
 
-enum { kWhole = 0, kSegState = 1, kSegOut = 2 };
-
 // One wave's 32 columns of a state, D_k rows: register r = 8 kb + e of tile `it` is row
 // 32 it + 16 kb + 8 (lane / 32) + e, column map32(lane % 32).
 // `base`: the element of the wave's first column in the state's first row.
@@ -93,7 +91,8 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
 // head: its value heads and their columns, which run on one XCD, so that q and k meet in its
 // L2. Units go round the XCDs (workgroup ids do), those of the longest entries first: with
 // ragged lengths every XCD, and every compute unit's two places, then get long and short ones.
-// (B=16, H=16/32, D=128, lengths from 0 to 1024: XCD_UNSORTED us with an XCD's units contiguous.)
+// (B=16, H=16/32, D=128, lengths from 0 to 1024: 101.5 us, against 108.2 with each XCD's units
+// contiguous.)
 struct LaItem {
     int b, seg, h, tile;
     bool live;
@@ -127,6 +126,148 @@ __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
     return m;
 }
 
+// S += sum_s k_s (w_s v_s)^T over the 64 tokens of a chunk: k from LDS, v's operands in registers, one
+// weight for each token in LDS.
+template <int DK, bool THREE>
+__device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const bf16x8 (&vf)[4],
+                                          const float *weight, int lane) {
+    constexpr int KP = DK / 8;
+    u32x4 kf[2][DK / 32];
+    f32x4 wf[2][2];
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int it = 0; it < DK / 32; ++it)
+            kf[kb & 1][it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            wf[kb & 1][i] = *reinterpret_cast<const f32x4 *>(weight + kb * 16 + (lane >> 5) * 8 + i * 4);
+    };
+    load(0);
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+        if (kb < 3) load(kb + 1);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay a step ahead of the products
+        float x[8];
+        u32x4 hi, lo;
+        const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16_lo(v[e]) * wf[kb & 1][e / 2][2 * e % 4];
+            x[2 * e + 1] = bf16_hi(v[e]) * wf[kb & 1][e / 2][2 * e % 4 + 1];
+        }
+        split2(x, hi, lo);
+        if constexpr (THREE) {
+            const u32x4 lo2 = split_rest(x, lo);
+#pragma unroll
+            for (int it = 0; it < DK / 32; ++it)
+                S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2), S[it]);
+        }
+#pragma unroll
+        for (int it = 0; it < DK / 32; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo), S[it]);
+#pragma unroll
+        for (int it = 0; it < DK / 32; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi), S[it]);
+    }
+}
+
+// What one segment adds to the state behind it, from a zero state, into the workspace: the first pass
+// over a long prompt. Its chunks are taken from the last to the first, each token weighted by the
+// decay from it to the segment's end, so nothing is rescaled in between. A segment that another one
+// of the entry follows is full. Bound: k and v once more; two chunks are in flight.
+template <int DK, bool FULL, bool THREE>
+__global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(const LaArgs a, const LaPlan p) {
+    constexpr int KP = DK / 8, NR = kChunk * KP / 256, NV = kChunk * 16 / 256;
+    constexpr int RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>();
+    __shared__ __align__(256) char lk[kChunk * RK], lv[kChunk * RV];
+    __shared__ __align__(16) float keep[2][kChunk];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const LaItem item = la_item<true>(a, p);
+    if (!item.live) return;
+    const int tile = item.tile, h = item.h, seg = item.seg, b = item.b;
+    const LaEntry en = la_entry(a, b);
+    const int t_begin = seg * p.seg_len;
+    if (!en.state || t_begin + p.seg_len >= en.L) return;  // no later segment needs it
+    const int bh = b * a.Hv + h;
+    const bool mine = FULL || tile * kCols + wave * 32 < a.Dv;  // this wave has columns
+    const int vpieces = FULL ? 16 : min(16, (a.Dv - tile * kCols) / 8);
+    const uint16_t *gk = a.k + b * a.sk.b + h / a.group * a.sk.h + t_begin * a.sk.t;
+    const uint16_t *gv = a.v + b * a.sv.b + h * a.sv.h + tile * kCols + t_begin * a.sv.t;
+    const float *gg = a.g + b * a.sg.b + h * a.sg.h + t_begin * a.sg.t;
+    const uint32_t kt = (uint32_t)a.sk.t * 2, vt = (uint32_t)a.sv.t * 2, g_at = lane * (uint32_t)a.sg.t;
+    const uint32_t k0 = tid / KP * kt + tid % KP * 16, v0 = tid / 16 * vt + min(tid % 16, vpieces - 1) * 16;
+    const int k_to = lds_at<KP, kTrPad>(tid / KP, tid % KP), v_to = lds_at<16, kTrPad>(tid / 16, tid % 16);
+
+    f32x16 S[DK / 32];
+#pragma unroll
+    for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[it][r] = 0.f;
+
+    u32x4 rk[2][NR], rv[2][NV];
+    auto fetch = [&](u32x4 (&fk)[NR], u32x4 (&fv)[NV], int c) {
+        const char *k = reinterpret_cast<const char *>(gk) + (uint64_t)(c * kChunk) * kt;
+        const char *v = reinterpret_cast<const char *>(gv) + (uint64_t)(c * kChunk) * vt;
+#pragma unroll
+        for (int m = 0; m < NR; ++m) fk[m] = *reinterpret_cast<const u32x4 *>(k + (uint64_t)(m * (256 / KP)) * kt + k0);
+#pragma unroll
+        for (int m = 0; m < NV; ++m) fv[m] = *reinterpret_cast<const u32x4 *>(v + (uint64_t)(m * 16) * vt + v0);
+    };
+    auto fetch_g = [&](int c) { return (gg + (long long)(c * kChunk) * a.sg.t)[g_at]; };
+    double behind = 0.0;  // wave 3: the log2 decay from the chunk's end to the segment's
+    auto weights = [&](float g, int to) {
+        constexpr double kLog2e = 1.4426950408889634;
+        const double G = wave_scan((double)la_log_decay(g) * kLog2e), end = wave_last(G);
+        keep[to][lane] = __builtin_amdgcn_exp2f((float)(behind + (end - G)));
+        behind += end;
+    };
+
+    int c = p.seg_len / kChunk - 1, buf = 0;
+    float g_next = 0.f;
+    fetch(rk[0], rv[0], c);
+    if (c > 0) fetch(rk[1], rv[1], c - 1);
+    if (wave == 3) {
+        weights(fetch_g(c), 0);
+        if (c > 0) g_next = fetch_g(c - 1);
+    }
+    auto step = [&](u32x4 (&fk)[NR], u32x4 (&fv)[NV]) {
+#pragma unroll
+        for (int m = 0; m < NR; ++m) *reinterpret_cast<u32x4 *>(lk + k_to + m * (256 / KP) * RK) = fk[m];
+#pragma unroll
+        for (int m = 0; m < NV; ++m) *reinterpret_cast<u32x4 *>(lv + v_to + m * 16 * RV) = fv[m];
+        __syncthreads();
+        if (c > 1) fetch(fk, fv, c - 2);
+        if (wave == 3 && c > 0) {
+            weights(g_next, buf ^ 1);
+            if (c > 1) g_next = fetch_g(c - 2);
+        }
+        if (mine) {
+            bf16x8 vf[4];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
+            add_chunk<DK, THREE>(S, lk, vf, keep[buf], lane);
+        }
+        __syncthreads();
+        buf ^= 1;
+    };
+    while (true) {
+        step(rk[0], rv[0]);
+        if (--c < 0) break;
+        step(rk[1], rv[1]);
+        if (--c < 0) break;
+    }
+    if (mine) {
+        float *const ws = p.seg_state + (((long long)seg * a.B * a.Hv + bh) * (a.Dv / 32) + tile * 4 + wave) * (DK * 32);
+#pragma unroll
+        for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                *reinterpret_cast<f32x4 *>(ws + ((it * 4 + m) * 64 + lane) * 4) =
+                    f32x4{S[it][m * 4], S[it][m * 4 + 1], S[it][m * 4 + 2], S[it][m * 4 + 3]};
+    }
+    if (wave == 3 && tile == 0 && lane == 0)
+        p.seg_decay[(long long)seg * a.B * a.Hv + bh] = __builtin_amdgcn_exp2f((float)behind);
+}
+
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
@@ -135,18 +276,17 @@ __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
 // FULL: D_v is a multiple of 128, so every wave has columns. THREE: the state leaves in fp32. Both are
 // template arguments so that a chunk is a few long stretches of code without branches, in which
 // the products and the vector work around them can be interleaved.
-template <int DK, int MODE, bool FULL, bool THREE>
+template <int DK, bool SEGMENTS, bool FULL, bool THREE>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8;                 // 16-byte pieces of a q or k row
     constexpr int NR = kChunk * KP / 256;      // of them in each thread's hands
     constexpr int NV = kChunk * 16 / 256;
-    constexpr bool kOut = MODE != kSegState;
     constexpr int RQ = lds_row_bytes<KP>(), RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>(),
                   RP = lds_row_bytes<8>();
-    __shared__ __align__(256) char lq[kOut ? kChunk * RQ : 256];
+    __shared__ __align__(256) char lq[kChunk * RQ];
     __shared__ __align__(256) char lk[kChunk * RK];
     __shared__ __align__(256) char lv[kChunk * RV];
-    __shared__ __align__(256) char lp[kOut ? 2 : 1][kOut ? kChunk * RP : 256];
+    __shared__ __align__(256) char lp[2][kChunk * RP];
     // Of each token of this chunk and the next: the log2 decay sum in two floats, what a later
     // state keeps of it, and what it keeps of the incoming state (with the scale).
     __shared__ __align__(16) float g_hi[2][kChunk], g_lo[2][kChunk], keep[2][kChunk], carry[2][kChunk];
@@ -154,14 +294,13 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const LaItem item = la_item<MODE != kWhole>(a, p);
+    const LaItem item = la_item<SEGMENTS>(a, p);
     if (!item.live) return;
     const int tile = item.tile, h = item.h, seg = item.seg, b = item.b;
     const LaEntry en = la_entry(a, b);
-    const int t_begin = MODE == kWhole ? 0 : seg * p.seg_len;
-    const int t_stop = MODE == kWhole ? a.T : min(a.T, t_begin + p.seg_len);
+    const int t_begin = SEGMENTS ? seg * p.seg_len : 0;
+    const int t_stop = SEGMENTS ? min(a.T, t_begin + p.seg_len) : a.T;
     const int t_end = min(en.L, t_stop);
-    if (MODE == kSegState && t_begin + p.seg_len >= en.L) return;  // no later segment needs it
     const int hq = h / a.group, bh = b * a.Hv + h;
     const int col0 = tile * kCols + wave * 32;
     const bool mine = FULL || col0 < a.Dv;  // this wave has columns
@@ -174,29 +313,21 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     uint16_t *go = a.out + b * a.so.b + h * a.so.h + col0;
 
     // rows of tokens past the entry's length
-    if (kOut) {
+    {
         const int from = max(t_begin, t_end);
         for (int j = tid; j < (t_stop - from) * vpieces; j += 256)
             *reinterpret_cast<u32x4 *>(a.out + b * a.so.b + h * a.so.h + tile * kCols +
                                        (from + j / vpieces) * a.so.t + (j % vpieces) * 8) = u32x4{0, 0, 0, 0};
     }
     if (!en.state) return;
-    if (t_begin >= t_end && !(kOut && t_begin == 0)) return;
+    if (t_begin >= t_end && t_begin != 0) return;
 
     f32x16 S[DK / 32];
     const long long base = ((long long)__builtin_amdgcn_readfirstlane(en.slot) * a.Hv + h) * DK * a.Dv + col0;
-    float *const ws = MODE == kWhole ? nullptr
-                                     : p.seg_state + (((long long)seg * a.B * a.Hv + bh) * (a.Dv / 32) +
-                                                      tile * 4 + wave) * (DK * 32);
     if (mine) {
-        if (MODE == kWhole) {
-            if (p.state_dtype == RGDR_F32)
-                load_state<DK, RGDR_F32>(S, a.pool, a.scales, base, a.Dv, lane);
-            else if (p.state_dtype == RGDR_BF16)
-                load_state<DK, RGDR_BF16>(S, a.pool, a.scales, base, a.Dv, lane);
-            else
-                load_state<DK, RGDR_MXI8>(S, a.pool, a.scales, base, a.Dv, lane);
-        } else if (MODE == kSegOut) {
+        if constexpr (SEGMENTS) {
+            const float *const ws =
+                p.seg_state + (((long long)seg * a.B * a.Hv + bh) * (a.Dv / 32) + tile * 4 + wave) * (DK * 32);
 #pragma unroll
             for (int it = 0; it < DK / 32; ++it)
 #pragma unroll
@@ -205,11 +336,12 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) S[it][m * 4 + e] = x[e];
                 }
+        } else if (p.state_dtype == RGDR_F32) {
+            load_state<DK, RGDR_F32>(S, a.pool, a.scales, base, a.Dv, lane);
+        } else if (p.state_dtype == RGDR_BF16) {
+            load_state<DK, RGDR_BF16>(S, a.pool, a.scales, base, a.Dv, lane);
         } else {
-#pragma unroll
-            for (int it = 0; it < DK / 32; ++it)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[it][r] = 0.f;
+            load_state<DK, RGDR_MXI8>(S, a.pool, a.scales, base, a.Dv, lane);
         }
     }
     auto commit = [&]() {
@@ -221,13 +353,13 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         else
             store_state<DK, RGDR_MXI8>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
     };
-    if (kOut && t_begin == 0 && en.n == 0) commit();
+    if (t_begin == 0 && en.n == 0) commit();
     if (t_begin >= t_end) return;
 
     // A chunk ends after 64 tokens, at the accepted count (whose state is committed) or at the end.
-    auto chunk_end = [&](int t) { return min(min(t + kChunk, t_end), kOut && t < en.n ? en.n : t_end); };
+    auto chunk_end = [&](int t) { return min(min(t + kChunk, t_end), t < en.n ? en.n : t_end); };
 
-    u32x4 rq[kOut ? NR : 1], rk[NR], rv[NV];
+    u32x4 rq[NR], rk[NR], rv[NV];
     // One row of a token for each 16 (or D_k / 8) threads. Rows past the chunk repeat its last row:
     // they are not padding's (never read), and their weights are zero.
     const uint32_t qt = (uint32_t)a.sq.t * 2, kt = (uint32_t)a.sk.t * 2, vt = (uint32_t)a.sv.t * 2;
@@ -241,7 +373,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
             const uint32_t q0 = qk_row * qt + qk_at, k0 = qk_row * kt + qk_at, v0 = v_row * vt + v_at;
 #pragma unroll
             for (int m = 0; m < NR; ++m) {
-                if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (uint64_t)(m * (256 / KP)) * qt + q0);
+                rq[m] = *reinterpret_cast<const u32x4 *>(q + (uint64_t)(m * (256 / KP)) * qt + q0);
                 rk[m] = *reinterpret_cast<const u32x4 *>(k + (uint64_t)(m * (256 / KP)) * kt + k0);
             }
 #pragma unroll
@@ -250,7 +382,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
             for (int m = 0; m < NR; ++m) {
                 const uint32_t t = min(m * (256 / KP) + qk_row, (uint32_t)n - 1);
-                if (kOut) rq[m] = *reinterpret_cast<const u32x4 *>(q + (t * qt + qk_at));
+                rq[m] = *reinterpret_cast<const u32x4 *>(q + (t * qt + qk_at));
                 rk[m] = *reinterpret_cast<const u32x4 *>(k + (t * kt + qk_at));
             }
 #pragma unroll
@@ -264,7 +396,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
         for (int m = 0; m < NR; ++m) {
             const int set = m * (256 / KP);  // rows of one set of pieces
-            if (kOut) *reinterpret_cast<u32x4 *>(lq + q_to + set * RQ) = rq[m];
+            *reinterpret_cast<u32x4 *>(lq + q_to + set * RQ) = rq[m];
             *reinterpret_cast<u32x4 *>(lk + k_to + set * RK) = rk[m];
         }
 #pragma unroll
@@ -285,15 +417,14 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     };
 
     // The two tiles above the diagonal that the products of 32 tokens by 32 read: zero for good.
-    if (kOut)
-        for (int j = tid; j < 2 * 2 * 16 * 2; j += 256) {
-            const int plane = j >> 6, half = j >> 5 & 1, row = j >> 1 & 15, piece = j & 1;
-            *reinterpret_cast<u32x4 *>(lp[kOut ? plane : 0] + (half * 32 + row) * RP + (half * 4 + 2 + piece) * 16) =
-                u32x4{0, 0, 0, 0};
-        }
+    for (int j = tid; j < 2 * 2 * 16 * 2; j += 256) {
+        const int plane = j >> 6, half = j >> 5 & 1, row = j >> 1 & 15, piece = j & 1;
+        *reinterpret_cast<u32x4 *>(lp[plane] + (half * 32 + row) * RP + (half * 4 + 2 + piece) * 16) =
+            u32x4{0, 0, 0, 0};
+    }
 
     int t0 = t_begin, t1 = chunk_end(t0), buf = 0;
-    float g_next = 0.f, seg_keep = 1.f;
+    float g_next = 0.f;
     fetch(t0, t1 - t0);
     if (wave == 3) {
         decays(fetch_g(t0, t1 - t0), t1 - t0, 0);
@@ -314,7 +445,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
             decays(g_next, t2 - t1, buf ^ 1);
             if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
         }
-        if (kOut) {
+        {
             // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal: (3,0..3),
             // (2,0..2), (1,0..1), (0,0). The last two waves' third tile is another wave's.
             const int l16 = lane & 15, l4 = lane >> 4;
@@ -368,7 +499,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 u32x2 lo = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
                 const int at = t * RP + s * 2;
                 *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
-                *reinterpret_cast<u32x2 *>(lp[kOut ? 1 : 0] + at) = lo;
+                *reinterpret_cast<u32x2 *>(lp[1] + at) = lo;
             }
         }
         bf16x8 vf[4];
@@ -376,7 +507,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         if (mine) {
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
-            if (kOut) {
+            {
                 bf16x8 qf[2][2];
                 auto load = [&](int c) {
 #pragma unroll
@@ -405,9 +536,9 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 }
             }
         }
-        if (kOut) __syncthreads();
+        __syncthreads();
         if (mine) {
-            if (kOut) {
+            {
                 // (second tokens, s block 3), (2), then both halves for blocks 1 and 0
                 bf16x8 pf[2][4];
                 auto load = [&](int kb) {
@@ -416,7 +547,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
                         for (int pl = 0; pl < 2; ++pl)
                             pf[kb & 1][tt * 2 + pl] =
-                                lds_read(lp[kOut ? pl : 0] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
+                                lds_read(lp[pl] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
                 };
                 load(3);
 #pragma unroll
@@ -443,68 +574,21 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                         }
                     }
             }
-            if (t1 < t_end || MODE == kSegState || t1 == en.n) {
+            if (t1 < t_end || t1 == en.n) {
                 const float d = whole[buf];
-                if (MODE == kSegState) seg_keep *= d;
-                u32x4 kf[2][DK / 32];
-                f32x4 wf[2][2];
-                auto load = [&](int kb) {
-#pragma unroll
-                    for (int it = 0; it < DK / 32; ++it)
-                        kf[kb & 1][it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        wf[kb & 1][i] = *reinterpret_cast<const f32x4 *>(&keep[buf][kb * 16 + hf * 8 + i * 4]);
-                };
-                load(0);
-                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int it = 0; it < DK / 32; ++it)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) S[it][r] *= d;
-#pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
-                    if (kb < 3) load(kb + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    float x[8];
-                    u32x4 hi, lo, lo2;
-                    const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = bf16_lo(v[e]) * wf[kb & 1][e / 2][2 * e % 4];
-                        x[2 * e + 1] = bf16_hi(v[e]) * wf[kb & 1][e / 2][2 * e % 4 + 1];
-                    }
-                    split2(x, hi, lo);
-                    if constexpr (THREE) {
-                        lo2 = split_rest(x, lo);
-#pragma unroll
-                        for (int it = 0; it < DK / 32; ++it)
-                            S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2), S[it]);
-                    }
-#pragma unroll
-                    for (int it = 0; it < DK / 32; ++it)
-                        S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo), S[it]);
-#pragma unroll
-                    for (int it = 0; it < DK / 32; ++it)
-                        S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi), S[it]);
-                }
+                add_chunk<DK, THREE>(S, lk, vf, keep[buf], lane);
             }
         }
-        if (kOut && t1 == en.n) commit();
+        if (t1 == en.n) commit();
         if (t2 == t1) break;
         __syncthreads();
         t0 = t1;
         t1 = t2;
         buf ^= 1;
-    }
-    if (MODE == kSegState && mine) {
-#pragma unroll
-        for (int it = 0; it < DK / 32; ++it)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                *reinterpret_cast<f32x4 *>(ws + ((it * 4 + m) * 64 + lane) * 4) =
-                    f32x4{S[it][m * 4], S[it][m * 4 + 1], S[it][m * 4 + 2], S[it][m * 4 + 3]};
-        if (tile == 0 && tid == 0) p.seg_decay[(long long)seg * a.B * a.Hv + bh] = seg_keep;
     }
 }
 
@@ -604,18 +688,18 @@ static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream)
     const unsigned items = (unsigned)(units * a.group * p.tiles);
     const dim3 block(256);
     if (p.nseg == 1) {
-        hipLaunchKernelGGL((la_chunk_kernel<DK, kWhole, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+        hipLaunchKernelGGL((la_chunk_kernel<DK, false, FULL, THREE>), dim3(items), block, 0, stream, a, p);
         return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
     }
     const unsigned scan = (unsigned)(((long long)a.B * a.Hv * (a.Dv * DK / 4) + 255) / 256);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegState, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_segment_kernel<DK, FULL, THREE>), dim3(items), block, 0, stream, a, p);
     if (p.state_dtype == RGDR_F32)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_F32>, dim3(scan), block, 0, stream, a, p, DK);
     else if (p.state_dtype == RGDR_BF16)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_BF16>, dim3(scan), block, 0, stream, a, p, DK);
     else
         hipLaunchKernelGGL(la_scan_kernel<RGDR_MXI8>, dim3(scan), block, 0, stream, a, p, DK);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, kSegOut, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, true, FULL, THREE>), dim3(items), block, 0, stream, a, p);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
