@@ -654,8 +654,12 @@ static int cu_count() {
 }
 
 // How many segments: as many as fill the device's resident workgroups (two on a compute unit, one
-// with D_k = 256), of at least two chunks. Two segments would do one and a half times the work in
-// half the length each, plus two launches, so a call is cut into three or more, or not at all.
+// with D_k = 256), of at least two chunks; and whether they pay. With `fill` the share of the
+// resident workgroups that the segments take, a chunk of a segment costs about 1.4 + 1.1 fill
+// chunks of a call in one pass (both passes over it, two workgroups on a compute unit), and the
+// launches and the states 2 + 4 fill. Measured at H = 16/32, D = 128, fp32, one pass against
+// segments, us: B=1 T=384 33.0/30.0, T=512 41.2/31.7, T=1024 68/35.6, T=8192 538/123; B=2 T=512
+// 42.2/35.9; B=4 T=512 42.9/51.6, T=1024 79.3/78.5, T=4096 283/215; B=5 T=2048 150/148.
 static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, size_t &bytes) {
     bytes = 0;
     p.nseg = 1;
@@ -668,10 +672,11 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
     const int chunks = (T + kChunk - 1) / kChunk;
     if (items <= 0) return true;
     const long long most = slots / items < chunks / 2 ? slots / items : chunks / 2;
-    if (most < 3) return true;
+    if (most < 2) return true;
     const int seg_chunks = (int)((chunks + most - 1) / most);
     const int nseg = (chunks + seg_chunks - 1) / seg_chunks;
-    if (nseg < 3) return true;
+    const double fill = (double)items * nseg / slots;
+    if (chunks <= seg_chunks * (1.4 + 1.1 * fill) + 2 + 4 * fill) return true;
     p.nseg = nseg;
     p.seg_len = seg_chunks * kChunk;
     const size_t bh = (size_t)B * H_v;
