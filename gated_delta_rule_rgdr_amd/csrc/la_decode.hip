@@ -64,12 +64,24 @@ struct StepShape {
     static_assert(NT % 64 == 0 && NT >= DK && 64 % LPR == 0 && DK % RPP == 0, "tile shape");
 };
 
-// Sum over the lanes of the wave that hold the same columns, LPR apart; every lane gets it.
+// Sum over the lanes of the wave that hold the same columns, LPR apart; every lane gets it. Rotations
+// within rows of 16 lanes, then exchanges between rows: register moves, no LDS.
+template <int CTRL>
+__device__ __forceinline__ float add_rotated(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
 template <int LPR>
 __device__ __forceinline__ float row_lanes_sum(float x) {
-#pragma unroll
-    for (int m = LPR; m < 64; m <<= 1) x += __shfl_xor(x, m);
-    return x;
+    static_assert(LPR >= 2 && LPR <= 32, "lanes across a row");
+    if constexpr (LPR <= 8) x = add_rotated<0x128>(x);
+    if constexpr (LPR <= 4) x = add_rotated<0x124>(x);
+    if constexpr (LPR <= 2) x = add_rotated<0x122>(x);
+    if constexpr (LPR <= 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // N bf16 values of a row, in fp32; p is aligned to their 2 N bytes or to 16.
