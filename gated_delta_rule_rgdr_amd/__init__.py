@@ -690,7 +690,7 @@ def _la_call(fn, query, key, value, g, state_pool, lens, idx, nacc, scale, state
                  query.data_ptr(), _strides(query), key.data_ptr(), _strides(key),
                  value.data_ptr(), _strides(value), g.data_ptr(), _strides(g),
                  state_pool.data_ptr(), _ptr(state_scales), _STATE_CODE[state], _ptr(lens),
-                 _ptr(idx), _ptr(nacc), scale, B, Hq, Hv, T, Dk, Dv, N, out.data_ptr(),
+                 _ptr(idx), _ptr(nacc), float(scale), B, Hq, Hv, T, Dk, Dv, N, out.data_ptr(),
                  _strides(out), state_out.data_ptr(), _ptr(state_scales_out), *ws)
     if rc:
         _check(rc, fn)
@@ -888,7 +888,7 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
 
     rc = _launch(lib.la_norm_gate, dev, stream, x.data_ptr(), _strides(x), _ptr(gate),
                  None if gate is None else bth(gate), weight.data_ptr(),
-                 D if weight.dim() == 2 else 0, _DTYPE_CODE[dtype], _ptr(actual_seq_lengths), eps,
+                 D if weight.dim() == 2 else 0, _DTYPE_CODE[dtype], _ptr(actual_seq_lengths), float(eps),
                  LA_GATE_SIGMOID if sigmoid else 0, B, H, T, D, out.data_ptr(), bth(out))
     if rc:
         _check(rc, "la_norm_gate")

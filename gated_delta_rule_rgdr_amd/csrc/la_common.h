@@ -74,6 +74,7 @@ struct LaArgs {
     LaStrides sq, sk, sv, sg, so;
     float scale;
     int B, Hq, Hv, T, Dv, N_slots, group;
+    bool in_place;  // a state that no token changes need not be written
 };
 
 constexpr long long kMaxTokenStride = 1 << 24;  // elements from one token's row to the next's

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
     const int h = item % a.Hv, b = item / a.Hv, hq = h / a.group;
     const LaEntry en = la_entry(a, b);
     uint16_t *go = a.out + b * a.so.b + h * a.so.h + tile * TV;
-    if (!en.state || (en.L == 0 && a.pool == a.pool_out)) {  // nothing to read, nothing new to write
+    if (!en.state || (en.L == 0 && a.in_place)) {  // nothing to read, nothing new to write
         for (int c = tid; c < TV; c += NT) go[c] = 0;
         return;
     }
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     uint16_t *const go = a.out + b * a.so.b + h * a.so.h + tile * 128;
     for (int j = tid; j < (a.T - L) * vpieces; j += NT)
         *reinterpret_cast<u32x4 *>(go + (L + j / vpieces) * a.so.t + j % vpieces * 8) = u32x4{0, 0, 0, 0};
-    if (!en.state || (L == 0 && a.pool == a.pool_out)) return;
+    if (!en.state || (L == 0 && a.in_place)) return;
 
     // operands: eight rows of q, k and v (the last token's again behind it: those have no weight)
     constexpr int QN = (DK + NT - 1) / NT, VN = (kMaxT * 16 + NT - 1) / NT;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     }
 
     f32x16 o[CB] = {};
-    const bool store = n || a.pool != a.pool_out;
+    const bool store = n || !a.in_place;
     char *const raw = lw[wave];
     // The wave's own pieces, read back across its lanes: LDS serves a wave's accesses in order, and
     // the compiler is kept from reordering them.
@@ -590,6 +590,7 @@ rgdr_status la_check(LaArgs &a, int max_t, const void *query, const la_strides *
     a.out = static_cast<uint16_t *>(out);
     a.pool_out = state_out;
     a.scales_out = state_scales_out;
+    a.in_place = state_pool == state_out && (!mx || state_scales == state_scales_out);
     a.lens = lens;
     a.idx = idx;
     a.nacc = nacc;

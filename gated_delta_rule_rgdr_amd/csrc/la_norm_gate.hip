@@ -47,6 +47,18 @@ struct NormVec {
     }
 };
 
+// Sum over aligned groups of LPR lanes, in each of them.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+    if constexpr (LPR != 32) {
+        return group_sum<LPR>(x);
+    } else {
+        x = group_sum<16>(x);
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+}
+
 // LPR lanes for each row, NV pieces of 16 bytes in each lane: the row stays in registers between the
 // sum and the product, so x and the gate are read once. A workgroup's 256 / LPR groups of lanes
 // take HR heads (2^hr_log) times TR = 256 / LPR / HR tokens, and U such sets of tokens one after
@@ -96,8 +108,7 @@ __global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a, int
             for (int c = 0; c < V::N; ++c) s1 = __builtin_fmaf(v[c], v[c], s1);
             ss += m == 0 || c0 + m * LPR * V::N < a.D ? s1 : 0.f;
         }
-#pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor(ss, m);
+        ss = row_sum<LPR>(ss);
         const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
         if (t >= a.T) continue;
 #pragma unroll

@@ -26,6 +26,17 @@ struct LaPlan {
     float *seg_decay;  // [nseg][B*H_v]
 };
 
+// The largest of 32 lanes' values: rotations within rows of 16, then the two rows' exchange.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_rotated(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t half_max(uint32_t x) {
+    x = max_rotated<0x121>(max_rotated<0x122>(max_rotated<0x124>(max_rotated<0x128>(x))));
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return max(r[0], r[1]);
+}
+
 // One wave's 32 columns of a state, D_k rows: register r = 8 kb + e of tile `it` is row
 // 32 it + 16 kb + 8 (lane / 32) + e, column map32(lane % 32).
 // `base`: the element of the wave's first column in the state's first row.
@@ -76,10 +87,7 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
             } else if constexpr (ST == RGDR_BF16) {
                 *reinterpret_cast<uint16_t *>(x + at) = f32_to_bf16(y);
             } else {
-                uint32_t top = __float_as_uint(y) & 0x7FFFFFFFu;  // as whole numbers NaN is the largest
-#pragma unroll
-                for (int m = 16; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-                const uint32_t eb = mx_exponent(top);
+                const uint32_t eb = mx_exponent(half_max(mx_top_bits(y)));
                 *reinterpret_cast<uint8_t *>(x + at) = (uint8_t)mx_code_bits(y, mx_inverse(eb));
                 if ((lane & 31) == 0) (sc + row * (Dv / kMxBlock))[sat] = (uint8_t)eb;
             }

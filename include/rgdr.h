@@ -386,7 +386,7 @@ typedef struct { int64_t b, h, t; } la_strides;
  *   D_k, D_v      D_k in {64, 128, 256}; D_v a multiple of 32 up to 4096.
  *   out           bf16 [B, H_v, T, D_v] with out_strides (NULL: contiguous; rows must not
  *                 overlap), written entirely: rows of tokens past an entry's length, and of
- *                 skipped entries, are +0.0. 16-byte aligned.
+ *                 skipped entries, are +0.0. 16-byte aligned; overlaps no input.
  *   state_out, state_scales_out
  *                 receive the state after the first num_accepted_tokens tokens in every slot that
  *                 an entry names, in the pool's type; other slots are not touched. They may be

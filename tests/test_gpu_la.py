@@ -140,6 +140,15 @@ def test_lengths_slots_and_counts(rg, fn, T, state):
     assert torch.all(out[6:].contiguous().view(torch.int16) == 0)
 
 
+@pytest.mark.parametrize("fn,T", [("la_decode", 1), ("la_decode", 4), ("la_prefill", 40)])
+def test_codes_in_place_scales_apart(rg, fn, T):
+    """Scales into an array of their own while the codes stay: entries without tokens, and with
+    none accepted, get theirs too."""
+    c = Case(4, 1, 2, T, 64, 64, "i8", seed=15, lens=[T, 0, T, T], acc=[T, 0, 0, T])
+    out, pool, scales = c.call(rg, fn, state_out=c.pool, state_scales_out=torch.zeros_like(c.scales))
+    c.check(out, pool, scales, f"{fn} scales apart")
+
+
 @pytest.mark.parametrize("state", ["f32", "i8"])
 @pytest.mark.parametrize("fn,T", [("la_decode", 5), ("la_prefill", 90), ("la_prefill", 600)])
 def test_padding_is_not_read(rg, fn, T, state):
