@@ -109,7 +109,11 @@ __device__ __forceinline__ void load_bf16(float (&x)[N], const uint16_t *p) {
 
 // One token: one workgroup for each (entry, value head, TV columns). A lane holds 16 bytes of each
 // of its rows, so the state moves in whole lines. The operands' loads go out before the state's,
-// whose answers are waited for last.
+// whose answers are waited for last. Bound: the state's bytes, in and out. H_v = 32, D = 128: bf16
+// B=1 3.4 us (launch and latency), B=256 96.9 us (5.6 TB/s; a large copy reaches 5.3); fp32 B=128
+// 95.2 us (5.7); 8 bits B=128 28.9 us (4.9), where widening, the block maximum and packing take
+// about 7 vector instructions an element. Held to more waves with fewer registers, the loads go out in
+// smaller sets: bf16 B=256 107 us at 6 waves for each SIMD, 151 at 8.
 template <int ST, int DK, int TV>
 __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles) {
     using Sh = StepShape<ST, DK, TV>;
@@ -196,7 +200,10 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
 // transposed (lanes: rows i, registers: columns j), and back; as bf16 they become an operand of
 // S^T q on the way. The tokens are a quarter of the products' 32 columns; the products are far
 // from bounding the call all the same (30 of them, under 0.5 us, for 4096 elements, whose bytes
-// take a compute unit 0.4 to 1.6 us).
+// take a compute unit 0.4 to 1.6 us). H_v = 32, D = 128, B = 32, T = 8: fp32 29.9 us (4.7 TB/s), bf16
+// 16.1 us (4.6), 8 bits 15.7 us (2.6: vector work, as above). Read and written straight in the products'
+// layout, 32 rows apart from lane to lane, the same took 46, 29 and 28 us; on the vector units
+// alone 60, 82 and 52.
 template <int ST, int DK, int CB>
 __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int tiles) {
     constexpr int KP = DK / 8;                          // 16-byte pieces of a q or k row

@@ -180,7 +180,8 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
 // What one segment adds to the state behind it, from a zero state, into the workspace: the first pass
 // over a long prompt. Its chunks are taken from the last to the first, each token weighted by the
 // decay from it to the segment's end, so nothing is rescaled in between. A segment that another one
-// of the entry follows is full. Bound: k and v once more; two chunks are in flight.
+// of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 38 us for 16
+// segments of 8 chunks, of which the last states' way out and the first loads are a third.
 template <int DK, bool FULL, bool THREE>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8, NR = kChunk * KP / 256, NV = kChunk * 16 / 256;
@@ -276,6 +277,12 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(cons
         p.seg_decay[(long long)seg * a.B * a.Hv + bh] = __builtin_amdgcn_exp2f((float)behind);
 }
 
+// Bound: for each SIMD and chunk, two waves' vector instructions (about 785 each, a quarter of them the
+// state's split, a fifth the weighted values') and products (82 of 32 cycles, 98 with fp32 states)
+// together fill nine tenths of the cycles: B=16, H=16/32, T=1024, D=128, bf16 131 us (3.3 TB/s, 262
+// TFLOP/s of the recurrence); with every operand in the L2 it is 121. One workgroup alone on a
+// compute unit takes 4.3 us for a chunk, two 8.2 us for two.
+//
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
@@ -328,7 +335,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                                        (from + j / vpieces) * a.so.t + (j % vpieces) * 8) = u32x4{0, 0, 0, 0};
     }
     if (!en.state) return;
-    if (t_begin >= t_end && t_begin != 0) return;
+    if (t_begin >= t_end && t_begin != 0) return;  // the first segment commits the state of no token
 
     f32x16 S[DK / 32];
     const long long base = ((long long)__builtin_amdgcn_readfirstlane(en.slot) * a.Hv + h) * DK * a.Dv + col0;
@@ -515,73 +522,69 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         if (mine) {
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
-            {
-                bf16x8 qf[2][2];
-                auto load = [&](int c) {
+            bf16x8 qf[2][2];
+            auto load = [&](int c) {
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) qf[c & 1][tt] = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
-                };
-                load(0);
+                for (int tt = 0; tt < 2; ++tt) qf[c & 1][tt] = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
+            };
+            load(0);
 #pragma unroll
-                for (int c = 0; c < DK / 16; ++c) {
-                    if (c + 1 < DK / 16) load(c + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    float x[8];
-                    u32x4 hi, lo;
+            for (int c = 0; c < DK / 16; ++c) {
+                if (c + 1 < DK / 16) load(c + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                float x[8];
+                u32x4 hi, lo;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
-                    split2(x, hi, lo);
+                for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
+                split2(x, hi, lo);
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi, qf[c & 1][tt], o[tt]);
+                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi, qf[c & 1][tt], o[tt]);
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo, qf[c & 1][tt], o[tt]);
-                }
+                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo, qf[c & 1][tt], o[tt]);
+            }
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    const float c = carry[buf][tt * 32 + col];
+            for (int tt = 0; tt < 2; ++tt) {
+                const float c = carry[buf][tt * 32 + col];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) o[tt][r] *= c;
-                }
+                for (int r = 0; r < 16; ++r) o[tt][r] *= c;
             }
         }
         __syncthreads();
         if (mine) {
-            {
-                // (second tokens, s block 3), (2), then both halves for blocks 1 and 0
-                bf16x8 pf[2][4];
-                auto load = [&](int kb) {
+            // (second tokens, s block 3), (2), then both halves for blocks 1 and 0
+            bf16x8 pf[2][4];
+            auto load = [&](int kb) {
 #pragma unroll
-                    for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
-#pragma unroll
-                        for (int pl = 0; pl < 2; ++pl)
-                            pf[kb & 1][tt * 2 + pl] =
-                                lds_read(lp[pl] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
-                };
-                load(3);
-#pragma unroll
-                for (int kb = 3; kb >= 0; --kb) {
-                    if (kb > 0) load(kb - 1);
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
 #pragma unroll
                     for (int pl = 0; pl < 2; ++pl)
+                        pf[kb & 1][tt * 2 + pl] =
+                            lds_read(lp[pl] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
+            };
+            load(3);
 #pragma unroll
-                        for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
-                            o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 2 + pl], o[tt]);
-                }
+            for (int kb = 3; kb >= 0; --kb) {
+                if (kb > 0) load(kb - 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-                    if (tt * 32 + col < n) {
-                        char *row = reinterpret_cast<char *>(go + (long long)(t0 + tt * 32) * a.so.t) + out_at;
+                for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            u32x4 y;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = pack_bf16x2(o[tt][m * 8 + 2 * e], o[tt][m * 8 + 2 * e + 1]);
-                            *reinterpret_cast<u32x4 *>(row + m * 32) = y;
-                        }
-                    }
+                    for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
+                        o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 2 + pl], o[tt]);
             }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+                if (tt * 32 + col < n) {
+                    char *row = reinterpret_cast<char *>(go + (long long)(t0 + tt * 32) * a.so.t) + out_at;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        u32x4 y;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = pack_bf16x2(o[tt][m * 8 + 2 * e], o[tt][m * 8 + 2 * e + 1]);
+                        *reinterpret_cast<u32x4 *>(row + m * 32) = y;
+                    }
+                }
             if (t1 < t_end || t1 == en.n) {
                 const float d = whole[buf];
 #pragma unroll
@@ -602,7 +605,8 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 
 // Segments' own contributions into their incoming states, in place: one thread for four rows of a
 // column. The states in the pool are read here and committed by the next kernel, since a slot may
-// be updated in place.
+// be updated in place. Bound: the states, in and out (13.3 us for 16 segments of 32 heads at D = 128,
+// 4.9 TB/s).
 template <int ST>
 __global__ __launch_bounds__(256) void la_scan_kernel(const LaArgs a, const LaPlan p, int DK) {
     const int per = a.Dv * DK / 4;  // threads for each (entry, head)

@@ -26,7 +26,9 @@ __device__ __forceinline__ bool move_slots(const StateMove &m, int i, int &s, in
 }
 
 // A lane holds 16 bytes of the wide pool, so both pools are read and written in whole lines: 4
-// columns in fp32 (8 lanes for a block), 8 in bf16 (4 lanes). U such units are in flight.
+// columns in fp32 (8 lanes for a block), 8 in bf16 (4 lanes). U such units are in flight. Bound: the
+// bytes. 96 slots of H_v = 32, D = 128: fp32 into 8 bits 49.1 us (5.2 TB/s), back 38.5 us (6.6);
+// bf16 27.3 us (5.6) and 24.3 us (6.3); one slot 2.2 us each (the launch).
 template <bool BF16>
 struct Unit {
     static constexpr int N = BF16 ? 8 : 4;            // columns

@@ -67,9 +67,10 @@ typedef enum {
     RGDR_ERR_NULL = 1,        /* a required pointer is NULL                                */
     RGDR_ERR_SHAPE = 2,       /* a size is negative, or zero where not allowed; T > 8
                                  (decode) or T > 65536 (prefill); H_v % H_q != 0; grid too
-                                 large; beta requested without b                          */
+                                 large; beta requested without b; a stride not allowed     */
     RGDR_ERR_UNSUPPORTED = 3, /* D_k not in {64, 128}, D_v not a multiple of 64 or above
-                                 4096, or an unknown option bit                             */
+                                 4096 (the la_ calls: their own sizes), or an unknown
+                                 option bit                                                 */
     RGDR_ERR_RANGE = 4,       /* (validate) a length, count or slot index out of range     */
     RGDR_ERR_DUPLICATE = 5,   /* (validate) two batch entries name the same slot           */
     RGDR_ERR_DTYPE = 6,       /* a dtype code not allowed for that argument                 */
