@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the HIP kernels of
 ``librgdr.so``; PyTorch supplies device memory and the current stream. There is no CPU
 fallback: if the library is missing, the first call of any binding function raises
-``ImportError``.
+``ImportError``. The ``rgdr_`` calls and ``la_gate`` go through ctypes, the linear-attention calls
+through the CPython module ``_la_binding`` (``csrc/la_binding.cpp``), which checks and calls; where
+it finds that a call does not fit, the checks here say why.
 
 * ``rgdr_decode``  -- the recurrent gated-delta-rule decode step (MindSpore Lite API page
   "lite_boost.ops.recurrent_gated_delta_rule"), in place on a bf16 state pool.
@@ -30,7 +32,6 @@ host, for debugging only (it cannot run under graph capture). A bad length, coun
 then raises ``RuntimeError`` instead of being clamped or skipped by the kernel.
 """
 import ctypes as C
-import functools
 import os
 
 import torch
@@ -62,12 +63,13 @@ class _Strides(C.Structure):  # la_strides of include/rgdr.h
 
 
 _lib = None
+_quick = None  # the CPython module
 VALIDATE = os.environ.get("RGDR_VALIDATE", "") == "1"
 
 
 def library():
     """Load ``librgdr.so`` (built by ``gated_delta_rule_rgdr_amd/build.py``)."""
-    global _lib
+    global _lib, _quick
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -122,6 +124,8 @@ def library():
     lib.rgdr_validate_host.argtypes = [vp, vp, vp, i32, i32, i32]
     lib.rgdr_status_string.restype = C.c_char_p
     lib.rgdr_status_string.argtypes = [C.c_int]
+    from . import _la_binding
+    _quick = _la_binding
     _lib = lib
     return lib
 
@@ -563,7 +567,7 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-_STATE_CODE = {torch.float32: RGDR_F32, torch.bfloat16: RGDR_BF16, torch.int8: RGDR_MXI8}
+_STATE_TYPES = (torch.float32, torch.bfloat16, torch.int8)
 
 
 def _scales(state, scales, name):
@@ -581,21 +585,25 @@ def _scales(state, scales, name):
     return scales
 
 
-def _la_refuse(fn, query, key, value, g, state_pool, index, state_scales, out, state_out,
-               state_scales_out):
+def _la_refuse(fn, query, key, value, g, state_pool, lens, idx, nacc, state_scales, out,
+               state_out, state_scales_out, workspace, final=True):
     """The checks of a linear-attention call one by one, each with its message."""
     _rows(query, "query", (torch.bfloat16,))
     _rows(key, "key", (torch.bfloat16,))
     _rows(value, "value", (torch.bfloat16,))
-    _rows(g, "g", (torch.float32,), 3)
     B, Hq, T, Dk = query.shape
     Hv, Dv = value.shape[1], value.shape[3]
-    if not isinstance(state_pool, torch.Tensor) or state_pool.dtype not in _STATE_CODE:
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        _dev(g, "g", torch.float32, 1)
+    else:
+        _rows(g, "g", (torch.float32,), 3)
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dtype not in _STATE_TYPES:
         raise RuntimeError("state_pool must be a float32, bfloat16 or int8 tensor")
     _dev(state_pool, "state_pool", state_pool.dtype, 4)
     N = state_pool.shape[0]
     if tuple(key.shape) != (B, Hq, T, Dk) or tuple(value.shape) != (B, Hv, T, Dv) \
-            or tuple(g.shape) != (B, Hv, T) or tuple(state_pool.shape) != (N, Hv, Dk, Dv):
+            or tuple(g.shape) not in ((B, Hv, T), (Hv,)) \
+            or tuple(state_pool.shape) != (N, Hv, Dk, Dv):
         raise RuntimeError(f"{fn}: inconsistent shapes")
     _scales(state_pool, state_scales, "state_scales")
     if state_out is not state_pool:
@@ -603,111 +611,79 @@ def _la_refuse(fn, query, key, value, g, state_pool, index, state_scales, out, s
         if state_out.shape != state_pool.shape:
             raise RuntimeError("state_out must have the pool's shape")
     _scales(state_out, state_scales_out, "state_scales_out")
+    index = {"actual_seq_lengths": lens, "ssm_state_indices": idx, "num_accepted_tokens": nacc}
     for nm, t in index.items():
         _index(t, nm, B)
     if out is not None:
         _rows(out, "out", (torch.bfloat16,))
         if tuple(out.shape) != (B, Hv, T, Dv):
             raise RuntimeError("out must be [B, H_v, T, D_v]")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor)
+                                  or workspace.dtype != torch.uint8 or not workspace.is_cuda
+                                  or not workspace.is_contiguous()):
+        raise RuntimeError("workspace must be a contiguous uint8 CUDA tensor")
     _same_device(query, key=key, value=value, g=g, state_pool=state_pool, out=out,
                  state_scales=state_scales, state_out=state_out,
-                 state_scales_out=state_scales_out, **index)
+                 state_scales_out=state_scales_out, workspace=workspace, **index)
+    if final:
+        raise RuntimeError(f"{fn}: unsupported arguments")
 
 
-# The quick form of the checks: whether a tensor is what a call takes. A call whose tensors all
-# are goes on; one that is not goes through the checks that say what is wrong.
-def _fits(t, dtype, dev, shape):
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-            and t.shape == shape and t.is_contiguous())
-
-
-def _fits_rows(t, dtype, dev, shape):
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-            and t.shape == shape and (t.dim() == 3 or t.stride(3) == 1))
-
-
-def _strides(t):
-    """None for a contiguous tensor."""
-    return None if t.is_contiguous() else _Strides(*t.stride()[:3])
+def _raw_stream(t, stream):
+    """The stream's handle; by default the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
 
 
 def _la_call(fn, query, key, value, g, state_pool, lens, idx, nacc, scale, state_scales, out,
              state_out, state_scales_out, stream, workspace=None):
-    lib = library()
-    bf16, i32 = torch.bfloat16, torch.int32
+    if _lib is None:
+        library()
     if state_out is None:
         if state_scales_out is not None:
             raise RuntimeError("state_scales_out goes with state_out")
         state_out, state_scales_out = state_pool, state_scales
-    fine = (isinstance(query, torch.Tensor) and query.is_cuda and query.dim() == 4
-            and isinstance(value, torch.Tensor) and value.dim() == 4
-            and isinstance(state_pool, torch.Tensor) and state_pool.dim() == 4)
-    if fine:
-        B, Hq, T, Dk = query.shape
-        _, Hv, _, Dv = value.shape
-        N, dev, state = state_pool.shape[0], query.get_device(), state_pool.dtype
-        if isinstance(g, torch.Tensor) and g.dim() == 1:
-            g = g[None, :, None].expand(B, g.shape[0], T)  # one decay for each head
-        pool, scales = (N, Hv, Dk, Dv), (N, Hv, Dk, Dv // LA_BLOCK)
-        fine = (_fits_rows(query, bf16, dev, (B, Hq, T, Dk))
-                and _fits_rows(key, bf16, dev, (B, Hq, T, Dk))
-                and _fits_rows(value, bf16, dev, (B, Hv, T, Dv))
-                and _fits_rows(g, torch.float32, dev, (B, Hv, T))
-                and state in _STATE_CODE and _fits(state_pool, state, dev, pool)
-                and (state_out is state_pool or _fits(state_out, state, dev, pool))
-                and (state_scales is None and state_scales_out is None if state is not torch.int8
-                     else Dv % LA_BLOCK == 0 and _fits(state_scales, torch.uint8, dev, scales)
-                     and _fits(state_scales_out, torch.uint8, dev, scales))
-                and (lens is None or _fits(lens, i32, dev, (B,)))
-                and (idx is None or _fits(idx, i32, dev, (B,)))
-                and (nacc is None or _fits(nacc, i32, dev, (B,)))
-                and (out is None or _fits_rows(out, bf16, dev, (B, Hv, T, Dv))))
-    if not fine:
-        _la_refuse(fn, query, key, value, g, state_pool,
-                   {"actual_seq_lengths": lens, "ssm_state_indices": idx,
-                    "num_accepted_tokens": nacc}, state_scales, out, state_out, state_scales_out)
-        raise RuntimeError(f"{fn}: unsupported arguments")
-    if out is None:
-        out = _empty((B, Hv, T, Dv), bf16, query.device, stream)
-    if VALIDATE and B:
-        def given(t, other):
-            return t if t is not None else torch.as_tensor(other, dtype=i32, device=query.device)
-        n = given(lens, [T] * B)
-        _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N)
-    ws = ()
-    if fn == "la_prefill":
-        if workspace is None:
-            size = la_prefill_workspace_size(B, Hv, T, Dk, Dv, dev)
-            if size:
-                workspace = _empty(size, torch.uint8, query.device, stream)
-        elif workspace.dtype != torch.uint8 or not workspace.is_cuda \
-                or not workspace.is_contiguous():
-            raise RuntimeError("workspace must be a contiguous uint8 CUDA tensor")
-        else:
-            _same_device(query, workspace=workspace)
-        ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    rc = _launch(getattr(lib, fn), dev, stream,
-                 query.data_ptr(), _strides(query), key.data_ptr(), _strides(key),
-                 value.data_ptr(), _strides(value), g.data_ptr(), _strides(g),
-                 state_pool.data_ptr(), _ptr(state_scales), _STATE_CODE[state], _ptr(lens),
-                 _ptr(idx), _ptr(nacc), float(scale), B, Hq, Hv, T, Dk, Dv, N, out.data_ptr(),
-                 _strides(out), state_out.data_ptr(), _ptr(state_scales_out), *ws)
+    if stream is not None or VALIDATE:
+        out, workspace = _la_prepare(fn, query, key, value, g, state_pool, lens, idx, nacc,
+                                     state_scales, out, state_out, state_scales_out, stream,
+                                     workspace)
+    done = _quick.attention(fn == "la_prefill", query, key, value, g, state_pool, state_scales,
+                            lens, idx, nacc, scale, out, state_out, state_scales_out, workspace,
+                            _raw_stream(query, stream))
+    if done is None:
+        _la_refuse(fn, query, key, value, g, state_pool, lens, idx, nacc, state_scales, out,
+                   state_out, state_scales_out, workspace)
+    rc, out = done
     if rc:
         _check(rc, fn)
     return (out, state_out) if state_scales is None else (out, state_out, state_scales_out)
 
 
-def _launch(call, dev, stream, *args):
-    """call(*args, stream) with the tensors' device current, which it need not be."""
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        return call(*args, handle)
-    with torch.cuda.device(dev):
-        return call(*args, handle)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _la_prepare(fn, query, key, value, g, state_pool, lens, idx, nacc, state_scales, out,
+                state_out, state_scales_out, stream, workspace):
+    """What a call needs before it when it has a stream of its own (its new tensors belong to that
+    stream) or when the index arrays are to be checked."""
+    _la_refuse(fn, query, key, value, g, state_pool, lens, idx, nacc, state_scales, out,
+               state_out, state_scales_out, workspace, final=False)
+    B, Hq, T, Dk = query.shape
+    Hv, Dv = value.shape[1], value.shape[3]
+    if VALIDATE and B:
+        def given(t, other):
+            return t if t is not None else torch.as_tensor(other, dtype=torch.int32,
+                                                           device=query.device)
+        n = given(lens, [T] * B)
+        _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T,
+                          state_pool.shape[0])
+    if stream is not None:
+        if out is None:
+            out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
+        if fn == "la_prefill" and workspace is None:
+            size = la_prefill_workspace_size(B, Hv, T, Dk, Dv, query.device)
+            if size:
+                workspace = _empty(size, torch.uint8, query.device, stream)
+    return out, workspace
 
 
 def la_decode(query, key, value, g, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
@@ -743,21 +719,15 @@ def la_prefill(query, key, value, g, state_pool, actual_seq_lengths=None, ssm_st
                     state_scales_out, stream, workspace)
 
 
-@functools.lru_cache(maxsize=1024)
-def _la_workspace(sizes, dev):
-    lib = library()
-    n = C.c_size_t(0)
-    with torch.cuda.device(dev):
-        rc = lib.la_prefill_workspace_size(*sizes, C.byref(n))
-    _check(rc, "la_prefill_workspace_size")
-    return n.value
-
-
 def la_prefill_workspace_size(B, H_v, T, D_k, D_v, device=None):
     """Bytes of workspace that ``la_prefill`` uses for a call of these sizes on ``device`` (0:
     it needs none)."""
-    return _la_workspace((B, H_v, T, D_k, D_v),
-                         device if device is not None else torch.cuda.current_device())
+    lib = library()
+    n = C.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        rc = lib.la_prefill_workspace_size(B, H_v, T, D_k, D_v, C.byref(n))
+    _check(rc, "la_prefill_workspace_size")
+    return n.value
 
 
 def _slots(src_slots, dst_slots, n_src):
@@ -814,15 +784,11 @@ def la_state_dequantize(codes, scales, state=None, *, dtype=torch.bfloat16, src_
 
 
 def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
-    lib = library()
-    dev, i32 = state.get_device(), torch.int32
-    shape = state.shape
-    if not (len(shape) == 4 and state.is_cuda and state.is_contiguous()
-            and isinstance(codes, torch.Tensor) and shape[3] % LA_BLOCK == 0
-            and _fits(codes, torch.int8, dev, (codes.shape[0], *shape[1:]))
-            and _fits(scales, torch.uint8, dev, (*codes.shape[:3], shape[3] // LA_BLOCK))
-            and (src_slots is None or _fits(src_slots, i32, dev, (n,)))
-            and (dst_slots is None or _fits(dst_slots, i32, dev, (n,)))):
+    if _lib is None:
+        library()
+    rc = _quick.move(fn == "la_state_dequantize", state, codes, scales, src_slots, dst_slots, n,
+                     _raw_stream(state, stream))
+    if rc is None:
         _dev(state, "state", state.dtype, 4)
         _dev(codes, "codes", torch.int8, 4)
         if codes.shape[1:] != state.shape[1:]:
@@ -832,17 +798,8 @@ def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
         _index(dst_slots, "dst_slots", n)
         _same_device(state, codes=codes, scales=scales, src_slots=src_slots, dst_slots=dst_slots)
         raise RuntimeError(f"{fn}: unsupported arguments")
-    if n:
-        wide = (state.data_ptr(), _STATE_CODE[state.dtype])
-        packed = (codes.data_ptr(), scales.data_ptr())
-        src, dst = _ptr(src_slots), _ptr(dst_slots)
-        if fn == "la_state_quantize":
-            args = (*wide, shape[0], src, *packed, codes.shape[0], dst)
-        else:
-            args = (*packed, codes.shape[0], src, *wide, shape[0], dst)
-        rc = _launch(getattr(lib, fn), dev, stream, *args, n, *shape[1:])
-        if rc:
-            _check(rc, fn)
+    if rc:
+        _check(rc, fn)
     return codes, scales
 
 
@@ -856,23 +813,20 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
     contiguous and rows at multiples of 8 elements, D a multiple of 8 up to 8192. ``weight``
     float32 ``[D]`` or ``[H,D]``. Returns ``out``, ``[B,T,H,D]`` of x's type; rows of tokens past
     ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
-    lib = library()
-    if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.dtype not in _DTYPE_CODE \
-            or not x.is_cuda:
+    if _lib is None:
+        library()
+    if stream is not None and out is None and isinstance(x, torch.Tensor) and x.dim() == 4:
+        B, H, T, D = x.shape
+        out = _empty((B, T, H, D), x.dtype, x.device, stream)
+    done = _quick.norm_gate(x, weight, gate, eps, LA_GATE_SIGMOID if sigmoid else 0,
+                            actual_seq_lengths, out, _raw_stream(x, stream))
+    if done is None:
         _rows(x, "x", tuple(_DTYPE_CODE))
-    B, H, T, D = x.shape
-    dtype, dev, rows = x.dtype, x.get_device(), (B, T, H, D)
-    if not (_fits_rows(x, dtype, dev, (B, H, T, D))
-            and (_fits(weight, torch.float32, dev, (D,)) or _fits(weight, torch.float32, dev, (H, D)))
-            and (gate is None or _fits_rows(gate, dtype, dev, rows))
-            and (out is None or _fits_rows(out, dtype, dev, rows))
-            and (actual_seq_lengths is None
-                 or _fits(actual_seq_lengths, torch.int32, dev, (B,)))):
-        _rows(x, "x", tuple(_DTYPE_CODE))
+        B, H, T, D = x.shape
         for nm, t in (("gate", gate), ("out", out)):
             if t is not None:
-                _rows(t, nm, (dtype,))
-                if tuple(t.shape) != rows:
+                _rows(t, nm, (x.dtype,))
+                if tuple(t.shape) != (B, T, H, D):
                     raise RuntimeError(f"{nm} must be [B, T, H, D]")
         if not isinstance(weight, torch.Tensor) or tuple(weight.shape) not in ((D,), (H, D)):
             raise RuntimeError("weight must be a [D] or [H, D] tensor")
@@ -880,16 +834,7 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
         _index(actual_seq_lengths, "actual_seq_lengths", B)
         _same_device(x, weight=weight, gate=gate, out=out, actual_seq_lengths=actual_seq_lengths)
         raise RuntimeError("la_norm_gate: unsupported arguments")
-    if out is None:
-        out = _empty(rows, dtype, x.device, stream)
-
-    def bth(t):  # the strides of a [B, T, H, D] tensor
-        return None if t.is_contiguous() else _Strides(t.stride(0), t.stride(2), t.stride(1))
-
-    rc = _launch(lib.la_norm_gate, dev, stream, x.data_ptr(), _strides(x), _ptr(gate),
-                 None if gate is None else bth(gate), weight.data_ptr(),
-                 D if weight.dim() == 2 else 0, _DTYPE_CODE[dtype], _ptr(actual_seq_lengths), float(eps),
-                 LA_GATE_SIGMOID if sigmoid else 0, B, H, T, D, out.data_ptr(), bth(out))
+    rc, out = done
     if rc:
         _check(rc, "la_norm_gate")
     return out

@@ -1,4 +1,5 @@
-"""Builds ``librgdr.so`` (the gfx950 HIP library behind ``include/rgdr.h``) in-tree.
+"""Builds ``librgdr.so`` (the gfx950 HIP library behind ``include/rgdr.h``) and ``_la_binding.so``
+(a CPython module, host code only, linked against torch) in-tree.
 
     python -m gated_delta_rule_rgdr_amd.build [--verbose]
 
@@ -16,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librgdr.so")
+BINDING = os.path.join(PKG, "_la_binding.so")
 
 SOURCES = ["rgdr_decode.hip", "rgdr_prefill.hip", "la_gate.hip", "la_decode.hip",
            "la_prefill.hip", "la_state.hip", "la_norm_gate.hip", "rgdr_host.cpp"]
@@ -30,6 +32,25 @@ def compile_cmd(src, obj, extra=()):
             + ["-c", src, "-o", obj])
 
 
+def binding_cmds(obj):
+    """Compile and link commands of the CPython module."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+               os.path.join(rocm, "include"), INCLUDE]
+    compile_ = (["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+                + [x for d in include for x in ("-isystem", d)]
+                + ["-c", os.path.join(CSRC, "la_binding.cpp"), "-o", obj])
+    link = ["g++", "-shared", "-fPIC", obj, "-L", PKG, "-l:librgdr.so", "-L", lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}", "-o", BINDING + ".tmp"]
+    return compile_, link
+
+
 def build(verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     procs = []
@@ -42,6 +63,12 @@ def build(verbose: bool = False, extra=()) -> str:
             print(" ".join(cmd), flush=True)
         procs.append((s, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    binding_obj = os.path.join(BUILD_DIR, "la_binding.o")
+    binding_compile, binding_link = binding_cmds(binding_obj)
+    if verbose:
+        print(" ".join(binding_compile), flush=True)
+    procs.append(("la_binding.cpp", subprocess.Popen(binding_compile, stdout=subprocess.PIPE,
+                                                     stderr=subprocess.STDOUT)))
     failed = []
     for s, p in procs:
         out, _ = p.communicate()
@@ -53,13 +80,17 @@ def build(verbose: bool = False, extra=()) -> str:
         if p.returncode:
             failed.append(s)
     if failed:
-        raise RuntimeError(f"hipcc failed for {failed}")
+        raise RuntimeError(f"the compiler failed for {failed}")
     tmp = LIB + ".tmp"
     link = ["hipcc", f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    if verbose:
+        print(" ".join(binding_link), flush=True)
+    subprocess.run(binding_link, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

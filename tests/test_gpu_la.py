@@ -316,6 +316,37 @@ def test_other_stream(rg):
     assert torch.equal(a, b) and all(torch.equal(x, y) for x, y in zip(outs, want))
 
 
+def test_two_calls_at_once(rg):
+    """Two prompts on two streams, each cut into segments with a workspace of its own, and decode
+    steps under a stream context: what the calls leave one after the other."""
+    cs = [Case(1, 2, 4, 1300, 128, 128, "f32", seed=62 + i, lens=[1300 - 77 * i], acc=[900]) for i in range(2)]
+    want = [c.call(rg, "la_prefill", pool=c.pool.clone()) for c in cs]
+    pools = [c.pool.clone() for c in cs]
+    args = [(c.lens.cuda(), c.idx.cuda(), c.acc.cuda(), c.scale) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [None, None]
+    for i, (c, st) in enumerate(zip(cs, streams)):
+        with torch.cuda.stream(st):
+            outs[i] = rg.la_prefill(c.q, c.k, c.v, c.g, pools[i], *args[i])[0]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i][0]) and torch.equal(pools[i], want[i][1])
+
+
+def test_index_arrays_are_validated(rg, monkeypatch):
+    monkeypatch.setattr(rg, "VALIDATE", True)
+    c = Case(2, 1, 2, 4, 64, 64, "f32", seed=63, lens=[4, 3], acc=[4, 1], idx=[2, 0])
+    out = c.call(rg, "la_decode")[0]
+    c.check(out, c.pool, None, "validated")
+    rg.la_decode(c.q, c.k, c.v, c.g, c.pool)  # every array left out
+    for name, bad in (("idx", [0, 0]), ("idx", [0, 4]), ("lens", [5, 1]), ("acc", [4, 2])):
+        d = Case(2, 1, 2, 4, 64, 64, "f32", seed=63, lens=[4, 1], acc=[4, 1], idx=[2, 0])
+        setattr(d, name, torch.tensor(bad, dtype=torch.int32))
+        with pytest.raises(RuntimeError, match="RGDR_ERR"):
+            d.call(rg, "la_prefill")
+
+
 def test_same_call_same_bits(rg):
     for fn, T in (("la_decode", 1), ("la_decode", 7), ("la_prefill", 333), ("la_prefill", 1500)):
         c = Case(2, 1, 2, T, 128, 128, "f32", seed=71)
@@ -591,6 +622,13 @@ def test_refusals_on_the_device(rg):
                                                                    device="cuda").expand(2, 2, 3, 64))
     with pytest.raises(RuntimeError, match="expected cuda"):
         rg._same_device(c.q, other=torch.zeros(1))
+    with pytest.raises(RuntimeError, match="workspace must be"):
+        rg.la_prefill(*good, state_scales=c.scales, workspace=torch.zeros(4, device="cuda"))
+    with pytest.raises(RuntimeError, match="RGDR_ERR_ALIGN"):
+        rg.la_prefill(*good, state_scales=c.scales,
+                      workspace=torch.zeros(1024, dtype=torch.uint8, device="cuda")[8:])
+    with pytest.raises(RuntimeError, match="actual_seq_lengths must have shape"):
+        rg.la_decode(*good, c.lens.cuda()[:1], state_scales=c.scales)
     with pytest.raises(RuntimeError, match="go together"):
         rg.la_state_quantize(c.pool.float(), torch.zeros_like(c.pool))
     with pytest.raises(RuntimeError, match="names slots"):

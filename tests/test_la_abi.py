@@ -153,6 +153,24 @@ def test_norm_gate_of_nothing(lib, size):
     assert norm(lib, **{size: 0}, x=None, w=None, out=None, gate=None, lens=None) == OK
 
 
+def test_quick_calls_leave_what_does_not_fit():
+    """The CPython module takes no call whose tensors are not on a GPU, or are no tensors, and
+    raises where it is called wrongly itself."""
+    from gated_delta_rule_rgdr_amd import _la_binding as quick
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    g, s = torch.zeros(1, 2, 3), torch.zeros(1, 2, 64, 64)
+    none = [None] * 4
+    assert quick.attention(False, x, x, x, g, s, *none, 1.0, None, s, None, None, 0) is None
+    assert quick.attention(True, 1, "q", x, g, s, *none, 1.0, None, s, None, None, 0) is None
+    assert quick.move(False, s, s.to(torch.int8), s, None, None, 1, 0) is None
+    assert quick.norm_gate(x, torch.ones(64), None, 1e-6, 0, None, None, 0) is None
+    for bad in (lambda: quick.attention(1), lambda: quick.move(), lambda: quick.norm_gate(x),
+                lambda: quick.attention(False, x, x, x, g, s, *none, "1", None, s, None, None, 0),
+                lambda: quick.norm_gate(x, x, None, "eps", 0, None, None, 0)):
+        with pytest.raises(TypeError):
+            bad()
+
+
 def test_python_refuses_host_tensors():
     x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
     s = torch.zeros(1, 2, 64, 64)
