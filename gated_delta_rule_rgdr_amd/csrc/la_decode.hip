@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
         float x = 0.f;
 #pragma unroll
         for (int m = 0; m < NW; ++m) x += red[m][c];
-        go[c] = f32_to_bf16(x);  // 0 where the entry has no token: its q, k and v are zero
+        go[c] = en.L ? f32_to_bf16(x) : 0;  // of no token: 0, also where the state is not finite
     }
 }
 

@@ -149,6 +149,26 @@ def test_codes_in_place_scales_apart(rg, fn, T):
     c.check(out, pool, scales, f"{fn} scales apart")
 
 
+@pytest.mark.parametrize("state", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("fn,T", [("la_decode", 1), ("la_decode", 4), ("la_prefill", 40)])
+def test_no_token_on_a_state_that_is_not_finite(rg, fn, T, state):
+    """Outputs of an entry without tokens are zero whatever its state holds, and that state is
+    copied."""
+    c = Case(2, 1, 2, T, 64, 64, state, seed=16, lens=[0, T], acc=[0, T], idx=[1, 0], N=2)
+    kw = {"state_out": torch.zeros_like(c.pool)}
+    if state == "i8":
+        c.scales[1] = 255
+        kw["state_scales_out"] = torch.zeros_like(c.scales)
+    else:
+        c.pool[1, 0], c.pool[1, 1] = NAN, float("inf")
+    out, *new = c.call(rg, fn, **kw)
+    assert torch.all(out[0].contiguous().view(torch.int16) == 0)
+    got = c.values(new[0], new[1] if state == "i8" else None)[1]
+    want = c.values(c.pool, c.scales)[1]
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isinf(got), torch.isinf(want))
+
+
 @pytest.mark.parametrize("state", ["f32", "i8"])
 @pytest.mark.parametrize("fn,T", [("la_decode", 5), ("la_prefill", 90), ("la_prefill", 600)])
 def test_padding_is_not_read(rg, fn, T, state):
