@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         else
             store_state<DK, RGDR_MXI8>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
     };
-    if (t_begin == 0 && en.n == 0) commit();
+    if (t_begin == 0 && en.n == 0 && !a.in_place) commit();
     if (t_begin >= t_end) return;
 
     // A chunk ends after 64 tokens, at the accepted count (whose state is committed) or at the end.

@@ -169,6 +169,26 @@ def test_no_token_on_a_state_that_is_not_finite(rg, fn, T, state):
     assert torch.equal(torch.isinf(got), torch.isinf(want))
 
 
+@pytest.mark.parametrize("state", ["bf16", "i8"])
+@pytest.mark.parametrize("fn,T", [("la_decode", 1), ("la_decode", 4), ("la_prefill", 40), ("la_prefill", 700)])
+def test_no_accepted_token_leaves_the_slot(rg, fn, T, state):
+    """In place, an entry whose tokens are all rejected keeps its slot's bytes (codes that a new
+    rounding would choose otherwise too), and a padding entry of length 0 that names a slot in
+    use does not disturb it."""
+    c = Case(3, 1, 2, T, 64, 64, state, seed=17, lens=[T, T, 0], acc=[T, 0, 0], idx=[1, 3, 2], N=4)
+    if state == "i8":
+        c.pool //= 8
+    before, sbefore = c.pool.clone(), None if c.scales is None else c.scales.clone()
+    clean = c.call(rg, fn, pool=before.clone(), scales=None if sbefore is None else sbefore.clone())
+    for s in (0, 2, 3):
+        assert torch.equal(clean[1][s], before[s])
+        assert sbefore is None or torch.equal(clean[2][s], sbefore[s])
+    c.idx[2] = 1
+    got = c.call(rg, fn)
+    for x, y in zip(got, clean):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("state", ["f32", "i8"])
 @pytest.mark.parametrize("fn,T", [("la_decode", 5), ("la_prefill", 90), ("la_prefill", 600)])
 def test_padding_is_not_read(rg, fn, T, state):
