@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float wk = __shfl(wk1, e);
-            y[e] = hf ? 0.f : (e & 1 ? bf16_hi(vf[cb][e / 2]) : bf16_lo(vf[cb][e / 2])) * wk;
+            y[e] = hf || e >= n ? 0.f : (e & 1 ? bf16_hi(vf[cb][e / 2]) : bf16_lo(vf[cb][e / 2])) * wk;
         }
         split2(y, v_hi[cb], v_lo[cb]);
         v_lo2[cb] = split_rest(y, v_lo[cb]);
@@ -358,7 +358,11 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         for (int m = 0; m < NM; ++m)
             *reinterpret_cast<u32x4 *>(raw + lds_at<PC>(m * (64 / PC) + row_l, piece_l)) = w[it][m];
         in_order();
-        const bf16x8 k = lds_read_tr<KP>(lk, 0, it, col);
+        // keys of the accepted tokens: a rejected one's may be anything
+        u32x4 kw = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, 0, it, col));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kw[e] &= n > 2 * e + 1 ? 0xFFFFFFFFu : n > 2 * e ? 0xFFFFu : 0u;
+        const bf16x8 k = __builtin_bit_cast(bf16x8, kw);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             // row map32(lane % 32) of the tile, columns 32 cb + 16 kb + 8 hf .. + 7

@@ -189,6 +189,22 @@ def test_no_accepted_token_leaves_the_slot(rg, fn, T, state):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("state", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("fn,T", [("la_decode", 1), ("la_decode", 2), ("la_decode", 7), ("la_prefill", 90),
+                                  ("la_prefill", 700)])
+def test_rejected_tokens_do_not_reach_the_state(rg, fn, T, state):
+    """NaN and infinity in tokens behind the accepted ones."""
+    acc = [T // 2, T - 1, 0, T]
+    c = Case(4, 1, 2, T, 64, 64, state, seed=18, lens=[T] * 4, acc=acc)
+    clean = c.call(rg, fn, pool=c.pool.clone(), scales=None if c.scales is None else c.scales.clone())
+    c.q, c.k, c.v, c.g = (x.clone() for x in (c.q, c.k, c.v, c.g))
+    for b, n in enumerate(acc):
+        c.q[b, :, n:], c.k[b, :, n:], c.v[b, :, n:], c.g[b, :, n:] = NAN, float("inf"), NAN, NAN
+    got = c.call(rg, fn)
+    for x, y in zip(got[1:], clean[1:]):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("state", ["f32", "i8"])
 @pytest.mark.parametrize("fn,T", [("la_decode", 5), ("la_prefill", 90), ("la_prefill", 600)])
 def test_padding_is_not_read(rg, fn, T, state):
