@@ -57,7 +57,6 @@ LA_BLOCK = 32          # columns of a state row that share a scale byte in an 8-
 _DTYPE_CODE = {torch.float32: RGDR_F32, torch.float16: RGDR_F16, torch.bfloat16: RGDR_BF16}
 
 
-
 class _Strides(C.Structure):  # la_strides of include/rgdr.h
     _fields_ = [("b", C.c_int64), ("h", C.c_int64), ("t", C.c_int64)]
 
@@ -732,8 +731,10 @@ def la_prefill_workspace_size(B, H_v, T, D_k, D_v, device=None):
 
 def _slots(src_slots, dst_slots, n_src):
     """The number of entries of a state move: the index arrays' length, or every source."""
-    for t in (src_slots, dst_slots):
+    for name, t in (("src_slots", src_slots), ("dst_slots", dst_slots)):
         if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 1:
+                raise TypeError(f"{name} must be a torch.Tensor of one dimension")
             return t.shape[0]
     return n_src
 
@@ -777,7 +778,8 @@ def la_state_dequantize(codes, scales, state=None, *, dtype=torch.bfloat16, src_
         if dtype not in (torch.float32, torch.bfloat16):
             raise RuntimeError("dtype must be float32 or bfloat16")
         state = _empty((n, *codes.shape[1:]), dtype, codes.device, stream)
-    elif state.dtype not in (torch.float32, torch.bfloat16):
+    elif not isinstance(state, torch.Tensor) or \
+            state.dtype not in (torch.float32, torch.bfloat16):
         raise RuntimeError("state must be a float32 or bfloat16 tensor")
     _move("la_state_dequantize", state, codes, scales, src_slots, dst_slots, n, stream)
     return state

@@ -38,7 +38,7 @@ bool sizes_are(const at::Tensor &t, std::initializer_list<int64_t> s) {
 }
 bool on(const Arg &a, at::ScalarType type, c10::Device dev) {
     return a.here() && a.t->scalar_type() == type && a.t->device() == dev &&
-           a.t->layout() == at::kStrided;
+           a.t->layout() == at::kStrided && !a.t->is_neg();
 }
 bool fits(const Arg &a, at::ScalarType type, c10::Device dev, std::initializer_list<int64_t> s) {
     return on(a, type, dev) && sizes_are(*a.t, s) && a.t->is_contiguous();

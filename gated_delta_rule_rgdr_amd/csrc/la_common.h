@@ -101,6 +101,8 @@ __device__ __forceinline__ float la_log_decay(float g) { return g < kMinLogDecay
 
 // ---- host checks ------------------------------------------------------------------------------
 
+constexpr long long kMaxGroups = 0xFFFFFF;  // workgroups of 256 in a launch, whose threads fit 32 bits
+
 inline LaStrides la_strides_or(const la_strides *s, long long b, long long h, long long t) {
     if (s) return {s->b, s->h, s->t};
     return {b, h, t};

@@ -546,8 +546,7 @@ rgdr_status la_check_sizes(int max_t, int32_t B, int32_t H_v, int32_t T, int32_t
     if (B < 0 || H_v <= 0 || T <= 0 || T > max_t || D_k <= 0 || D_v <= 0) return RGDR_ERR_SHAPE;
     if (D_k != 64 && D_k != 128 && D_k != 256) return RGDR_ERR_UNSUPPORTED;
     if (D_v % 32 != 0 || D_v > 4096) return RGDR_ERR_UNSUPPORTED;
-    // the grids are counted in ints
-    if ((__int128)B * H_v * (D_v / 32) > 0x7FFFFFFF) return RGDR_ERR_SHAPE;
+    if ((__int128)B * H_v * (D_v % 128 ? D_v / 32 : D_v / 128) > kMaxGroups) return RGDR_ERR_SHAPE;
     return RGDR_OK;
 }
 

@@ -156,7 +156,7 @@ static rgdr_status launch_norm_rows(const NormArgs &a, hipStream_t stream) {
     const int tu = (ROWS >> hr_log) * U;
     const long long h_blocks = ((long long)a.H + (1 << hr_log) - 1) >> hr_log;
     const long long t_blocks = ((long long)a.T + tu - 1) / tu;
-    if ((__int128)h_blocks * t_blocks * a.B > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
+    if ((__int128)h_blocks * t_blocks * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
     const dim3 grid((unsigned)(h_blocks * t_blocks * a.B)), block(256);
     if (a.gate)
         hipLaunchKernelGGL((la_norm_gate_kernel<E, LPR, NV, U, true>), grid, block, 0, stream, a, hr_log,

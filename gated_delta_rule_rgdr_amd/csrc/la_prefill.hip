@@ -701,7 +701,7 @@ static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream)
     p.tiles = (a.Dv + kCols - 1) / kCols;
     // whole rounds of units over the XCDs
     const long long units = ((long long)a.B * a.Hq * p.nseg + kXcds - 1) / kXcds * kXcds;
-    if (units * a.group * p.tiles > 0x7FFFFFFF) return RGDR_ERR_SHAPE;
+    if (units * a.group * p.tiles > kMaxGroups) return RGDR_ERR_SHAPE;
     const unsigned items = (unsigned)(units * a.group * p.tiles);
     const dim3 block(256);
     if (p.nseg == 1) {

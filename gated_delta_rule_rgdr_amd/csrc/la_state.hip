@@ -152,7 +152,7 @@ static rgdr_status launch_move(StateMove &m, int n, hipStream_t stream) {
     const long long groups = (m.blocks * Unit<BF16>::LANES + 255) / 256;
     const bool four = groups / 4 * n >= 1024;
     const long long parts = four ? (groups + 3) / 4 : groups;
-    if (parts * n > 0x7FFFFFFF) return RGDR_ERR_SHAPE;  // the grid is counted in an int
+    if ((__int128)parts * n > kMaxGroups) return RGDR_ERR_SHAPE;
     m.parts = (unsigned)parts;
     const dim3 grid((unsigned)(parts * n)), block(256);
     if (four)

@@ -384,7 +384,8 @@ typedef struct { int64_t b, h, t; } la_strides;
  *                 int32 [B], as in rgdr_decode; each may be NULL: all T tokens valid, entry b
  *                 in slot b (needs N_slots >= B), every valid token accepted.
  *   scale, B, H_q, H_v, T   as in rgdr_decode.
- *   D_k, D_v      D_k in {64, 128, 256}; D_v a multiple of 32 up to 4096.
+ *   D_k, D_v      D_k in {64, 128, 256}; D_v a multiple of 32 up to 4096. B H_v ceil(D_v / 128)
+ *                 (B H_v D_v / 32 where D_v is no multiple of 128) below 2^24.
  *   out           bf16 [B, H_v, T, D_v] with out_strides (NULL: contiguous; rows must not
  *                 overlap), written entirely: rows of tokens past an entry's length, and of
  *                 skipped entries, are +0.0. 16-byte aligned; overlaps no input.
@@ -497,7 +498,7 @@ enum { LA_GATE_SIGMOID = 1u /* the gate's function is sigmoid, not silu */ };
  *              stride. 16-byte aligned, weight_h_stride a multiple of 4.
  *   actual_seq_lengths  int32 [B] or NULL: rows of tokens past an entry's length are written as
  *              +0.0 and not read.
- *   eps        >= 0.
+ *   eps        >= 0; mean(x^2) + eps is taken to be a normal fp32 number.
  *   flags      0 or LA_GATE_SIGMOID.
  *   B, H, T, D sizes >= 0 (a zero: nothing is read or launched); D a multiple of 8 up to 8192.
  *   out        as x with out_strides; NULL strides: contiguous [B, T, H, D]. It may be x's or

@@ -695,6 +695,23 @@ def test_refusals_on_the_device(rg):
         rg.la_norm_gate(c.v, torch.ones(64, device="cuda"), c.v)
 
 
+def test_refuses_odd_tensors(rg):
+    """Slot arrays that are no arrays, and a decay that torch holds as its negative."""
+    x = torch.zeros(2, 2, 64, 64, device="cuda")
+    codes, scales = rg.la_state_quantize(x)
+    with pytest.raises(TypeError, match="src_slots"):
+        rg.la_state_quantize(x, src_slots=[0, 1])
+    with pytest.raises(TypeError, match="dst_slots"):
+        rg.la_state_dequantize(codes, scales, x, dst_slots=torch.tensor(0, device="cuda"))
+    with pytest.raises(RuntimeError, match="state must be"):
+        rg.la_state_dequantize(codes, scales, [x])
+    c = Case(1, 1, 2, 4, 64, 64, "f32", seed=19)
+    c.g = torch.randn(1, 2, 4, dtype=torch.complex64, device="cuda").conj().imag
+    assert c.g.is_neg()
+    with pytest.raises(RuntimeError, match="unsupported arguments"):
+        c.call(rg, "la_decode")
+
+
 def test_empty_calls(rg):
     q = torch.zeros(0, 2, 3, 64, dtype=torch.bfloat16, device="cuda")
     g = torch.zeros(0, 2, 3, device="cuda")

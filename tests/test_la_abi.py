@@ -58,6 +58,7 @@ BAD_ATTENTION = [
     (dict(os=(2048, 128, 256)), SHAPE),         # head 2 of token 0 is head 0 of token 1
     (dict(qs=(1 << 61, 1 << 10, 128)), SHAPE),  # past any address
     (dict(B=1 << 20, Hv=1 << 12, Hq=1 << 12), SHAPE),
+    (dict(B=1 << 17, Hv=1 << 7, Hq=1, Dv=128, idx=P, N=4), SHAPE),  # 2^24 workgroups of 256
 ]
 
 
@@ -101,6 +102,7 @@ BAD_MOVE = [
     (dict(n=-1), SHAPE), (dict(H=0), SHAPE), (dict(Dk=0), SHAPE), (dict(Dv=0), SHAPE),
     (dict(Ns=0), SHAPE), (dict(Nd=0), SHAPE), (dict(src=None, Ns=2), SHAPE),
     (dict(dst=None, Nd=2), SHAPE), (dict(H=1 << 30, Dk=1 << 30, Dv=32), SHAPE),
+    (dict(n=1 << 24), SHAPE),
     (dict(Dv=40), UNSUP), (dict(dt=F16), DTYPE), (dict(dt=MXI8), DTYPE),
     (dict(x=P + 8), ALIGN), (dict(codes=P + 4), ALIGN), (dict(sc=P + 1), ALIGN),
     (dict(src=P + 2), ALIGN), (dict(dst=P + 2), ALIGN),
@@ -134,6 +136,7 @@ BAD_NORM = [
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(out=None), NULL),
     (dict(B=-1), SHAPE), (dict(H=-1), SHAPE), (dict(T=-1), SHAPE), (dict(D=-8), SHAPE),
     (dict(eps=-1e-6), SHAPE), (dict(eps=float("nan")), SHAPE),
+    (dict(B=1 << 24, H=32, lens=None), SHAPE),
     (dict(xs=(-1, 1, 1)), SHAPE), (dict(ws=-4), SHAPE), (dict(os=(1536, 128, 128)), SHAPE),
     (dict(D=100), UNSUP), (dict(D=8200), UNSUP), (dict(fl=2), UNSUP),
     (dict(dt=MXI8), DTYPE), (dict(dt=9), DTYPE),
