@@ -134,46 +134,78 @@ __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
     return m;
 }
 
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
+// One step of a stretch of products: LOADS reads of LDS, then N products with VALU vector
+// instructions behind each, which issue while it runs. Left to itself the compiler puts a step's
+// products in a row and its vector work behind them (B=16, T=1024, D=128, bf16: 132 us, B=8 80.5; so
+// 130 and 78.9).
+template <int LOADS, int N, int VALU>
+__device__ __forceinline__ void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, LOADS, 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // S += sum_s k_s (w_s v_s)^T over the 64 tokens of a chunk: k from LDS, v's operands in registers, one
 // weight for each token in LDS.
 template <int DK, bool THREE>
 __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const bf16x8 (&vf)[4],
                                           const float *weight, int lane) {
     constexpr int KP = DK / 8;
-    u32x4 kf[2][DK / 32];
+    constexpr int NI = DK / 32;
+    u32x4 kf[2][NI], hi[2], lo[2], lo2[2];
     f32x4 wf[2][2];
-    auto load = [&](int kb) {
+    auto load_k = [&](int kb) {
 #pragma unroll
-        for (int it = 0; it < DK / 32; ++it)
+        for (int it = 0; it < NI; ++it)
             kf[kb & 1][it] = __builtin_bit_cast(u32x4, lds_read_tr<KP, kTrPad>(lk, kb * 16, it, lane));
+    };
+    auto load_w = [&](int kb) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             wf[kb & 1][i] = *reinterpret_cast<const f32x4 *>(weight + kb * 16 + (lane >> 5) * 8 + i * 4);
     };
-    load(0);
-#pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-        if (kb < 3) load(kb + 1);
-        __builtin_amdgcn_sched_barrier(0);  // the loads stay a step ahead of the products
+    auto weigh = [&](int kb) {
         float x[8];
-        u32x4 hi, lo;
         const u32x4 v = __builtin_bit_cast(u32x4, vf[kb]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             x[2 * e] = bf16_lo(v[e]) * wf[kb & 1][e / 2][2 * e % 4];
             x[2 * e + 1] = bf16_hi(v[e]) * wf[kb & 1][e / 2][2 * e % 4 + 1];
         }
-        split2(x, hi, lo);
-        if constexpr (THREE) {
-            const u32x4 lo2 = split_rest(x, lo);
+        split2(x, hi[kb & 1], lo[kb & 1]);
+        if constexpr (THREE) lo2[kb & 1] = split_rest(x, lo[kb & 1]);
+    };
+    load_w(0);
+    load_k(0);
+    load_w(1);
+    weigh(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int it = 0; it < DK / 32; ++it)
-                S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2), S[it]);
+    for (int kb = 0; kb < 4; ++kb) {
+        if (kb < 3) {
+            load_k(kb + 1);
+            weigh(kb + 1);
         }
+        if (kb < 2) load_w(kb + 2);
+        if constexpr (THREE)
 #pragma unroll
-        for (int it = 0; it < DK / 32; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo), S[it]);
+            for (int it = 0; it < NI; ++it)
+                S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2[kb & 1]), S[it]);
 #pragma unroll
-        for (int it = 0; it < DK / 32; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi), S[it]);
+        for (int it = 0; it < NI; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo[kb & 1]), S[it]);
+#pragma unroll
+        for (int it = 0; it < NI; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi[kb & 1]), S[it]);
+        // a step: eight values, weighted and split, 5 instructions each, or 8 with the third part
+        interleave<2 * NI, (THREE ? 3 : 2) * NI, (THREE ? 64 : 40) / ((THREE ? 3 : 2) * NI)>();
     }
 }
 
@@ -455,27 +487,24 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         const int lane = now & 63, col = lane & 31, hf = lane >> 5;
         stage();
         __syncthreads();
-        if (t2 > t1) fetch(t1, t2 - t1);
-        if (wave == 3 && t2 > t1) {
-            decays(g_next, t2 - t1, buf ^ 1);
-            if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
-        }
-        {
-            // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal: (3,0..3),
-            // (2,0..2), (1,0..1), (0,0). The last two waves' third tile is another wave's.
+        // scores of tokens t (lanes) and s (registers), in tiles on and below the diagonal: (3,0..3),
+        // (2,0..2), (1,0..1), (0,0); the last two waves have two, and the last one the decays, whose
+        // chain the others would wait for.
+        auto scores = [&](auto count) {
+            constexpr int NS = decltype(count)::value;
             const int l16 = lane & 15, l4 = lane >> 4;
-            f32x4 x[3] = {};
-            int ts[3], ss[3];
+            f32x4 x[NS] = {};
+            int ts[NS], ss[NS];
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int i = min(wave + 4 * j, 9);
+            for (int j = 0; j < NS; ++j) {
+                const int i = wave + 4 * j;
                 ts[j] = (i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0) * 16 + l16;
                 ss[j] = (i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0) * 16;
             }
-            bf16x8 kf[2][3], qf[2][3];
+            bf16x8 kf[2][NS], qf[2][NS];
             auto load = [&](int c) {
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
+                for (int j = 0; j < NS; ++j) {
                     kf[c & 1][j] = lds_read(lk + lds_at<KP, kTrPad>(ss[j] + l16, c * 4 + l4));
                     qf[c & 1][j] = lds_read(lq + lds_at<KP>(ts[j], c * 4 + l4));
                 }
@@ -486,12 +515,12 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 if (c + 1 < DK / 32) load(c + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) x[j] = mfma16(kf[c & 1][j], qf[c & 1][j], x[j]);
+                for (int j = 0; j < NS; ++j) x[j] = mfma16(kf[c & 1][j], qf[c & 1][j], x[j]);
             }
-            float th[3], tl[3];
-            f32x4 sh[3], sl[3];
+            float th[NS], tl[NS];
+            f32x4 sh[NS], sl[NS];
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
+            for (int j = 0; j < NS; ++j) {
                 th[j] = g_hi[buf][ts[j]];
                 tl[j] = g_lo[buf][ts[j]];
                 sh[j] = *reinterpret_cast<const f32x4 *>(&g_hi[buf][ss[j] + l4 * 4]);
@@ -499,7 +528,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
+            for (int j = 0; j < NS; ++j) {
                 const int t = ts[j], s = ss[j] + l4 * 4;
                 float y[4];
 #pragma unroll
@@ -516,31 +545,75 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
                 *reinterpret_cast<u32x2 *>(lp[1] + at) = lo;
             }
+        };
+        if (wave < 2) {
+            scores(Count<3>{});
+        } else {
+            if (wave == 3 && t2 > t1) {
+                decays(g_next, t2 - t1, buf ^ 1);
+                if (t2 < t_end) g_next = fetch_g(t2, chunk_end(t2) - t2);
+            }
+            scores(Count<2>{});
         }
         bf16x8 vf[4];
         f32x16 o[2] = {};
-        if (mine) {
+        // S^T q; the next chunk's loads go out between the products, since twelve in a row keep each
+        // wave waiting 800 cycles for their issue; before them all where that chunk is not whole.
+        // (B=16 130 -> 128 us, B=8 78.9 -> 75.2, one prompt of 8192 tokens 120 -> 117, with the
+        // scores' share for each wave below.)
+        auto incoming = [&](auto loads) {
+            constexpr bool LOADS = decltype(loads)::value;
+            constexpr int NS = DK / 16, NL = 2 * NR + NV;
+            const char *gq1 = reinterpret_cast<const char *>(gq + t1 * a.sq.t);
+            const char *gk1 = reinterpret_cast<const char *>(gk + t1 * a.sk.t);
+            const char *gv1 = reinterpret_cast<const char *>(gv + t1 * a.sv.t);
+            const uint32_t q0 = qk_row * qt + qk_at, k0 = qk_row * kt + qk_at, v0 = v_row * vt + v_at;
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
             bf16x8 qf[2][2];
+            u32x4 hi[2], lo[2];
             auto load = [&](int c) {
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) qf[c & 1][tt] = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
             };
-            load(0);
-#pragma unroll
-            for (int c = 0; c < DK / 16; ++c) {
-                if (c + 1 < DK / 16) load(c + 1);
-                __builtin_amdgcn_sched_barrier(0);
+            auto halves = [&](int c) {
                 float x[8];
-                u32x4 hi, lo;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
-                split2(x, hi, lo);
+                split2(x, hi[c & 1], lo[c & 1]);
+            };
+            load(0);
+            halves(0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi, qf[c & 1][tt], o[tt]);
+            for (int c = 0; c < NS; ++c) {
+                if (c + 1 < NS) {
+                    load(c + 1);
+                    halves(c + 1);
+                }
+                if constexpr (LOADS)
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo, qf[c & 1][tt], o[tt]);
+                    for (int i = c * NL / NS; i < (c + 1) * NL / NS; ++i) {
+                        const int m = i < 2 * NR ? i / 2 : i - 2 * NR;
+                        if (i >= 2 * NR)
+                            rv[m] = *reinterpret_cast<const u32x4 *>(gv1 + (uint64_t)(m * 16) * vt + v0);
+                        else if (i % 2)
+                            rk[m] = *reinterpret_cast<const u32x4 *>(gk1 + (uint64_t)(m * (256 / KP)) * kt + k0);
+                        else
+                            rq[m] = *reinterpret_cast<const u32x4 *>(gq1 + (uint64_t)(m * (256 / KP)) * qt + q0);
+                    }
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi[c & 1], qf[c & 1][tt], o[tt]);
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo[c & 1], qf[c & 1][tt], o[tt]);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    if (LOADS && i % 2) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -548,6 +621,12 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[tt][r] *= c;
             }
+        };
+        if (mine && t2 - t1 == kChunk) {
+            incoming(Count<1>{});
+        } else {
+            if (t2 > t1) fetch(t1, t2 - t1);
+            if (mine) incoming(Count<0>{});
         }
         __syncthreads();
         if (mine) {
@@ -562,15 +641,27 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                             lds_read(lp[pl] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
             };
             load(3);
+            const float d = whole[buf];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int kb = 3; kb >= 0; --kb) {
                 if (kb > 0) load(kb - 1);
-                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int it = kb * DK / 128; it < (kb + 1) * DK / 128; ++it)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) S[it][r] *= d;
+#pragma unroll
+                for (int it = kb * DK / 128; it < (kb + 1) * DK / 128; ++it)
+                    asm volatile("" : "+v"(S[it]));  // here, among the products
 #pragma unroll
                 for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
                     for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
                         o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 2 + pl], o[tt]);
+                if (kb < 2)
+                    interleave<4, 4, 4>();
+                else
+                    interleave<4, 2, 8>();
             }
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
@@ -586,11 +677,6 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     }
                 }
             if (t1 < t_end || t1 == en.n) {
-                const float d = whole[buf];
-#pragma unroll
-                for (int it = 0; it < DK / 32; ++it)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) S[it][r] *= d;
                 add_chunk<DK, THREE>(S, lk, vf, keep[buf], lane);
             }
         }
