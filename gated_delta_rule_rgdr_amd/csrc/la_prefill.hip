@@ -808,7 +808,7 @@ static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream)
 
 template <int DK>
 static rgdr_status launch_prefill_dk(const LaArgs &a, const LaPlan &p, hipStream_t stream) {
-    const bool three = p.state_dtype == RGDR_F32;
+    const bool three = p.state_dtype != RGDR_BF16;
     if (a.Dv % kCols == 0)
         return three ? launch_prefill<DK, true, true>(a, p, stream) : launch_prefill<DK, true, false>(a, p, stream);
     return three ? launch_prefill<DK, false, true>(a, p, stream) : launch_prefill<DK, false, false>(a, p, stream);

@@ -278,6 +278,24 @@ def test_strides(rg, fn, T):
     assert torch.equal(out.transpose(1, 2).contiguous(), o2) and torch.equal(p1, p2)
 
 
+@pytest.mark.parametrize("fn", ["la_decode", "la_prefill"])
+def test_codes_are_those_of_the_state(rg, fn):
+    """An 8-bit commit rounds a state that is good to fp32, so a code differs from the exact state's
+    only where that is within fp32's error of a step's middle. Two tokens, every one accepted, so
+    S = d S0 + w k1 v1 + k2 v2: of the sum's magnitudes, d and w are off by 2^-24 for their
+    exponent's rounding (it is below 1), 2^-23 for the exponential and 2^-24 for the product, what is
+    left of a value in three bf16 parts is 2^-27, and each of the up to four sums into which the terms
+    go rounds by 2^-24 (2^-23 where it truncates): 2^-20 for all."""
+    c = Case(4, 8, 16, 2, 128, 128, "i8", seed=21, lens=[2] * 4, acc=[2] * 4)
+    _, pool, scales = c.call(rg, fn)
+    _, states, _, smags = attention(c.q, c.k, c.v, c.g, c.S0, c.lens, c.idx, c.acc, c.scale)
+    for b in range(c.B):
+        got = mx_values(pool[c.idx[b]], scales[c.idx[b]])
+        slack = 2.0 ** -20 * smags[b]
+        over = (got - states[b]).abs() - mx_step(states[b].abs() + slack) / 2 - slack
+        assert over.max() <= 0, f"{(over > 0).sum()} codes, off by {over.max():.3g} more than half a step"
+
+
 def test_shared_entries(rg):
     """One prompt for every entry (stride 0 along the batch)."""
     c = Case(3, 1, 2, 40, 64, 64, "f32", seed=9, lens=[40, 17, 40], acc=[40, 17, 3])
