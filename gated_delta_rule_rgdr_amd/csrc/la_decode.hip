@@ -164,7 +164,6 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
 
     char *const o_state = static_cast<char *>(a.pool_out) + first * kSize;
     uint8_t *const o_scale = ST == RGDR_MXI8 ? a.scales_out + first / kMxBlock : nullptr;
-    const bool store = en.n || !a.in_place;
     float acc[CPL] = {};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -176,7 +175,6 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
             x[c] = __builtin_fmaf(op[1], vt[c], sc * Piece<ST>::get(w[r], c));
             acc[c] = __builtin_fmaf(op[0], x[c], acc[c]);
         }
-        if (!store) continue;
         if (en.n) w[r] = round_piece<ST>(x, eb[r]);  // else the token is rejected: the bytes as they were
         __builtin_nontemporal_store(w[r], reinterpret_cast<u32x4 *>(o_state + r * row_bytes));
         if constexpr (ST == RGDR_MXI8)

@@ -393,7 +393,7 @@ typedef struct { int64_t b, h, t; } la_strides;
  *                 receive the state after the first num_accepted_tokens tokens in every slot that
  *                 an entry names, in the pool's type; other slots are not touched. They may be
  *                 state_pool and state_scales (in place: then a slot whose entry accepts no token
- *                 is not written); any other overlap is undefined.
+ *                 keeps its bytes); any other overlap is undefined.
  *
  * The arithmetic is fp32; the state is rounded once, when it is committed. RGDR_MXI8 commits
  * choose for each block of 32 columns the smallest power of two with which its largest value
