@@ -9,8 +9,9 @@
 //
 // Precision: q, k and v are bf16 and enter the products as they are. What is computed enters as a
 // sum of bf16 numbers: the state and the scores as two (2^-16 of each, far below the output's
-// bf16 rounding), the scaled v of the state's update as two as well, and as three (2^-24) where the
-// state leaves in fp32 and nothing coarser follows. The state is kept in fp32 over the whole prompt.
+// bf16 rounding), the scaled v of the state's update as two as well for a bf16 state, and as three
+// (2^-24) where the state leaves in fp32, or in 8 bits, whose values near a step's middle go by
+// what the sum is good to (142 and 160 against 128 us for B=16, T=1024, H=16/32, D=128). The state is kept in fp32 over the whole prompt.
 #include "la_mfma.h"
 
 namespace rgdr {
@@ -100,7 +101,7 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
 // L2. Units go round the XCDs (workgroup ids do), those of the longest entries first: with
 // ragged lengths every XCD, and every compute unit's two places, then get long and short ones.
 // (B=16, H=16/32, D=128, lengths from 0 to 1024: 101.5 us, against 108.2 with each XCD's units
-// contiguous.)
+// contiguous, both before the work between the products below.)
 struct LaItem {
     int b, seg, h, tile;
     bool live;
@@ -212,7 +213,7 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
 // What one segment adds to the state behind it, from a zero state, into the workspace: the first pass
 // over a long prompt. Its chunks are taken from the last to the first, each token weighted by the
 // decay from it to the segment's end, so nothing is rescaled in between. A segment that another one
-// of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 38 us for 16
+// of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 35.5 us for 16
 // segments of 8 chunks, of which the last states' way out and the first loads are a third.
 template <int DK, bool FULL, bool THREE>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(const LaArgs a, const LaPlan p) {
@@ -309,18 +310,18 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(cons
         p.seg_decay[(long long)seg * a.B * a.Hv + bh] = __builtin_amdgcn_exp2f((float)behind);
 }
 
-// Bound: for each SIMD and chunk, two waves' vector instructions (about 785 each, a quarter of them the
-// state's split, a fifth the weighted values') and products (82 of 32 cycles, 98 with fp32 states)
-// together fill nine tenths of the cycles: B=16, H=16/32, T=1024, D=128, bf16 131 us (3.3 TB/s, 262
-// TFLOP/s of the recurrence); with every operand in the L2 it is 121. One workgroup alone on a
-// compute unit takes 4.3 us for a chunk, two 8.2 us for two.
+// Bound: for each SIMD and chunk, two waves' vector instructions (about 760 each, a quarter of them the
+// state's split, a fifth the weighted values') and products (82 of 32 cycles, 98 with fp32 and 8-bit
+// states) together fill nine tenths of the cycles, at 1.96 GHz: B=16, H=16/32, T=1024, D=128, bf16 128
+// us (3.4 TB/s, 268 TFLOP/s of the recurrence). One workgroup alone on a compute unit runs at 2.38 GHz
+// and takes 3.9 us for a chunk, two 7.9 us for two.
 //
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
 // each; one with two also sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
 //
-// FULL: D_v is a multiple of 128, so every wave has columns. THREE: the state leaves in fp32. Both are
+// FULL: D_v is a multiple of 128, so every wave has columns. THREE: the state leaves in fp32 or 8 bits. Both are
 // template arguments so that a chunk is a few long stretches of code without branches, in which
 // the products and the vector work around them can be interleaved.
 template <int DK, bool SEGMENTS, bool FULL, bool THREE>
