@@ -344,18 +344,12 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     f32x16 o[CB] = {};
     const bool store = n || !a.in_place;
     char *const raw = lw[wave];
-    // The wave's own pieces, read back across its lanes: LDS serves a wave's accesses in order, and
-    // the compiler is kept from reordering them.
-    auto in_order = [&]() {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    };
 #pragma unroll
     for (int it = 0; it < NI; ++it) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
             *reinterpret_cast<u32x4 *>(raw + lds_at<PC>(m * (64 / PC) + row_l, piece_l)) = w[it][m];
-        in_order();
+        wave_in_order();
         // keys of the accepted tokens: a rejected one's may be anything
         u32x4 kw = __builtin_bit_cast(u32x4, lds_read_tr<KP>(lk, 0, it, col));
 #pragma unroll
@@ -406,7 +400,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
                 }
                 *reinterpret_cast<u32x4 *>(ls[wave][0] + pa) = hi;
             }
-            in_order();
+            wave_in_order();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const bf16x8 q = lds_read(lq + lds_at<KP>(col & 7, (it * 2 + c) * 2 + hf));
@@ -414,7 +408,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
                 for (int pl = PL - 1; pl >= 0; --pl)
                     o[cb] = mfma(__builtin_bit_cast(u32x4, lds_read_tr<4>(ls[wave][pl], c * 16, 0, lane)), q, o[cb]);
             }
-            in_order();
+            wave_in_order();
             if (!n) continue;
             f32x16 z;
 #pragma unroll
@@ -456,7 +450,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
                 }
             }
         }
-        in_order();
+        wave_in_order();
         if (store) {
             char *p = static_cast<char *>(a.pool_out) + (head + (long long)it * 32 * a.Dv) * kSize + lane_off;
 #pragma unroll
@@ -473,7 +467,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
                         *reinterpret_cast<uint16_t *>(sp) = (uint16_t)eb[it];
                 }
         }
-        in_order();
+        wave_in_order();
     }
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {

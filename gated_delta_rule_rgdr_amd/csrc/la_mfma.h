@@ -99,6 +99,13 @@ __device__ __forceinline__ u32x4 split_rest(float (&x)[8], const u32x4 &lo) {
     return lo2;
 }
 
+// Between a wave's writes into its own part of LDS and its reads of them across the lanes: LDS serves
+// a wave's accesses in order, and the compiler is kept from reordering them.
+__device__ __forceinline__ void wave_in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }

@@ -11,7 +11,7 @@
 // sum of bf16 numbers: the state and the scores as two (2^-16 of each, far below the output's
 // bf16 rounding), the scaled v of the state's update as two as well for a bf16 state, and as three
 // (2^-24) where the state leaves in fp32, or in 8 bits, whose values near a step's middle go by
-// what the sum is good to (142 and 160 against 128 us for B=16, T=1024, H=16/32, D=128). The state is kept in fp32 over the whole prompt.
+// what the sum is good to (142 and 141 against 128 us for B=16, T=1024, H=16/32, D=128). The state is kept in fp32 over the whole prompt.
 #include "la_mfma.h"
 
 namespace rgdr {
@@ -42,13 +42,10 @@ __device__ __forceinline__ uint32_t half_max(uint32_t x) {
 // 32 it + 16 kb + 8 (lane / 32) + e, column map32(lane % 32).
 // `base`: the element of the wave's first column in the state's first row.
 template <int DK, int ST>
-__device__ __forceinline__ void load_state(f32x16 (&S)[DK / 32], const void *pool,
-                                           const uint8_t *scales, long long base, int Dv, int lane) {
-    constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
+__device__ __forceinline__ void load_state(f32x16 (&S)[DK / 32], const void *pool, long long base, int Dv, int lane) {
+    constexpr int kSize = ST == RGDR_F32 ? 4 : 2;
     const char *p = static_cast<const char *>(pool) + base * kSize;
-    const uint8_t *sc = scales + base / kMxBlock;
     const uint32_t at = (uint32_t)((lane >> 5) * 8 * Dv + map32(lane & 31)) * kSize;
-    const uint32_t sat = (uint32_t)((lane >> 5) * 8 * (Dv / kMxBlock));
 #pragma unroll
     for (int it = 0; it < DK / 32; ++it) {
 #pragma unroll
@@ -57,25 +54,19 @@ __device__ __forceinline__ void load_state(f32x16 (&S)[DK / 32], const void *poo
             const char *x = p + (uint32_t)(row * Dv) * kSize;
             if constexpr (ST == RGDR_F32)
                 S[it][r] = *reinterpret_cast<const float *>(x + at);
-            else if constexpr (ST == RGDR_BF16)
-                S[it][r] = bf16_to_f32(*reinterpret_cast<const uint16_t *>(x + at));
             else
-                S[it][r] = static_cast<float>(*reinterpret_cast<const int8_t *>(x + at)) *
-                           mx_scale((sc + row * (Dv / kMxBlock))[sat]);
+                S[it][r] = bf16_to_f32(*reinterpret_cast<const uint16_t *>(x + at));
         }
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 template <int DK, int ST>
-__device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *pool,
-                                            uint8_t *scales, long long base, int Dv, int lane) {
-    constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
+__device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *pool, long long base, int Dv, int lane) {
+    constexpr int kSize = ST == RGDR_F32 ? 4 : 2;
     char *p = static_cast<char *>(pool) + base * kSize;
-    uint8_t *sc = scales + base / kMxBlock;
     asm volatile("" : "+v"(lane));  // the rows' addresses are formed here, not kept from the prompt's start
     const uint32_t at = (uint32_t)((lane >> 5) * 8 * Dv + map32(lane & 31)) * kSize;
-    const uint32_t sat = (uint32_t)((lane >> 5) * 8 * (Dv / kMxBlock));
 #pragma unroll
     for (int it = 0; it < DK / 32; ++it)
 #pragma unroll
@@ -83,17 +74,81 @@ __device__ __forceinline__ void store_state(const f32x16 (&S)[DK / 32], void *po
             const int row = it * 32 + (r >> 3) * 16 + (r & 7);
             char *x = p + (uint32_t)(row * Dv) * kSize;
             const float y = S[it][r];
-            if constexpr (ST == RGDR_F32) {
+            if constexpr (ST == RGDR_F32)
                 *reinterpret_cast<float *>(x + at) = y;
-            } else if constexpr (ST == RGDR_BF16) {
+            else
                 *reinterpret_cast<uint16_t *>(x + at) = f32_to_bf16(y);
-            } else {
-                const uint32_t eb = mx_exponent(half_max(mx_top_bits(y)));
-                *reinterpret_cast<uint8_t *>(x + at) = (uint8_t)mx_code_bits(y, mx_inverse(eb));
-                if ((lane & 31) == 0) (sc + row * (Dv / kMxBlock))[sat] = (uint8_t)eb;
-            }
             if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few rows at a time: registers
         }
+}
+
+// 8-bit states go in pieces of 16 bytes (half a block) through LDS that is the wave's own: the codes of
+// its D_k blocks, then their scale bytes. (B=16, T=1024, H=16/32, D=128: 141 us; code by code to and
+// from memory 160.)
+template <int DK>
+__device__ __forceinline__ constexpr int mx_lds_bytes() {
+    return DK * (kMxBlock + 1);
+}
+template <int DK>
+__device__ __forceinline__ void load_state_mx(f32x16 (&S)[DK / 32], const void *pool, const uint8_t *scales,
+                                              long long base, int Dv, char *lds, int lane) {
+    const char *p = static_cast<const char *>(pool) + base;
+    const uint8_t *sc = scales + base / kMxBlock;
+    u32x4 w[DK / 32];
+    uint8_t eb[DK / 64];
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m)
+        w[m] = *reinterpret_cast<const u32x4 *>(p + (uint32_t)((m * 32 + lane / 2) * Dv + lane % 2 * 16));
+#pragma unroll
+    for (int m = 0; m < DK / 64; ++m) eb[m] = sc[(uint32_t)((m * 64 + lane) * (Dv / kMxBlock))];
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m) *reinterpret_cast<u32x4 *>(lds + (m * 64 + lane) * 16) = w[m];
+#pragma unroll
+    for (int m = 0; m < DK / 64; ++m) lds[DK * kMxBlock + m * 64 + lane] = (char)eb[m];
+    wave_in_order();
+    const char *const code = lds + (lane >> 5) * 8 * kMxBlock + map32(lane & 31);
+    const char *const scale = lds + DK * kMxBlock + (lane >> 5) * 8;
+#pragma unroll
+    for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int row = it * 32 + kb * 16;
+            const u32x2 e8 = *reinterpret_cast<const u32x2 *>(scale + row);  // of eight rows
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                S[it][kb * 8 + e] =
+                    static_cast<float>(*reinterpret_cast<const int8_t *>(code + (row + e) * kMxBlock)) *
+                    mx_scale(e8[e / 4] >> (e % 4 * 8) & 255);
+        }
+    wave_in_order();
+}
+template <int DK>
+__device__ __forceinline__ void store_state_mx(const f32x16 (&S)[DK / 32], void *pool, uint8_t *scales,
+                                               long long base, int Dv, char *lds, int lane) {
+    asm volatile("" : "+v"(lane));  // as in store_state
+    char *const code = lds + (lane >> 5) * 8 * kMxBlock + map32(lane & 31);
+    char *const scale = lds + DK * kMxBlock + (lane >> 5) * 8;
+#pragma unroll
+    for (int it = 0; it < DK / 32; ++it)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = it * 32 + (r >> 3) * 16 + (r & 7);
+            const uint32_t eb = mx_exponent(half_max(mx_top_bits(S[it][r])));
+            code[row * kMxBlock] = (char)mx_code_bits(S[it][r], mx_inverse(eb));
+            scale[row] = (char)eb;  // the same from 32 lanes
+            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+    wave_in_order();
+    char *p = static_cast<char *>(pool) + base;
+    uint8_t *sc = scales + base / kMxBlock;
+#pragma unroll
+    for (int m = 0; m < DK / 32; ++m)
+        *reinterpret_cast<u32x4 *>(p + (uint32_t)((m * 32 + lane / 2) * Dv + lane % 2 * 16)) =
+            *reinterpret_cast<const u32x4 *>(lds + (m * 64 + lane) * 16);
+#pragma unroll
+    for (int m = 0; m < DK / 64; ++m)
+        sc[(uint32_t)((m * 64 + lane) * (Dv / kMxBlock))] = (uint8_t)lds[DK * kMxBlock + m * 64 + lane];
+    wave_in_order();
 }
 
 // Which (entry, segment, value head, columns) a workgroup works on. A unit is what shares a query/key
@@ -370,6 +425,9 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     if (!en.state) return;
     if (t_begin >= t_end && t_begin != 0) return;  // the first segment commits the state of no token
 
+    // The wave's share of q's place: free before the first chunk, and from the scores on until the next.
+    static_assert(4 * mx_lds_bytes<DK>() <= kChunk * RQ, "8-bit states pass through q's rows");
+    char *const lmx = lq + wave * mx_lds_bytes<DK>();
     f32x16 S[DK / 32];
     const long long base = ((long long)__builtin_amdgcn_readfirstlane(en.slot) * a.Hv + h) * DK * a.Dv + col0;
     if (mine) {
@@ -385,24 +443,25 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     for (int e = 0; e < 4; ++e) S[it][m * 4 + e] = x[e];
                 }
         } else if (p.state_dtype == RGDR_F32) {
-            load_state<DK, RGDR_F32>(S, a.pool, a.scales, base, a.Dv, lane);
+            load_state<DK, RGDR_F32>(S, a.pool, base, a.Dv, lane);
         } else if (p.state_dtype == RGDR_BF16) {
-            load_state<DK, RGDR_BF16>(S, a.pool, a.scales, base, a.Dv, lane);
+            load_state<DK, RGDR_BF16>(S, a.pool, base, a.Dv, lane);
         } else {
-            load_state<DK, RGDR_MXI8>(S, a.pool, a.scales, base, a.Dv, lane);
+            load_state_mx<DK>(S, a.pool, a.scales, base, a.Dv, lmx, lane);
         }
     }
     auto commit = [&]() {
         if (!mine) return;
         if (p.state_dtype == RGDR_F32)
-            store_state<DK, RGDR_F32>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+            store_state<DK, RGDR_F32>(S, a.pool_out, base, a.Dv, lane);
         else if (p.state_dtype == RGDR_BF16)
-            store_state<DK, RGDR_BF16>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+            store_state<DK, RGDR_BF16>(S, a.pool_out, base, a.Dv, lane);
         else
-            store_state<DK, RGDR_MXI8>(S, a.pool_out, a.scales_out, base, a.Dv, lane);
+            store_state_mx<DK>(S, a.pool_out, a.scales_out, base, a.Dv, lmx, lane);
     };
     if (t_begin == 0 && en.n == 0 && !a.in_place) commit();
     if (t_begin >= t_end) return;
+    if (p.state_dtype == RGDR_MXI8) __syncthreads();  // every wave's state is through q's place
 
     // A chunk ends after 64 tokens, at the accepted count (whose state is committed) or at the end.
     auto chunk_end = [&](int t) { return min(min(t + kChunk, t_end), t < en.n ? en.n : t_end); };
