@@ -7,11 +7,11 @@
 // which is the recurrence, regrouped into four dense products for the matrix cores. Exponents are
 // differences of sums held in fp64, so a chunk may decay by any amount.
 //
-// Precision: q, k and v are bf16 and enter the products as they are. What is computed enters as a
-// sum of bf16 numbers: the state and the scores as two (2^-16 of each, far below the output's
-// bf16 rounding), the scaled v of the state's update as two as well for a bf16 state, and as three
-// (2^-24) where the state leaves in fp32, or in 8 bits, whose values near a step's middle go by
-// what the sum is good to (142 and 141 against 128 us for B=16, T=1024, H=16/32, D=128). The state is kept in fp32 over the whole prompt.
+// Precision: q, k and v are bf16 and enter the products as they are. What is computed (the state, the
+// scores, the weighted v of the state's update) enters as the sum of three bf16 numbers, which hold
+// fp32's 24 bits, so that outputs and states are good to fp32 also where large terms cancel. (With two
+// numbers, 16 bits, in all three places B=16, T=1024, H=16/32, D=128 took 128 us against 155 for a bf16
+// state.) The state is kept in fp32 over the whole prompt.
 #include "la_mfma.h"
 
 namespace rgdr {
@@ -212,7 +212,7 @@ __device__ __forceinline__ void interleave() {
 
 // S += sum_s k_s (w_s v_s)^T over the 64 tokens of a chunk: k from LDS, v's operands in registers, one
 // weight for each token in LDS.
-template <int DK, bool THREE>
+template <int DK>
 __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const bf16x8 (&vf)[4],
                                           const float *weight, int lane) {
     constexpr int KP = DK / 8;
@@ -238,7 +238,7 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
             x[2 * e + 1] = bf16_hi(v[e]) * wf[kb & 1][e / 2][2 * e % 4 + 1];
         }
         split2(x, hi[kb & 1], lo[kb & 1]);
-        if constexpr (THREE) lo2[kb & 1] = split_rest(x, lo[kb & 1]);
+        lo2[kb & 1] = split_rest(x, lo[kb & 1]);
     };
     load_w(0);
     load_k(0);
@@ -252,16 +252,14 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
             weigh(kb + 1);
         }
         if (kb < 2) load_w(kb + 2);
-        if constexpr (THREE)
 #pragma unroll
-            for (int it = 0; it < NI; ++it)
-                S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2[kb & 1]), S[it]);
+        for (int it = 0; it < NI; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo2[kb & 1]), S[it]);
 #pragma unroll
         for (int it = 0; it < NI; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, lo[kb & 1]), S[it]);
 #pragma unroll
         for (int it = 0; it < NI; ++it) S[it] = mfma(kf[kb & 1][it], __builtin_bit_cast(bf16x8, hi[kb & 1]), S[it]);
-        // a step: eight values, weighted and split, 5 instructions each, or 8 with the third part
-        interleave<2 * NI, (THREE ? 3 : 2) * NI, (THREE ? 64 : 40) / ((THREE ? 3 : 2) * NI)>();
+        // a step: eight values, weighted and split, 8 instructions each
+        interleave<2 * NI, 3 * NI, 64 / (3 * NI)>();
     }
 }
 
@@ -270,7 +268,7 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
 // decay from it to the segment's end, so nothing is rescaled in between. A segment that another one
 // of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 35.5 us for 16
 // segments of 8 chunks, of which the last states' way out and the first loads are a third.
-template <int DK, bool FULL, bool THREE>
+template <int DK, bool FULL>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8, NR = kChunk * KP / 256, NV = kChunk * 16 / 256;
     constexpr int RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>();
@@ -341,7 +339,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(cons
             bf16x8 vf[4];
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
-            add_chunk<DK, THREE>(S, lk, vf, keep[buf], lane);
+            add_chunk<DK>(S, lk, vf, keep[buf], lane);
         }
         __syncthreads();
         buf ^= 1;
@@ -365,31 +363,31 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(cons
         p.seg_decay[(long long)seg * a.B * a.Hv + bh] = __builtin_amdgcn_exp2f((float)behind);
 }
 
-// Bound: for each SIMD and chunk, two waves' vector instructions (about 760 each, a quarter of them the
-// state's split, a fifth the weighted values') and products (82 of 32 cycles, 98 with fp32 and 8-bit
-// states) together fill nine tenths of the cycles, at 1.96 GHz: B=16, H=16/32, T=1024, D=128, bf16 128
-// us (3.4 TB/s, 268 TFLOP/s of the recurrence). One workgroup alone on a compute unit runs at 2.38 GHz
-// and takes 3.9 us for a chunk, two 7.9 us for two.
+// Bound: for each SIMD and chunk, two waves' vector instructions and products (119 of 32 cycles for each
+// wave), which overlap only in part. B=16, H=16/32, T=1024, D=128, bf16 155 us (2.8 TB/s, 221 TFLOP/s of
+// the recurrence).
 //
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
 // chunk's q, k and v lie in LDS, and the waves share the ten 16 x 16 tiles of the scores, two or three
 // each; one with two also sums the next chunk's decays. The next chunk's rows are in flight meanwhile.
 //
-// FULL: D_v is a multiple of 128, so every wave has columns. THREE: the state leaves in fp32 or 8 bits. Both are
-// template arguments so that a chunk is a few long stretches of code without branches, in which
-// the products and the vector work around them can be interleaved.
-template <int DK, bool SEGMENTS, bool FULL, bool THREE>
+// FULL: D_v is a multiple of 128, so every wave has columns; a template argument, so that a chunk is a
+// few long stretches of code without branches, in which the products and the vector work around them
+// can be interleaved.
+template <int DK, bool SEGMENTS, bool FULL>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const LaArgs a, const LaPlan p) {
     constexpr int KP = DK / 8;                 // 16-byte pieces of a q or k row
     constexpr int NR = kChunk * KP / 256;      // of them in each thread's hands
     constexpr int NV = kChunk * 16 / 256;
-    constexpr int RQ = lds_row_bytes<KP>(), RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>(),
-                  RP = lds_row_bytes<8>();
+    constexpr int RQ = lds_row_bytes<KP>(), RK = lds_row_bytes<KP, kTrPad>(), RV = lds_row_bytes<16, kTrPad>();
+    // Scores: 32 rows of the 32 tokens that they may see, then 32 of all 64, each with a spare piece. (Rows of
+    // one length for all would take the second workgroup's place on the compute unit at D_k = 128.)
+    constexpr int RP0 = 5 * 16, RP1 = 9 * 16, kPlane = 32 * (RP0 + RP1);
     __shared__ __align__(256) char lq[kChunk * RQ];
     __shared__ __align__(256) char lk[kChunk * RK];
     __shared__ __align__(256) char lv[kChunk * RV];
-    __shared__ __align__(256) char lp[2][kChunk * RP];
+    __shared__ __align__(256) char lp[3][kPlane];
     // Of each token of this chunk and the next: the log2 decay sum in two floats, what a later
     // state keeps of it, and what it keeps of the incoming state (with the scale).
     __shared__ __align__(16) float g_hi[2][kChunk], g_lo[2][kChunk], keep[2][kChunk], carry[2][kChunk];
@@ -524,9 +522,9 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
     };
 
     // The two tiles above the diagonal that the products of 32 tokens by 32 read: zero for good.
-    for (int j = tid; j < 2 * 2 * 16 * 2; j += 256) {
-        const int plane = j >> 6, half = j >> 5 & 1, row = j >> 1 & 15, piece = j & 1;
-        *reinterpret_cast<u32x4 *>(lp[plane] + (half * 32 + row) * RP + (half * 4 + 2 + piece) * 16) =
+    if (tid < 3 * 2 * 16 * 2) {
+        const int plane = tid >> 6, half = tid >> 5 & 1, row = tid >> 1 & 15, piece = tid & 1;
+        *reinterpret_cast<u32x4 *>(lp[plane] + (half ? 32 * RP0 + row * RP1 + 96 : row * RP0 + 32) + piece * 16) =
             u32x4{0, 0, 0, 0};
     }
 
@@ -597,13 +595,14 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     asm volatile("" : "+v"(w));  // formed for every lane: no branch around it
                     y[e] = s + e <= t ? x[j][e] * w : 0.f;  // columns t past the chunk are not stored
                 }
-                u32x2 hi = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-                bf16_rest(hi[0], y[0], y[1]);
-                bf16_rest(hi[1], y[2], y[3]);
-                u32x2 lo = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-                const int at = t * RP + s * 2;
-                *reinterpret_cast<u32x2 *>(lp[0] + at) = hi;
-                *reinterpret_cast<u32x2 *>(lp[1] + at) = lo;
+                const int at = wave + 4 * j < 7 ? 32 * RP0 + (t - 32) * RP1 + s * 2 : t * RP0 + s * 2;
+#pragma unroll
+                for (int pl = 0; pl < 3; ++pl) {
+                    const u32x2 part = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+                    *reinterpret_cast<u32x2 *>(lp[pl] + at) = part;
+                    bf16_rest(part[0], y[0], y[1]);
+                    bf16_rest(part[1], y[2], y[3]);
+                }
             }
         };
         if (wave < 2) {
@@ -631,25 +630,26 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) vf[kb] = lds_read_tr<16, kTrPad>(lv, kb * 16, wave, lane);
             bf16x8 qf[2][2];
-            u32x4 hi[2], lo[2];
+            u32x4 hi[2], lo[2], lo2[2];
             auto load = [&](int c) {
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) qf[c & 1][tt] = lds_read(lq + lds_at<KP>(tt * 32 + col, c * 2 + hf));
             };
-            auto halves = [&](int c) {
+            auto parts = [&](int c) {
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = S[c / 2][(c & 1) * 8 + e];
                 split2(x, hi[c & 1], lo[c & 1]);
+                lo2[c & 1] = split_rest(x, lo[c & 1]);
             };
             load(0);
-            halves(0);
+            parts(0);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int c = 0; c < NS; ++c) {
                 if (c + 1 < NS) {
                     load(c + 1);
-                    halves(c + 1);
+                    parts(c + 1);
                 }
                 if constexpr (LOADS)
 #pragma unroll
@@ -666,11 +666,13 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(hi[c & 1], qf[c & 1][tt], o[tt]);
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo[c & 1], qf[c & 1][tt], o[tt]);
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) o[tt] = mfma(lo2[c & 1], qf[c & 1][tt], o[tt]);
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 6; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                    if (LOADS && i % 2) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                    if (LOADS && i % 3 == 1) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
                     __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -691,14 +693,14 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
         __syncthreads();
         if (mine) {
             // (second tokens, s block 3), (2), then both halves for blocks 1 and 0
-            bf16x8 pf[2][4];
+            bf16x8 pf[2][6];
             auto load = [&](int kb) {
 #pragma unroll
                 for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
 #pragma unroll
-                    for (int pl = 0; pl < 2; ++pl)
-                        pf[kb & 1][tt * 2 + pl] =
-                            lds_read(lp[pl] + lds_at<8>(tt * 32 + col, kb * 2 + hf));
+                    for (int pl = 0; pl < 3; ++pl)
+                        pf[kb & 1][tt * 3 + pl] =
+                            lds_read(lp[pl] + (tt ? 32 * RP0 + col * RP1 : col * RP0) + (kb * 2 + hf) * 16);
             };
             load(3);
             const float d = whole[buf];
@@ -714,14 +716,14 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                 for (int it = kb * DK / 128; it < (kb + 1) * DK / 128; ++it)
                     asm volatile("" : "+v"(S[it]));  // here, among the products
 #pragma unroll
-                for (int pl = 0; pl < 2; ++pl)
+                for (int pl = 0; pl < 3; ++pl)
 #pragma unroll
                     for (int tt = kb < 2 ? 0 : 1; tt < 2; ++tt)
-                        o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 2 + pl], o[tt]);
+                        o[tt] = mfma(__builtin_bit_cast(u32x4, vf[kb]), pf[kb & 1][tt * 3 + pl], o[tt]);
                 if (kb < 2)
-                    interleave<4, 4, 4>();
+                    interleave<6, 6, 3>();
                 else
-                    interleave<4, 2, 8>();
+                    interleave<6, 3, 6>();
             }
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
@@ -737,7 +739,7 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_chunk_kernel(const 
                     }
                 }
             if (t1 < t_end || t1 == en.n) {
-                add_chunk<DK, THREE>(S, lk, vf, keep[buf], lane);
+                add_chunk<DK>(S, lk, vf, keep[buf], lane);
             }
         }
         if (t1 == en.n) commit();
@@ -842,7 +844,7 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
     return true;
 }
 
-template <int DK, bool FULL, bool THREE>
+template <int DK, bool FULL>
 static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream) {
     p.tiles = (a.Dv + kCols - 1) / kCols;
     // whole rounds of units over the XCDs
@@ -851,27 +853,24 @@ static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream)
     const unsigned items = (unsigned)(units * a.group * p.tiles);
     const dim3 block(256);
     if (p.nseg == 1) {
-        hipLaunchKernelGGL((la_chunk_kernel<DK, false, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+        hipLaunchKernelGGL((la_chunk_kernel<DK, false, FULL>), dim3(items), block, 0, stream, a, p);
         return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
     }
     const unsigned scan = (unsigned)(((long long)a.B * a.Hv * (a.Dv * DK / 4) + 255) / 256);
-    hipLaunchKernelGGL((la_segment_kernel<DK, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_segment_kernel<DK, FULL>), dim3(items), block, 0, stream, a, p);
     if (p.state_dtype == RGDR_F32)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_F32>, dim3(scan), block, 0, stream, a, p, DK);
     else if (p.state_dtype == RGDR_BF16)
         hipLaunchKernelGGL(la_scan_kernel<RGDR_BF16>, dim3(scan), block, 0, stream, a, p, DK);
     else
         hipLaunchKernelGGL(la_scan_kernel<RGDR_MXI8>, dim3(scan), block, 0, stream, a, p, DK);
-    hipLaunchKernelGGL((la_chunk_kernel<DK, true, FULL, THREE>), dim3(items), block, 0, stream, a, p);
+    hipLaunchKernelGGL((la_chunk_kernel<DK, true, FULL>), dim3(items), block, 0, stream, a, p);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 template <int DK>
 static rgdr_status launch_prefill_dk(const LaArgs &a, const LaPlan &p, hipStream_t stream) {
-    const bool three = p.state_dtype != RGDR_BF16;
-    if (a.Dv % kCols == 0)
-        return three ? launch_prefill<DK, true, true>(a, p, stream) : launch_prefill<DK, true, false>(a, p, stream);
-    return three ? launch_prefill<DK, false, true>(a, p, stream) : launch_prefill<DK, false, false>(a, p, stream);
+    return a.Dv % kCols == 0 ? launch_prefill<DK, true>(a, p, stream) : launch_prefill<DK, false>(a, p, stream);
 }
 
 }  // namespace rgdr
