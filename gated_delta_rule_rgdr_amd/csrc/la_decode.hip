@@ -198,8 +198,9 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
 // blocks of 32 columns for each wave. A wave moves 32 rows at a time, in whole lines (16 bytes for
 // each lane, up to 128 for each row), through LDS into the layout of the products' results,
 // transposed (lanes: rows i, registers: columns j), and back; as bf16 they become an operand of
-// S^T q on the way. The tokens are a quarter of the products' 32 columns; the products are far
-// from bounding the call all the same (30 of them, under 0.5 us, for 4096 elements, whose bytes
+// S^T q on the way. What fp32 holds (fp32 states, scores, weighted values) enters the products as the
+// sum of three bf16 numbers, 24 bits; two for the states and scores were no faster. The tokens are a quarter of the products' 32 columns; the products are far
+// from bounding the call all the same (32 to 40 of them, under 0.6 us, for 4096 elements, whose bytes
 // take a compute unit 0.4 to 1.6 us). H_v = 32, D = 128, B = 32, T = 8: fp32 29.9 us (4.7 TB/s), bf16
 // 16.1 us (4.6), 8 bits 15.7 us (2.6: vector work, as above). Read and written straight in the products'
 // layout, 32 rows apart from lane to lane, the same took 46, 29 and 28 us; on the vector units
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     constexpr int KP = DK / 8;                          // 16-byte pieces of a q or k row
     constexpr int NI = DK / 32;                         // tiles of 32 rows
     constexpr int NT = 256 / CB, NW = 4 / CB;
-    constexpr int PL = ST == RGDR_F32 ? 2 : 1;          // bf16 and 8-bit states are whole bf16 numbers
+    constexpr int PL = ST == RGDR_F32 ? 3 : 1;          // bf16 and 8-bit states are whole bf16 numbers
     constexpr int kSize = ST == RGDR_F32 ? 4 : ST == RGDR_BF16 ? 2 : 1;
     constexpr int WP = 2 * kSize;                       // words of 8 columns
     constexpr int PC = CB * 2 * kSize;                  // 16-byte pieces of the wave's part of a row
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         x = mfma(__builtin_bit_cast(u32x4, lds_read(lk + lds_at<KP>(col & 7, c * 2 + hf))),
                  lds_read(lq + lds_at<KP>(col & 7, c * 2 + hf)), x);
     float y[8];
-    u32x4 p_hi, p_lo;
+    u32x4 p_hi, p_lo, p_lo2;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const uint32_t z = __float_as_uint(gap[r] != 0.f ? x[r] * gap[r] : 0.f);
@@ -326,6 +327,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         y[r + 4] = hf ? 0.f : __uint_as_float(sw[1]);
     }
     split2(y, p_hi, p_lo);
+    p_lo2 = split_rest(y, p_lo);
     // values: lanes j, eight tokens in each lane (the upper lanes' have no weight), and the same
     // weighted for the state
     u32x4 vf[CB], v_hi[CB], v_lo[CB], v_lo2[CB];
@@ -392,7 +394,8 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
 #pragma unroll
                     for (int e = 0; e < 8; ++e) rest[e] = s[kb][e];
                     split2(rest, hi, lo);
-                    *reinterpret_cast<u32x4 *>(ls[wave][PL - 1] + pa) = lo;
+                    *reinterpret_cast<u32x4 *>(ls[wave][PL - 2] + pa) = lo;
+                    *reinterpret_cast<u32x4 *>(ls[wave][PL - 1] + pa) = split_rest(rest, lo);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -473,6 +476,7 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
     for (int cb = 0; cb < CB; ++cb) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[cb][r] *= carry;
+        o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_lo2), o[cb]);
         o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_lo), o[cb]);
         o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_hi), o[cb]);
         if (col < L) {

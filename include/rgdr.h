@@ -395,7 +395,8 @@ typedef struct { int64_t b, h, t; } la_strides;
  *                 state_pool and state_scales (in place: then a slot whose entry accepts no token
  *                 keeps its bytes); any other overlap is undefined.
  *
- * The arithmetic is fp32; the state is rounded once, when it is committed. RGDR_MXI8 commits
+ * The arithmetic is fp32 (what it computes enters matrix products as three bf16 numbers, which hold
+ * its 24 bits); the state is rounded once, when it is committed. RGDR_MXI8 commits
  * choose for each block of 32 columns the smallest power of two with which its largest value
  * fits +-127, and round to nearest even; a block that holds a NaN, an infinity or a magnitude
  * above 127 * 2^121 (the last that 8 bits and fp32 both hold) becomes NaN, with byte 255.

@@ -6,7 +6,7 @@ import torch
 from la_util import BF16_HALF
 
 pytestmark = pytest.mark.gpu
-CALLS = [("la_prefill", 3), ("la_prefill", 65), ("la_prefill", 700)]  # the last in segments
+CALLS = [("la_decode", 3), ("la_decode", 8), ("la_prefill", 3), ("la_prefill", 65), ("la_prefill", 700)]  # the last in segments
 
 
 @pytest.fixture(scope="module")
