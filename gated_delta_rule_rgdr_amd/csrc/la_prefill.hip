@@ -23,6 +23,7 @@ constexpr int kCols = 128;    // columns of one workgroup: 32 for each of its 4 
 
 struct LaPlan {
     int state_dtype, tiles, seg_len, nseg;
+    int per;           // workgroups of a unit, which run on one XCD
     float *seg_state;  // [nseg][B*H_v][D_v/32][D_k/32][4][64][4]: accumulator layout
     float *seg_decay;  // [nseg][B*H_v]
 };
@@ -156,7 +157,8 @@ __device__ __forceinline__ void store_state_mx(const f32x16 (&S)[DK / 32], void 
 // L2. Units go round the XCDs (workgroup ids do), those of the longest entries first: with
 // ragged lengths every XCD, and every compute unit's two places, then get long and short ones.
 // (B=16, H=16/32, D=128, lengths from 0 to 1024: 101.5 us, against 108.2 with each XCD's units
-// contiguous, both before the work between the products below.)
+// contiguous, both before the work between the products below.) Where units do not go round the XCDs
+// evenly, each workgroup is a unit of its own (launch_prefill).
 struct LaItem {
     int b, seg, h, tile;
     bool live;
@@ -176,12 +178,16 @@ __device__ __forceinline__ int entry_of_rank(const LaArgs &a, int rank) {
 
 template <bool SEGMENTS>
 __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
-    const int per = a.group * p.tiles, local = blockIdx.x / kXcds;
-    int unit = local / per * kXcds + blockIdx.x % kXcds;
+    const int local = blockIdx.x / kXcds, share = a.group * p.tiles;  // workgroups of a query/key head
+    int unit = local / p.per * kXcds + blockIdx.x % kXcds, in_group = local % p.per;
     LaItem m;
-    m.tile = local % per % p.tiles;
-    const int in_group = local % per / p.tiles;
-    m.live = unit < a.B * a.Hq * (SEGMENTS ? p.nseg : 1);
+    m.live = unit < a.B * a.Hq * (SEGMENTS ? p.nseg : 1) * (share / p.per);
+    if (p.per == 1) {
+        in_group = unit % share;
+        unit /= share;
+    }
+    m.tile = in_group % p.tiles;
+    in_group /= p.tiles;
     const int hq = unit % a.Hq;
     unit /= a.Hq;
     m.seg = SEGMENTS ? unit % p.nseg : 0;
@@ -847,10 +853,16 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
 template <int DK, bool FULL>
 static rgdr_status launch_prefill(const LaArgs &a, LaPlan p, hipStream_t stream) {
     p.tiles = (a.Dv + kCols - 1) / kCols;
-    // whole rounds of units over the XCDs
-    const long long units = ((long long)a.B * a.Hq * p.nseg + kXcds - 1) / kXcds * kXcds;
-    if (units * a.group * p.tiles > kMaxGroups) return RGDR_ERR_SHAPE;
-    const unsigned items = (unsigned)(units * a.group * p.tiles);
+    const long long units = (long long)a.B * a.Hq * p.nseg, share = (long long)a.group * p.tiles;
+    // Units of whole query/key heads leave XCDs idle where there are few of them, and whole rounds of them
+    // can be more workgroups than a launch takes; workgroups one by one meet neither, and read q and k
+    // into more than one L2. One by one where more than a fifth of the rounds is empty (T=1024, D=128, bf16, heads
+    // together / one by one, us: B=1 H=1/128 227/74, B=4 H=1/64 131/82, B=5 131/120, B=12 H=1/32
+    // 133/126; with less empty B=13 133/135, B=20 201/207, B=16 H=16/32 154.6/157.7).
+    const long long rounds = (units + kXcds - 1) / kXcds * kXcds;  // whole rounds over the XCDs
+    const bool even = rounds * 4 <= units * 5 && rounds * share <= kMaxGroups;
+    p.per = even ? (int)share : 1;
+    const unsigned items = (unsigned)((even ? rounds : units) * share);  // at most kMaxGroups: la_check_sizes
     const dim3 block(256);
     if (p.nseg == 1) {
         hipLaunchKernelGGL((la_chunk_kernel<DK, false, FULL>), dim3(items), block, 0, stream, a, p);
