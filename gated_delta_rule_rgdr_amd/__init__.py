@@ -5,7 +5,7 @@ Argument marshalling only: every step of the computation runs in the HIP kernels
 fallback: if the library is missing, the first call of any binding function raises
 ``ImportError``. The ``rgdr_`` calls and ``la_gate`` go through ctypes, the linear-attention calls
 through the CPython module ``_la_binding`` (``csrc/la_binding.cpp``), which checks and calls; where
-it finds that a call does not fit, the checks here say why.
+it finds that a call does not fit, the checks here say why. It is loaded by the first of those calls.
 
 * ``rgdr_decode``  -- the recurrent gated-delta-rule decode step (MindSpore Lite API page
   "lite_boost.ops.recurrent_gated_delta_rule"), in place on a bf16 state pool.
@@ -68,7 +68,7 @@ VALIDATE = os.environ.get("RGDR_VALIDATE", "") == "1"
 
 def library():
     """Load ``librgdr.so`` (built by ``gated_delta_rule_rgdr_amd/build.py``)."""
-    global _lib, _quick
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -123,10 +123,16 @@ def library():
     lib.rgdr_validate_host.argtypes = [vp, vp, vp, i32, i32, i32]
     lib.rgdr_status_string.restype = C.c_char_p
     lib.rgdr_status_string.argtypes = [C.c_int]
-    from . import _la_binding
-    _quick = _la_binding
     _lib = lib
     return lib
+
+
+def _load_quick():
+    """Load the CPython module of the linear-attention calls; the others do without it."""
+    global _quick
+    library()
+    from . import _la_binding
+    _quick = _la_binding
 
 
 def status_string(code: int) -> str:
@@ -638,8 +644,8 @@ def _raw_stream(t, stream):
 
 def _la_call(fn, query, key, value, g, state_pool, lens, idx, nacc, scale, state_scales, out,
              state_out, state_scales_out, stream, workspace=None):
-    if _lib is None:
-        library()
+    if _quick is None:
+        _load_quick()
     if state_out is None:
         if state_scales_out is not None:
             raise RuntimeError("state_scales_out goes with state_out")
@@ -786,8 +792,8 @@ def la_state_dequantize(codes, scales, state=None, *, dtype=torch.bfloat16, src_
 
 
 def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
-    if _lib is None:
-        library()
+    if _quick is None:
+        _load_quick()
     rc = _quick.move(fn == "la_state_dequantize", state, codes, scales, src_slots, dst_slots, n,
                      _raw_stream(state, stream))
     if rc is None:
@@ -815,8 +821,8 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
     contiguous and rows at multiples of 8 elements, D a multiple of 8 up to 8192. ``weight``
     float32 ``[D]`` or ``[H,D]``. Returns ``out``, ``[B,T,H,D]`` of x's type; rows of tokens past
     ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
-    if _lib is None:
-        library()
+    if _quick is None:
+        _load_quick()
     if stream is not None and out is None and isinstance(x, torch.Tensor) and x.dim() == 4:
         B, H, T, D = x.shape
         out = _empty((B, T, H, D), x.dtype, x.device, stream)
