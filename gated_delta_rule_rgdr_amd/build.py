@@ -51,24 +51,8 @@ def binding_cmds(obj):
     return compile_, link
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    procs = []
-    objs = []
-    for s in SOURCES:
-        src = os.path.join(CSRC, s)
-        obj = os.path.join(BUILD_DIR, os.path.splitext(s)[0] + ".o")
-        cmd = compile_cmd(src, obj, extra)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((s, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-        objs.append(obj)
-    binding_obj = os.path.join(BUILD_DIR, "la_binding.o")
-    binding_compile, binding_link = binding_cmds(binding_obj)
-    if verbose:
-        print(" ".join(binding_compile), flush=True)
-    procs.append(("la_binding.cpp", subprocess.Popen(binding_compile, stdout=subprocess.PIPE,
-                                                     stderr=subprocess.STDOUT)))
+def _finish(procs, verbose):
+    """The sources whose compilation failed."""
     failed = []
     for s, p in procs:
         out, _ = p.communicate()
@@ -81,17 +65,46 @@ def build(verbose: bool = False, extra=()) -> str:
             failed.append(s)
     if failed:
         raise RuntimeError(f"the compiler failed for {failed}")
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    """Both libraries. ``librgdr.so`` needs neither Python's nor torch's headers and is in place when
+    an error of the other one is raised."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    procs = []
+    objs = []
+    for s in SOURCES:
+        src = os.path.join(CSRC, s)
+        obj = os.path.join(BUILD_DIR, os.path.splitext(s)[0] + ".o")
+        cmd = compile_cmd(src, obj, extra)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        procs.append((s, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        objs.append(obj)
+    _finish(procs, verbose)
     tmp = LIB + ".tmp"
     link = ["hipcc", f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
-    if verbose:
-        print(" ".join(binding_link), flush=True)
-    subprocess.run(binding_link, check=True)
-    os.replace(BINDING + ".tmp", BINDING)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The CPython module, against a built ``librgdr.so``."""
+    obj = os.path.join(BUILD_DIR, "la_binding.o")
+    compile_, link = binding_cmds(obj)
+    if verbose:
+        print(" ".join(compile_), flush=True)
+    _finish([("la_binding.cpp", subprocess.Popen(compile_, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT))], verbose)
+    if verbose:
+        print(" ".join(link), flush=True)
+    subprocess.run(link, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -21,3 +21,23 @@ def test_other_calls_do_without_the_module(monkeypatch):
         rg.la_decode(x, x, x, torch.zeros(1, 2, 3), torch.zeros(1, 2, 64, 64))
     with pytest.raises(ImportError):
         rg.la_norm_gate(x, torch.ones(64))
+
+
+@pytest.mark.parametrize("missing", ["compiler error", "no torch"])
+def test_the_library_is_built_without_the_module(monkeypatch, tmp_path, missing):
+    """Where the module cannot be compiled, or torch's headers are missing, librgdr.so is linked all the
+    same, and the error is raised."""
+    from gated_delta_rule_rgdr_amd import build
+
+    def commands(obj):
+        if missing == "no torch":
+            raise ImportError("torch")
+        return ["false"], ["false"]
+    monkeypatch.setattr(build, "SOURCES", ["rgdr_host.cpp"])
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "librgdr.so"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_la_binding.so"))
+    monkeypatch.setattr(build, "binding_cmds", commands)
+    with pytest.raises((RuntimeError, ImportError), match="la_binding.cpp|torch"):
+        build.build()
+    assert (tmp_path / "librgdr.so").exists() and not (tmp_path / "_la_binding.so").exists()
