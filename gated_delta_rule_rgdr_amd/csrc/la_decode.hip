@@ -194,6 +194,11 @@ __global__ __launch_bounds__(256) void la_step_kernel(const LaArgs a, int tiles)
     }
 }
 
+// Neither of the two is NaN or an infinity.
+__device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
+    return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+}
+
 // 2 to 8 tokens, on the matrix cores: one workgroup for each (entry, value head, 128 columns), CB
 // blocks of 32 columns for each wave. A wave moves 32 rows at a time, in whole lines (16 bytes for
 // each lane, up to 128 for each row), through LDS into the layout of the products' results,
@@ -342,6 +347,21 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         split2(y, v_hi[cb], v_lo[cb]);
         v_lo2[cb] = split_rest(y, v_lo[cb]);
     }
+    // A value that is not finite would meet the zero scores of the tokens before its own: it is a 0 in the
+    // product, and is added behind it.
+    bool odd = false;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= !finite_bf16x2(vf[cb][e]);
+    odd = __any(odd);
+    if (odd)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                vf[cb][e] = (finite_bf16x2(vf[cb][e] & 0xFFFFu) ? vf[cb][e] & 0xFFFFu : 0u) |
+                            (finite_bf16x2(vf[cb][e] & 0xFFFF0000u) ? vf[cb][e] & 0xFFFF0000u : 0u);
 
     f32x16 o[CB] = {};
     const bool store = n || !a.in_place;
@@ -479,6 +499,23 @@ __global__ __launch_bounds__(256 / CB) void la_tokens_kernel(const LaArgs a, int
         o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_lo2), o[cb]);
         o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_lo), o[cb]);
         o[cb] = mfma(vf[cb], __builtin_bit_cast(bf16x8, p_hi), o[cb]);
+        if (odd)
+            for (int s = 0; s < L; ++s) {
+                // of token t = lane % 32; the rest of it changes no infinity
+                const uint32_t hi = s < 2 ? p_hi[0] : s < 4 ? p_hi[1] : s < 6 ? p_hi[2] : p_hi[3];
+                const float score = __shfl(s & 1 ? bf16_hi(hi) : bf16_lo(hi), col);
+                if (s > col) continue;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(
+                        lv + lds_at<16>(s, (wave * CB + cb) * 4 + m * 2 + hf));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float x = e & 1 ? bf16_hi(v[e / 2]) : bf16_lo(v[e / 2]);
+                        if (!__builtin_isfinite(x)) o[cb][m * 8 + e] += score * x;
+                    }
+                }
+            }
         if (col < L) {
             uint16_t *row = go + col * a.so.t + (wave * CB + cb) * 32 + hf * 8;
 #pragma unroll

@@ -400,9 +400,10 @@ typedef struct { int64_t b, h, t; } la_strides;
  * choose for each block of 32 columns the smallest power of two with which its largest value
  * fits +-127, and round to nearest even; a block that holds a NaN, an infinity or a magnitude
  * above 127 * 2^121 (the last that 8 bits and fp32 both hold) becomes NaN, with byte 255.
- * Inputs of valid tokens are taken to be finite: outputs of other tokens of the same entry may
- * see a NaN or an infinity among them, the state only those of accepted tokens. Padded tokens and
- * skipped entries are never read.
+ * A NaN or an infinity in a valid token shows in its own output and may show in those of the tokens behind
+ * it, and in the state if the token is accepted. (la_prefill's outputs of up to 63 tokens before
+ * it may see it too, but not accepted tokens' outputs that of a rejected one.) Padded tokens and skipped
+ * entries are never read.
  * Errors: RGDR_ERR_NULL; RGDR_ERR_SHAPE (sizes, negative strides, overlapping out rows, no
  * slot indices with N_slots < B); RGDR_ERR_UNSUPPORTED (D_k, D_v); RGDR_ERR_DTYPE
  * (state_dtype); RGDR_ERR_ALIGN; RGDR_ERR_HIP.

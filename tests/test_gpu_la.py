@@ -742,3 +742,25 @@ def test_empty_calls(rg):
     assert codes.shape == (0, 2, 64, 64)
     assert rg.la_state_dequantize(codes, scales).shape == (0, 2, 64, 64)
     assert rg.la_norm_gate(q, torch.ones(64, device="cuda")).shape == (0, 3, 2, 64)
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("Dv,B", [(96, 2), (64, 70)])
+@pytest.mark.parametrize("T", [2, 5, 8])
+def test_tokens_do_not_reach_earlier_outputs(rg, T, Dv, B, state):
+    """NaN and infinities in a drafted token, accepted or not, leave the outputs of the tokens before it
+    as they are without them, and show in its own and in the later ones'. (B = 70: two blocks of columns for
+    each wave.)"""
+    c = Case(B, 16, 32, T, 64, Dv, state, seed=19, lens=[T] * B, acc=[T - 1 - b % 2 for b in range(B)])
+    clean = c.call(rg, "la_decode", pool=c.pool.clone(), scales=None if c.scales is None else c.scales.clone())
+    c.q, c.k, c.v, c.g = (x.clone() for x in (c.q, c.k, c.v, c.g))
+    c.v[0, :, T - 1, 5:40], c.k[0, :, T - 1, 3], c.q[0, :, T - 1, 9], c.g[0, :, T - 1] = NAN, float("inf"), NAN, NAN
+    c.v[1, :, T // 2, 7], c.v[1, :, T // 2, 41] = float("inf"), -float("inf")
+    out = c.call(rg, "la_decode")[0]
+    for b, s in ((0, T - 1), (1, T // 2)):
+        assert torch.equal(out[b, :, :s], clean[0][b, :, :s])
+        assert not torch.isfinite(out[b, :, s:, 7]).any()
+    assert not torch.isfinite(out[1, :, T // 2:, 41]).any()
+    rest = [x for x in range(Dv) if x not in (7, 41)]
+    assert torch.equal(out[1][..., rest], clean[0][1][..., rest])
+    assert torch.equal(out[2:], clean[0][2:])
