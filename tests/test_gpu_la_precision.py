@@ -1,20 +1,13 @@
-"""Linear attention where large terms cancel: what fp32 arithmetic gives, and operands of the matrix
-products that hold fewer bits than fp32 do not."""
+"""Linear attention where large terms cancel (what fp32 arithmetic gives, and operands of the matrix
+products that hold fewer bits than fp32 do not), and over many steps on rounded states."""
 import pytest
 import torch
 
-from la_util import BF16_HALF
+from la_util import BF16_HALF, c_out, c_state, mx_step
+from test_gpu_la import Case, rg  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 CALLS = [("la_decode", 3), ("la_decode", 8), ("la_prefill", 3), ("la_prefill", 65), ("la_prefill", 700)]  # the last in segments
-
-
-@pytest.fixture(scope="module")
-def rg():
-    assert torch.cuda.is_available(), "GPU tests need a GPU"
-    import gated_delta_rule_rgdr_amd as m
-    m.library()
-    return m
 
 
 def zeros(*shape):
@@ -85,3 +78,45 @@ def test_state_of_two_tokens_that_cancel(rg, fn, T, state):
     assert over.max() <= 0, f"{(over > 0).sum()} of {over.numel()} off, by {over.max():.3g} more than the bound"
     pool[0, :, 5] = 0
     assert torch.all(pool == 0)
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16", "i8"])
+def test_many_steps_against_unrounded_states(rg, state):
+    """A prompt and sixty steps of one to three tokens, against states that are never rounded. Per element
+    the error after a step is what was there, decayed, the step's own arithmetic, and the commit's rounding
+    of what it then holds; an output is off by the state's errors at its token, weighted by |q|, and its
+    own rounding."""
+    B, Hv, D = 2, 2, 64
+    steps = [40] + [1, 1, 3] * 20
+    T = sum(steps)
+    c = Case(B, 1, Hv, T, D, D, state, seed=33, N=B, lens=[T] * B, acc=[T] * B, idx=[1, 0], decay=0.2)
+    S = c.S0[c.idx.long()].double().cpu()
+    off = torch.zeros_like(S)
+    pool, scales = c.pool, c.scales
+    at = 0
+    for n in steps:
+        d = Case.__new__(Case)
+        d.__dict__.update(c.__dict__)
+        d.q, d.k, d.v, d.g = (x[:, :, at:at + n] for x in (c.q, c.k, c.v, c.g))
+        d.lens = d.acc = torch.tensor([n] * B, dtype=torch.int32)
+        out = d.call(rg, "la_prefill" if n > 8 else "la_decode", pool=pool, scales=scales)[0].double().cpu()
+        q, k, v, g = (x.double().cpu() for x in (d.q, d.k, d.v, d.g))
+        A = S.abs() + off
+        for t in range(n):
+            keep = torch.exp(g[:, :, t])[..., None, None]
+            term = k[:, :, t, :, None] * v[:, :, t, None, :]
+            S, A, off = keep * S + term, keep * A + term.abs(), keep * off
+            qt = (q[:, :, t] * c.scale).expand(B, Hv, D)[..., None]
+            ref, bound = (qt * S).sum(2), (qt.abs() * (off + c_out(n, D) * A)).sum(2)
+            over = (out[:, :, t] - ref).abs() - bound - BF16_HALF * (ref.abs() + bound)
+            assert over.max() <= 0, f"{state} token {at + t}: out off by {over.max():.3g} more than its bound"
+        off = off + c_state(n) * A
+        if state == "bf16":
+            off = off + BF16_HALF * (S.abs() + off)
+        elif state == "i8":
+            off = off + mx_step(S.abs() + off) / 2
+        got = c.values(pool, scales)[c.idx.long()].double().cpu()
+        over = (got - S).abs() - off
+        assert over.max() <= 0, f"{state} after token {at + n}: state off by {over.max():.3g} more than its bound"
+        at += n
+    assert at == T
