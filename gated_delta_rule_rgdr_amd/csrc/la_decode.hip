@@ -204,10 +204,11 @@ __device__ __forceinline__ bool finite_bf16x2(uint32_t w) {
 // each lane, up to 128 for each row), through LDS into the layout of the products' results,
 // transposed (lanes: rows i, registers: columns j), and back; as bf16 they become an operand of
 // S^T q on the way. What fp32 holds (fp32 states, scores, weighted values) enters the products as the
-// sum of three bf16 numbers, 24 bits; two for the states and scores were no faster. The tokens are a quarter of the products' 32 columns; the products are far
-// from bounding the call all the same (32 to 40 of them, under 0.6 us, for 4096 elements, whose bytes
-// take a compute unit 0.4 to 1.6 us). H_v = 32, D = 128, B = 32, T = 8: fp32 29.9 us (4.7 TB/s), bf16
-// 16.1 us (4.6), 8 bits 15.7 us (2.6: vector work, as above). Read and written straight in the products'
+// sum of three bf16 numbers, 24 bits; two for the states and scores were no faster. The tokens are a
+// quarter of the products' 32 columns; the products are far from bounding the call all the same (31 to
+// 47 of them, under 0.7 us, for 4096 elements, whose bytes take a compute unit 0.4 to 1.6 us). H_v = 32,
+// D = 128, B = 32, T = 8: fp32 30 us (4.7 TB/s), bf16 16.5 to 18 us (4.1 to 4.4), 8 bits 16 us (2.5: two trips
+// of each value through LDS, and vector work as above). Read and written straight in the products'
 // layout, 32 rows apart from lane to lane, the same took 46, 29 and 28 us; on the vector units
 // alone 60, 82 and 52.
 template <int ST, int DK, int CB>

@@ -11,7 +11,8 @@
 // scores, the weighted v of the state's update) enters as the sum of three bf16 numbers, which hold
 // fp32's 24 bits, so that outputs and states are good to fp32 also where large terms cancel. (With two
 // numbers, 16 bits, in all three places B=16, T=1024, H=16/32, D=128 took 128 us against 155 for a bf16
-// state.) The state is kept in fp32 over the whole prompt.
+// state; the comparisons of parts below were timed in that form.) The state is kept in fp32 over the
+// whole prompt.
 #include "la_mfma.h"
 
 namespace rgdr {
@@ -272,7 +273,7 @@ __device__ __forceinline__ void add_chunk(f32x16 (&S)[DK / 32], char *lk, const 
 // What one segment adds to the state behind it, from a zero state, into the workspace: the first pass
 // over a long prompt. Its chunks are taken from the last to the first, each token weighted by the
 // decay from it to the segment's end, so nothing is rescaled in between. A segment that another one
-// of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 35.5 us for 16
+// of the entry follows is full. Two chunks are in flight. B=1, H=16/32, T=8192, D=128: 37 us for 16
 // segments of 8 chunks, of which the last states' way out and the first loads are a third.
 template <int DK, bool FULL>
 __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(const LaArgs a, const LaPlan p) {
@@ -369,9 +370,12 @@ __global__ __launch_bounds__(256, DK == 256 ? 1 : 2) void la_segment_kernel(cons
         p.seg_decay[(long long)seg * a.B * a.Hv + bh] = __builtin_amdgcn_exp2f((float)behind);
 }
 
-// Bound: for each SIMD and chunk, two waves' vector instructions and products (119 of 32 cycles for each
-// wave), which overlap only in part. B=16, H=16/32, T=1024, D=128, bf16 155 us (2.8 TB/s, 221 TFLOP/s of
-// the recurrence).
+// Bound: latency in each wave. B=16, H=16/32, T=1024, D=128, bf16 155 us (2.8 TB/s, 221 TFLOP/s of the
+// recurrence): of the 15,700 cycles that a SIMD's two waves spend on a chunk each, their products take
+// 7,600 and the issue of their other vector instructions 8,100, so each of the two pipes is free for
+// half of the time. A wave waits for three fifths of it: at the three barriers of a chunk, for results of
+// its own chain (scores, their split, their product; the state's split, its product), and for its turn
+// to issue.
 //
 // A workgroup works through the tokens of one (entry, value head, 128 columns): a whole prompt, or
 // one segment of it. The 4 waves hold 32 columns of the state each, in accumulator registers; the
@@ -824,8 +828,10 @@ static int cu_count() {
 // resident workgroups that the segments take, a chunk of a segment costs about 1.4 + 1.1 fill
 // chunks of a call in one pass (both passes over it, two workgroups on a compute unit), and the
 // launches and the states 2 + 4 fill. Measured at H = 16/32, D = 128, fp32, one pass against
-// segments, us: B=1 T=384 33.0/30.0, T=512 41.2/31.7, T=1024 68/35.6, T=8192 538/123; B=2 T=512
-// 42.2/35.9; B=4 T=512 42.9/51.6, T=1024 79.3/78.5, T=4096 283/215; B=5 T=2048 150/148.
+// segments, us: B=1 T=256 23.3/26.4, T=384 31.7/29.6, T=512 40.0/31.0, T=1024 72/35, T=8192 525/128; B=2
+// T=512 41.1/35.6; B=4 T=512 41.8/53.0, T=1024 74.3/78.3, T=4096 271/223; B=5 T=2048 143/154; B=8 T=1024
+// 90/130. At D = 64 and 256 what the rule cuts up is faster so too (B=1 T=8192 392/66 and 984/420), but
+// some calls that it leaves in one pass would gain (D = 64 B=4 T=1024 54.7/42.8; D = 256 B=1 T=512 74/58).
 static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, size_t &bytes) {
     bytes = 0;
     p.nseg = 1;
