@@ -22,6 +22,10 @@ it finds that a call does not fit, the checks here say why. It is loaded by the 
   correction), for a few tokens and for prompts, on pools of fp32, bf16 or 8-bit states.
 * ``la_state_quantize`` / ``la_state_dequantize`` -- states into and out of 8-bit pools.
 * ``la_norm_gate`` -- the per-head norm of the outputs times the output gate.
+* ``la_conv`` -- the short causal convolution in front of a recurrence, on a pool of last inputs.
+* ``la_rope`` -- rotary positions of queries and keys; ``la_rope_frequencies`` -- their frequencies.
+* ``ssm_decode`` / ``ssm_prefill`` -- the selective state space scan (a decay for each channel and
+  state), for a few tokens and for prompts, on pools of fp32 or bf16 states.
 * ``rgdr_validate`` -- synchronous check of the index arrays.
 
 A non-OK status from the library raises ``RuntimeError`` (the page's error behaviour).
@@ -32,6 +36,7 @@ host, for debugging only (it cannot run under graph capture). A bad length, coun
 then raises ``RuntimeError`` instead of being clamped or skipped by the kernel.
 """
 import ctypes as C
+import math
 import os
 
 import torch
@@ -42,7 +47,8 @@ __all__ = ["rgdr_decode", "rgdr_decode_snapshots", "rgdr_decode_gated",
            "rgdr_prefill_noalloc",
            "recurrent_gated_delta_rule", "la_gate", "la_decode", "la_prefill",
            "la_prefill_workspace_size", "la_state_quantize", "la_state_dequantize",
-           "la_norm_gate",
+           "la_norm_gate", "la_conv", "la_rope", "la_rope_frequencies", "ssm_decode", "ssm_prefill",
+           "ssm_prefill_workspace_size",
            "rgdr_validate", "VALIDATE",
            "rgdr_validate_host", "status_string", "library", "LIB_PATH", "RGDR_F32",
            "RGDR_F16", "RGDR_BF16", "RGDR_MXI8"]
@@ -53,6 +59,9 @@ RGDR_F32, RGDR_F16, RGDR_BF16, RGDR_MXI8 = 0, 1, 2, 3
 RGDR_NORMALIZE_QK = 1  # option bit of rgdr_decode_gated
 NORMALIZE_QK = RGDR_NORMALIZE_QK
 LA_GATE_SIGMOID = 1    # option bit of la_norm_gate
+LA_CONV_SILU = 1       # option bit of la_conv
+LA_ROPE_INTERLEAVED = 1  # option bit of la_rope
+SSM_DT_SOFTPLUS = 1    # option bit of ssm_decode and ssm_prefill
 LA_BLOCK = 32          # columns of a state row that share a scale byte in an 8-bit pool
 _DTYPE_CODE = {torch.float32: RGDR_F32, torch.float16: RGDR_F16, torch.bfloat16: RGDR_BF16}
 
@@ -117,6 +126,19 @@ def library():
     lib.la_norm_gate.restype = C.c_int
     lib.la_norm_gate.argtypes = ([vp, st, vp, st, vp, i64, C.c_int, vp, f32, C.c_uint32]
                                  + [i32] * 4 + [vp, st, vp])
+    lib.la_conv.restype = C.c_int
+    lib.la_conv.argtypes = ([vp, st, vp, vp, C.c_int] + [vp] * 4 + [C.c_uint32] + [i32] * 5
+                            + [vp, st, vp, vp])
+    lib.la_rope.restype = C.c_int
+    lib.la_rope.argtypes = ([vp, st, vp, st, vp, vp, C.c_int, vp, f32, C.c_uint32] + [i32] * 6
+                            + [vp, st, vp, st, vp])
+    lib.ssm_decode.restype = C.c_int
+    lib.ssm_decode.argtypes = ([vp, st, vp, st, vp, vp, st, vp, st, vp, vp, st, vp, C.c_int, vp,
+                                C.c_int] + [vp] * 3 + [C.c_uint32] + [i32] * 6 + [vp, st, vp, vp])
+    lib.ssm_prefill.restype = C.c_int
+    lib.ssm_prefill.argtypes = lib.ssm_decode.argtypes[:-1] + [vp, C.c_size_t, vp]
+    lib.ssm_prefill_workspace_size.restype = C.c_int
+    lib.ssm_prefill_workspace_size.argtypes = [i32] * 5 + [C.POINTER(C.c_size_t)]
     lib.rgdr_validate.restype = C.c_int
     lib.rgdr_validate.argtypes = [vp, vp, vp, i32, i32, i32, vp]
     lib.rgdr_validate_host.restype = C.c_int
@@ -675,12 +697,7 @@ def _la_prepare(fn, query, key, value, g, state_pool, lens, idx, nacc, state_sca
     B, Hq, T, Dk = query.shape
     Hv, Dv = value.shape[1], value.shape[3]
     if VALIDATE and B:
-        def given(t, other):
-            return t if t is not None else torch.as_tensor(other, dtype=torch.int32,
-                                                           device=query.device)
-        n = given(lens, [T] * B)
-        _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T,
-                          state_pool.shape[0])
+        _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], query.device)
     if stream is not None:
         if out is None:
             out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
@@ -846,6 +863,305 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
     if rc:
         _check(rc, "la_norm_gate")
     return out
+
+
+def _validate_given(lens, idx, nacc, B, T, N, device):
+    """rgdr_validate of a call's index arrays, any of which may be left out."""
+    def given(t, other):
+        return t if t is not None else torch.as_tensor(other, dtype=torch.int32, device=device)
+    n = given(lens, [T] * B)
+    _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N)
+
+
+def _tokens(t, name, dtypes, shape):
+    """A [B, T, ..] operand whose last axis is contiguous; the other axes may have any strides."""
+    _rows(t, name, dtypes, len(shape))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise RuntimeError(f"{name}: the last axis must be contiguous")
+    if tuple(t.shape) != tuple(shape):
+        raise RuntimeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _vector(t, name, shape):
+    """An optional fp32 parameter."""
+    if t is not None:
+        _dev(t, name, torch.float32)
+        if tuple(t.shape) != tuple(shape):
+            raise RuntimeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _pool(t, name, dtypes, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise RuntimeError(f"{name} must be a tensor of {' or '.join(map(str, dtypes))}")
+    _dev(t, name, t.dtype, len(shape) + 1)
+    if tuple(t.shape[1:]) != tuple(shape):
+        raise RuntimeError(f"{name} must be [N_slots, {', '.join(map(str, shape))}]")
+
+
+def _conv_refuse(x, weight, bias, state_pool, lens, idx, nacc, out, state_out):
+    _rows(x, "x", tuple(_DTYPE_CODE), 3)
+    B, T, Ch = x.shape
+    _tokens(x, "x", (x.dtype,), x.shape)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise RuntimeError("weight must be a [C, W] tensor")
+    W = weight.shape[1]
+    _vector(weight, "weight", (Ch, W))
+    _vector(bias, "bias", (Ch,))
+    _pool(state_pool, "state_pool", (x.dtype,), (W - 1, Ch))
+    if state_out is not state_pool:
+        _pool(state_out, "state_out", (x.dtype,), (W - 1, Ch))
+        if state_out.shape != state_pool.shape:
+            raise RuntimeError("state_out must have the pool's shape")
+    index = {"actual_seq_lengths": lens, "ssm_state_indices": idx, "num_accepted_tokens": nacc}
+    for nm, t in index.items():
+        _index(t, nm, B)
+    if out is not None:
+        _tokens(out, "out", (x.dtype,), x.shape)
+    _same_device(x, weight=weight, bias=bias, state_pool=state_pool, out=out, state_out=state_out,
+                 **index)
+
+
+def la_conv(x, weight, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
+            num_accepted_tokens=None, *, bias=None, silu=True, out=None, state_out=None,
+            stream=None):
+    """The short causal convolution between an input projection and a recurrence:
+    ``y[t] = silu(bias + sum_j weight[:, j] line[t - (W - 1) + j])`` (``silu=False``: without silu)
+    for each channel, on the line of the slot's W - 1 inputs and the call's; returns
+    ``(out, state_out)``.
+
+    x ``[B,T,C]`` float32, float16 or bfloat16, any strides with the last axis contiguous and rows
+    at multiples of 8 elements (columns of a wider projection are fine), T up to 65536, C a multiple
+    of 8. weight float32 ``[C,W]`` with W 2, 3 or 4 (a depthwise convolution's ``[C,1,W]`` weight
+    without its middle axis), bias float32 ``[C]``. state_pool ``[N_slots,W-1,C]`` of x's type: the
+    inputs before the call, the latest last; it receives those of the accepted tokens, in place
+    unless ``state_out`` is given. A new sequence's slot is zeros. The index arrays are int32
+    ``[B]``, each may be left out, as in ``la_decode``."""
+    if _quick is None:
+        _load_quick()
+    if state_out is None:
+        state_out = state_pool
+    if stream is not None or VALIDATE:
+        _conv_refuse(x, weight, bias, state_pool, actual_seq_lengths, ssm_state_indices,
+                     num_accepted_tokens, out, state_out)
+        if VALIDATE and x.shape[0]:
+            _validate_given(actual_seq_lengths, ssm_state_indices, num_accepted_tokens,
+                            x.shape[0], x.shape[1], state_pool.shape[0], x.device)
+        if out is None and stream is not None:
+            out = _empty(x.shape, x.dtype, x.device, stream)
+    done = _quick.conv(x, weight, bias, state_pool, actual_seq_lengths, ssm_state_indices,
+                       num_accepted_tokens, LA_CONV_SILU if silu else 0, out, state_out,
+                       _raw_stream(x, stream))
+    if done is None:
+        _conv_refuse(x, weight, bias, state_pool, actual_seq_lengths, ssm_state_indices,
+                     num_accepted_tokens, out, state_out)
+        raise RuntimeError("la_conv: unsupported arguments")
+    rc, out = done
+    if rc:
+        _check(rc, "la_conv")
+    return out, state_out
+
+
+def _rope_refuse(query, key, inv_freq, positions, lens, query_out, key_out):
+    _rows(query, "query", tuple(_DTYPE_CODE))
+    B, Hq, T, D = query.shape
+    if key is not None:
+        _rows(key, "key", (query.dtype,))
+        if (key.shape[0], key.shape[2], key.shape[3]) != (B, T, D):
+            raise RuntimeError("key must be [B, H_k, T, D] with query's B, T and D")
+    elif key_out is not None:
+        raise RuntimeError("key_out goes with key")
+    _dev(inv_freq, "inv_freq", torch.float32, 1)
+    if 2 * inv_freq.shape[0] > D:
+        raise RuntimeError(f"inv_freq turns {2 * inv_freq.shape[0]} columns of {D}")
+    if positions is not None:
+        _dev(positions, "positions", torch.int32)
+        if tuple(positions.shape) not in ((B,), (B, T)):
+            raise RuntimeError("positions must be [B] or [B, T]")
+    _index(lens, "actual_seq_lengths", B)
+    for nm, t, x in (("query_out", query_out, query), ("key_out", key_out, key)):
+        if t is not None:
+            _rows(t, nm, (query.dtype,))
+            if t.shape != x.shape:
+                raise RuntimeError(f"{nm} must have the shape of what it receives")
+    _same_device(query, key=key, inv_freq=inv_freq, positions=positions, query_out=query_out,
+                 key_out=key_out, actual_seq_lengths=lens)
+
+
+def la_rope(query, key, inv_freq, positions=None, *, interleaved=False, factor=1.0,
+            actual_seq_lengths=None, query_out=None, key_out=None, stream=None):
+    """Rotary positions: pair i of each row's first ``2 len(inv_freq)`` columns (columns i and
+    ``len(inv_freq) + i``, or 2i and 2i + 1 when ``interleaved``) is turned by ``position *
+    inv_freq[i]`` and multiplied by ``factor``; the other columns are copied. Returns
+    ``(query_out, key_out)``, contiguous when allocated.
+
+    query ``[B,H_q,T,D]``, key ``[B,H_k,T,D]`` (or None) float32, float16 or bfloat16, any strides
+    with the last axis contiguous and rows at multiples of 8 elements, D a multiple of 8 up to 1024.
+    inv_freq float32, as from ``la_rope_frequencies``. positions int32 ``[B]``: the position of each
+    entry's first token (the tokens that came before it), or ``[B,T]``: each token's own; None: all
+    start at 0. ``query_out=query, key_out=key`` turns them in place. Rows of tokens past
+    ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
+    if _quick is None:
+        _load_quick()
+    if stream is not None:
+        _rope_refuse(query, key, inv_freq, positions, actual_seq_lengths, query_out, key_out)
+        if query_out is None:
+            query_out = _empty(query.shape, query.dtype, query.device, stream)
+        if key_out is None and key is not None:
+            key_out = _empty(key.shape, key.dtype, key.device, stream)
+    done = _quick.rope(query, key, inv_freq, positions, actual_seq_lengths, factor,
+                       LA_ROPE_INTERLEAVED if interleaved else 0, query_out, key_out,
+                       _raw_stream(query, stream))
+    if done is None:
+        _rope_refuse(query, key, inv_freq, positions, actual_seq_lengths, query_out, key_out)
+        raise RuntimeError("la_rope: unsupported arguments")
+    rc, query_out, key_out = done
+    if rc:
+        _check(rc, "la_rope")
+    return query_out, key_out
+
+
+def la_rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, scale=1.0, original_length=None,
+                        fast_turns=32.0, slow_turns=1.0, device="cuda"):
+    """The frequencies ``base ** (-2 i / rotary_dim)`` that ``la_rope`` takes, computed in 64 bits;
+    returns ``(inv_freq, factor)``, float32 ``[rotary_dim / 2]`` and la_rope's factor.
+
+    For texts ``scale`` times as long as those that a model was trained on, ``scaling`` is
+    ``"linear"`` (every frequency divided by ``scale``), ``"base"`` (a larger base, so that the
+    slowest pair is divided by ``scale`` and the fastest stays) or ``"blend"``: pairs that turn at
+    least ``fast_turns`` times within ``original_length`` tokens stay, those that turn at most
+    ``slow_turns`` times are divided by ``scale``, those between go over linearly in their index,
+    and the factor is ``0.1 ln(scale) + 1``."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise RuntimeError("rotary_dim must be even and at least 2")
+    if not base > 1.0:
+        raise RuntimeError("base must be above 1")
+    if scaling not in (None, "linear", "base", "blend"):
+        raise RuntimeError("scaling must be None, 'linear', 'base' or 'blend'")
+    if not scale >= 1.0:
+        raise RuntimeError("scale must be at least 1")
+    half, factor = rotary_dim // 2, 1.0
+    i = torch.arange(half, dtype=torch.float64)
+    if scaling == "base" and rotary_dim > 2:
+        base = base * scale ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        freq = freq / scale
+    elif scaling == "blend":
+        if not original_length or original_length <= 0 or not fast_turns > slow_turns > 0:
+            raise RuntimeError("'blend' needs original_length and fast_turns > slow_turns > 0")
+
+        def index(turns):  # of the pair that turns this often within original_length tokens
+            return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low, high = max(math.floor(index(fast_turns)), 0), min(math.ceil(index(slow_turns)), half - 1)
+        divided = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        freq = freq * (1 - divided) + freq / scale * divided
+        factor = 0.1 * math.log(scale) + 1.0
+    return freq.to(torch.float32).to(device), factor
+
+
+def _ssm_refuse(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, out, state_out,
+                workspace):
+    _rows(x, "x", tuple(_DTYPE_CODE), 3)
+    B, T, Ch = x.shape
+    for nm, t in (("x", x), ("dt", dt), ("z", z), ("out", out)):
+        if t is not None or nm == "dt":
+            _tokens(t, nm, (x.dtype,), x.shape)
+    _dev(A, "A", torch.float32, 2)
+    N = A.shape[1]
+    _vector(A, "A", (Ch, N))
+    _rows(Bm, "B", (x.dtype,))
+    for nm, t in (("B", Bm), ("C", Cm)):
+        _tokens(t, nm, (x.dtype,), (B, T, Bm.shape[2], N))
+    _vector(D, "D", (Ch,))
+    _vector(dt_bias, "dt_bias", (Ch,))
+    _pool(state_pool, "state_pool", (torch.float32, torch.bfloat16), (Ch, N))
+    if state_out is not state_pool:
+        _pool(state_out, "state_out", (state_pool.dtype,), (Ch, N))
+        if state_out.shape != state_pool.shape:
+            raise RuntimeError("state_out must have the pool's shape")
+    index = {"actual_seq_lengths": lens, "ssm_state_indices": idx, "num_accepted_tokens": nacc}
+    for nm, t in index.items():
+        _index(t, nm, B)
+    if workspace is not None and (not isinstance(workspace, torch.Tensor)
+                                  or workspace.dtype != torch.uint8 or not workspace.is_cuda
+                                  or not workspace.is_contiguous()):
+        raise RuntimeError("workspace must be a contiguous uint8 CUDA tensor")
+    _same_device(x, dt=dt, A=A, B=Bm, C=Cm, state_pool=state_pool, D=D, z=z, dt_bias=dt_bias,
+                 out=out, state_out=state_out, workspace=workspace, **index)
+
+
+def _ssm_call(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, dt_softplus, out,
+              state_out, stream, workspace=None):
+    if _quick is None:
+        _load_quick()
+    if state_out is None:
+        state_out = state_pool
+    if stream is not None or VALIDATE:
+        _ssm_refuse(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, out,
+                    state_out, workspace)
+        B, T, Ch = x.shape
+        if VALIDATE and B:
+            _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], x.device)
+        if stream is not None:
+            if out is None:
+                out = _empty(x.shape, x.dtype, x.device, stream)
+            if fn == "ssm_prefill" and workspace is None:
+                size = ssm_prefill_workspace_size(B, T, Ch, A.shape[1], Bm.shape[2], x.device)
+                if size:
+                    workspace = _empty(size, torch.uint8, x.device, stream)
+    done = _quick.scan(fn == "ssm_prefill", x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z,
+                       dt_bias, SSM_DT_SOFTPLUS if dt_softplus else 0, out, state_out, workspace,
+                       _raw_stream(x, stream))
+    if done is None:
+        _ssm_refuse(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, out,
+                    state_out, workspace)
+        raise RuntimeError(f"{fn}: unsupported arguments")
+    rc, out = done
+    if rc:
+        _check(rc, fn)
+    return out, state_out
+
+
+def ssm_decode(x, dt, A, B, C, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
+               num_accepted_tokens=None, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+               out=None, state_out=None, stream=None):
+    """The selective state space scan, T <= 8 tokens per entry: for each channel, on its N states,
+    ``d = softplus(dt + dt_bias)``, ``h = exp(d A) h + d x B``, ``y = (C . h + D x) silu(z)``;
+    returns ``(out, state_out)``.
+
+    x, dt, z ``[B,T,C]`` and B, C ``[B,T,G,N]`` (group g serves channels g C/G on) of one type,
+    float32, float16 or bfloat16, any strides with the last axis contiguous and rows at multiples of
+    8 elements (columns of a wider projection are fine); channels a multiple of 8, N 8, 16 or 32. A
+    float32 ``[C,N]``, D and dt_bias float32 ``[C]``; D, z and dt_bias may be left out.
+    ``dt_softplus=False`` takes ``d = dt + dt_bias``. state_pool float32 or bfloat16
+    ``[N_slots,C,N]``, updated in place unless ``state_out`` is given; a new sequence's slot is
+    zeros. The index arrays are int32 ``[B]``, each may be left out, as in ``la_decode``."""
+    return _ssm_call("ssm_decode", x, dt, A, B, C, state_pool, actual_seq_lengths,
+                     ssm_state_indices, num_accepted_tokens, D, z, dt_bias, dt_softplus, out,
+                     state_out, stream)
+
+
+def ssm_prefill(x, dt, A, B, C, state_pool, actual_seq_lengths=None, ssm_state_indices=None,
+                num_accepted_tokens=None, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+                workspace=None, out=None, state_out=None, stream=None):
+    """``ssm_decode`` over whole prompts (T up to 65536); arguments and results as there.
+
+    ``workspace``: a uint8 CUDA tensor of ``ssm_prefill_workspace_size`` bytes for calls of few
+    channels, which then work on parts of a prompt at once; allocated for the call when None."""
+    return _ssm_call("ssm_prefill", x, dt, A, B, C, state_pool, actual_seq_lengths,
+                     ssm_state_indices, num_accepted_tokens, D, z, dt_bias, dt_softplus, out,
+                     state_out, stream, workspace)
+
+
+def ssm_prefill_workspace_size(B, T, channels, N, groups=1, device=None):
+    """Bytes of workspace that ``ssm_prefill`` uses for a call of B entries, T tokens and so many
+    channels of N states in so many groups on ``device`` (0: it needs none)."""
+    lib = library()
+    n = C.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        rc = lib.ssm_prefill_workspace_size(B, T, channels, N, groups, C.byref(n))
+    _check(rc, "ssm_prefill_workspace_size")
+    return n.value
 
 
 def rgdr_validate(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N_slots,

@@ -47,6 +47,10 @@ bool fits(const Arg &a, at::ScalarType type, c10::Device dev, std::initializer_l
 bool fits_rows(const Arg &a, at::ScalarType type, c10::Device dev, std::initializer_list<int64_t> s) {
     return on(a, type, dev) && sizes_are(*a.t, s) && (s.size() == 3 || a.t->stride(3) == 1);
 }
+// [B, T, ..] of any strides, the last axis contiguous
+bool fits_tokens(const Arg &a, at::ScalarType type, c10::Device dev, std::initializer_list<int64_t> s) {
+    return on(a, type, dev) && sizes_are(*a.t, s) && (a.t->size(a.t->dim() - 1) <= 1 || a.t->stride(a.t->dim() - 1) == 1);
+}
 bool fits_index(const Arg &a, c10::Device dev, int64_t n) {
     return !a.bad && (!a.here() || fits(a, at::kInt, dev, {n}));
 }
@@ -54,6 +58,11 @@ bool fits_index(const Arg &a, c10::Device dev, int64_t n) {
 void *ptr(const Arg &a) { return a.here() ? a.t->data_ptr() : nullptr; }
 la_strides strides(const at::Tensor &t) { return {t.stride(0), t.stride(1), t.stride(2)}; }
 la_strides strides_bth(const at::Tensor &t) { return {t.stride(0), t.stride(2), t.stride(1)}; }
+
+la_strides strides_bt(const Arg &a) {  // [B, T, C]
+    return a.here() ? la_strides{a.t->stride(0), 0, a.t->stride(1)} : la_strides{0, 0, 0};
+}
+bool row_type(at::ScalarType t) { return t == at::kFloat || t == at::kHalf || t == at::kBFloat16; }
 
 int dtype_code(at::ScalarType t) {
     switch (t) {
@@ -233,10 +242,179 @@ PyObject *norm_gate(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// conv(x, weight, bias, pool, lens, idx, nacc, flags, out, pool_out, stream) -> (status, out), or None
+PyObject *conv(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 11) {
+        PyErr_SetString(PyExc_TypeError, "conv takes 11 arguments");
+        return nullptr;
+    }
+    const Arg x(args[0]), weight(args[1]), bias(args[2]), pool(args[3]), lens(args[4]), idx(args[5]), nacc(args[6]);
+    const unsigned long flags = PyLong_AsUnsignedLong(args[7]);
+    const Arg out(args[8]), pool_out(args[9]);
+    const auto stream = reinterpret_cast<hipStream_t>(PyLong_AsVoidPtr(args[10]));
+    if (PyErr_Occurred()) return nullptr;
+    if (!x.here() || !weight.here() || !pool.here() || !x.t->is_cuda() || x.t->dim() != 3 || weight.t->dim() != 2 ||
+        pool.t->dim() != 3)
+        Py_RETURN_NONE;
+    const c10::Device dev = x.t->device();
+    const auto type = x.t->scalar_type();
+    const int64_t B = x.t->size(0), T = x.t->size(1), C = x.t->size(2), W = weight.t->size(1), N = pool.t->size(0);
+    if (!row_type(type) || !int_sizes({B, T, C, W, N}) || !fits_tokens(x, type, dev, {B, T, C}) ||
+        !fits(weight, at::kFloat, dev, {C, W}) || bias.bad || (bias.here() && !fits(bias, at::kFloat, dev, {C})) ||
+        !fits(pool, type, dev, {N, W - 1, C}) || !fits(pool_out, type, dev, {N, W - 1, C}) ||
+        !fits_index(lens, dev, B) || !fits_index(idx, dev, B) || !fits_index(nacc, dev, B) || out.bad ||
+        (out.here() && !fits_tokens(out, type, dev, {B, T, C})))
+        Py_RETURN_NONE;
+    const c10::DeviceGuard guard(dev);
+    const at::Tensor o = out.here() ? *out.t : at::empty({B, T, C}, x.t->options());
+    const la_strides sx = strides_bt(x), so = {o.stride(0), 0, o.stride(1)};
+    rgdr_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = la_conv(ptr(x), &sx, (const float *)ptr(weight), (const float *)ptr(bias), (rgdr_dtype)dtype_code(type),
+                 ptr(pool), (const int32_t *)ptr(lens), (const int32_t *)ptr(idx), (const int32_t *)ptr(nacc),
+                 (uint32_t)flags, (int)B, (int)T, (int)C, (int)W, (int)N, o.data_ptr(), &so, ptr(pool_out), stream);
+    Py_END_ALLOW_THREADS
+    return status_and(rc, o);
+    END_HANDLE_TH_ERRORS
+}
+
+// rope(query, key, freq, pos, lens, factor, flags, query_out, key_out, stream) -> (status, query_out,
+// key_out), or None
+PyObject *rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "rope takes 10 arguments");
+        return nullptr;
+    }
+    const Arg q(args[0]), k(args[1]), freq(args[2]), pos(args[3]), lens(args[4]);
+    const double factor = PyFloat_AsDouble(args[5]);
+    unsigned long flags = PyLong_AsUnsignedLong(args[6]);
+    const Arg qo(args[7]), ko(args[8]);
+    const auto stream = reinterpret_cast<hipStream_t>(PyLong_AsVoidPtr(args[9]));
+    if (PyErr_Occurred()) return nullptr;
+    if (!q.here() || !freq.here() || !q.t->is_cuda() || q.t->dim() != 4 || freq.t->dim() != 1 || k.bad || pos.bad ||
+        qo.bad || ko.bad || (k.here() && k.t->dim() != 4) || (ko.here() && !k.here()))
+        Py_RETURN_NONE;
+    const c10::Device dev = q.t->device();
+    const auto type = q.t->scalar_type();
+    const int64_t B = q.t->size(0), Hq = q.t->size(1), T = q.t->size(2), D = q.t->size(3), R = 2 * freq.t->size(0);
+    const int64_t Hk = k.here() ? k.t->size(1) : 0;
+    if (!row_type(type) || !int_sizes({B, Hq, Hk, T, D, R}) || !fits_rows(q, type, dev, {B, Hq, T, D}) ||
+        (k.here() && !fits_rows(k, type, dev, {B, Hk, T, D})) || !fits(freq, at::kFloat, dev, {R / 2}) ||
+        !fits_index(lens, dev, B) || (qo.here() && !fits_rows(qo, type, dev, {B, Hq, T, D})) ||
+        (ko.here() && !fits_rows(ko, type, dev, {B, Hk, T, D})))
+        Py_RETURN_NONE;
+    if (pos.here() && fits(pos, at::kInt, dev, {B, T}))
+        flags |= LA_ROPE_EACH_POSITION;
+    else if (!fits_index(pos, dev, B))
+        Py_RETURN_NONE;
+    const c10::DeviceGuard guard(dev);
+    const at::Tensor oq = qo.here() ? *qo.t : at::empty({B, Hq, T, D}, q.t->options());
+    at::Tensor ok;
+    if (k.here()) ok = ko.here() ? *ko.t : at::empty({B, Hk, T, D}, k.t->options());
+    const la_strides sq = strides(*q.t), sk = k.here() ? strides(*k.t) : la_strides{0, 0, 0};
+    const la_strides soq = strides(oq), sok = k.here() ? strides(ok) : la_strides{0, 0, 0};
+    rgdr_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = la_rope(ptr(q), &sq, ptr(k), &sk, (const float *)ptr(freq), (const int32_t *)ptr(pos),
+                 (rgdr_dtype)dtype_code(type), (const int32_t *)ptr(lens), (float)factor, (uint32_t)flags, (int)B,
+                 (int)Hq, (int)Hk, (int)T, (int)D, (int)R, oq.data_ptr(), &soq, k.here() ? ok.data_ptr() : nullptr,
+                 &sok, stream);
+    Py_END_ALLOW_THREADS
+    PyObject *first = THPVariable_Wrap(oq);
+    if (!first) return nullptr;
+    PyObject *second = Py_None;
+    if (k.here()) {
+        second = THPVariable_Wrap(ok);
+        if (!second) {
+            Py_DECREF(first);
+            return nullptr;
+        }
+    } else {
+        Py_INCREF(second);
+    }
+    return Py_BuildValue("(iNN)", (int)rc, first, second);
+    END_HANDLE_TH_ERRORS
+}
+
+// scan(prefill, x, dt, A, Bm, Cm, pool, lens, idx, nacc, D, z, dt_bias, flags, out, pool_out, workspace,
+//      stream) -> (status, out), or None
+PyObject *scan(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 18) {
+        PyErr_SetString(PyExc_TypeError, "scan takes 18 arguments");
+        return nullptr;
+    }
+    const bool prefill = args[0] == Py_True;
+    const Arg x(args[1]), dt(args[2]), A(args[3]), Bm(args[4]), Cm(args[5]), pool(args[6]);
+    const Arg lens(args[7]), idx(args[8]), nacc(args[9]), D(args[10]), z(args[11]), bias(args[12]);
+    const unsigned long flags = PyLong_AsUnsignedLong(args[13]);
+    const Arg out(args[14]), pool_out(args[15]), workspace(args[16]);
+    const auto stream = reinterpret_cast<hipStream_t>(PyLong_AsVoidPtr(args[17]));
+    if (PyErr_Occurred()) return nullptr;
+    if (!x.here() || !A.here() || !Bm.here() || !pool.here() || !x.t->is_cuda() || x.t->dim() != 3 ||
+        A.t->dim() != 2 || Bm.t->dim() != 4 || pool.t->dim() != 3)
+        Py_RETURN_NONE;
+    const c10::Device dev = x.t->device();
+    const auto type = x.t->scalar_type(), state = pool.t->scalar_type();
+    const int64_t B = x.t->size(0), T = x.t->size(1), C = x.t->size(2), N = A.t->size(1), G = Bm.t->size(2);
+    const int64_t slots = pool.t->size(0);
+    if (!row_type(type) || (state != at::kFloat && state != at::kBFloat16) || !int_sizes({B, T, C, N, G, slots}) ||
+        !fits_tokens(x, type, dev, {B, T, C}) || !fits_tokens(dt, type, dev, {B, T, C}) ||
+        !fits(A, at::kFloat, dev, {C, N}) || !fits_tokens(Bm, type, dev, {B, T, G, N}) ||
+        !fits_tokens(Cm, type, dev, {B, T, G, N}) || !fits(pool, state, dev, {slots, C, N}) ||
+        !fits(pool_out, state, dev, {slots, C, N}) || !fits_index(lens, dev, B) || !fits_index(idx, dev, B) ||
+        !fits_index(nacc, dev, B) || D.bad || (D.here() && !fits(D, at::kFloat, dev, {C})) || z.bad ||
+        (z.here() && !fits_tokens(z, type, dev, {B, T, C})) || bias.bad ||
+        (bias.here() && !fits(bias, at::kFloat, dev, {C})) || out.bad ||
+        (out.here() && !fits_tokens(out, type, dev, {B, T, C})))
+        Py_RETURN_NONE;
+    if (workspace.bad || (workspace.here() && (!on(workspace, at::kByte, dev) || !workspace.t->is_contiguous())))
+        Py_RETURN_NONE;
+    const c10::DeviceGuard guard(dev);
+    const at::Tensor o = out.here() ? *out.t : at::empty({B, T, C}, x.t->options());
+    at::Tensor ws;
+    if (prefill) {
+        if (workspace.here()) {
+            ws = *workspace.t;
+        } else {
+            size_t bytes = 0;
+            const rgdr_status rc = ssm_prefill_workspace_size((int)B, (int)T, (int)C, (int)N, (int)G, &bytes);
+            if (rc != RGDR_OK) return status_and(rc, o);
+            if (bytes) ws = at::empty({(int64_t)bytes}, x.t->options().dtype(at::kByte));
+        }
+    }
+    const la_strides sx = strides_bt(x), sdt = strides_bt(dt), sz = strides_bt(z), so = {o.stride(0), 0, o.stride(1)};
+    const la_strides sB = strides_bth(*Bm.t), sC = strides_bth(*Cm.t);
+    const auto type_code = (rgdr_dtype)dtype_code(type), state_code = (rgdr_dtype)dtype_code(state);
+    rgdr_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    if (prefill)
+        rc = ssm_prefill(ptr(x), &sx, ptr(dt), &sdt, (const float *)ptr(A), ptr(Bm), &sB, ptr(Cm), &sC,
+                         (const float *)ptr(D), ptr(z), &sz, (const float *)ptr(bias), type_code, ptr(pool),
+                         state_code, (const int32_t *)ptr(lens), (const int32_t *)ptr(idx),
+                         (const int32_t *)ptr(nacc), (uint32_t)flags, (int)B, (int)T, (int)C, (int)N, (int)G,
+                         (int)slots, o.data_ptr(), &so, ptr(pool_out), ws.defined() ? ws.data_ptr() : nullptr,
+                         ws.defined() ? (size_t)ws.numel() : 0, stream);
+    else
+        rc = ssm_decode(ptr(x), &sx, ptr(dt), &sdt, (const float *)ptr(A), ptr(Bm), &sB, ptr(Cm), &sC,
+                        (const float *)ptr(D), ptr(z), &sz, (const float *)ptr(bias), type_code, ptr(pool),
+                        state_code, (const int32_t *)ptr(lens), (const int32_t *)ptr(idx),
+                        (const int32_t *)ptr(nacc), (uint32_t)flags, (int)B, (int)T, (int)C, (int)N, (int)G,
+                        (int)slots, o.data_ptr(), &so, ptr(pool_out), stream);
+    Py_END_ALLOW_THREADS
+    return status_and(rc, o);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef kMethods[] = {
     {"attention", (PyCFunction)(void (*)())attention, METH_FASTCALL, "la_decode and la_prefill"},
     {"move", (PyCFunction)(void (*)())move, METH_FASTCALL, "la_state_quantize and la_state_dequantize"},
     {"norm_gate", (PyCFunction)(void (*)())norm_gate, METH_FASTCALL, "la_norm_gate"},
+    {"conv", (PyCFunction)(void (*)())conv, METH_FASTCALL, "la_conv"},
+    {"rope", (PyCFunction)(void (*)())rope, METH_FASTCALL, "la_rope"},
+    {"scan", (PyCFunction)(void (*)())scan, METH_FASTCALL, "ssm_decode and ssm_prefill"},
     {nullptr, nullptr, 0, nullptr},
 };
 

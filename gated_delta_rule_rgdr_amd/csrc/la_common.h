@@ -1,6 +1,7 @@
 // la_common.h -- what the linear-attention kernels (la_decode.hip, la_prefill.hip), the 8-bit
-// state pools (la_state.hip) and the gated norm (la_norm_gate.hip) share: argument blocks, host
-// checks, and the 8-bit block format. Not part of the C ABI.
+// state pools (la_state.hip), the gated norm (la_norm_gate.hip), the short convolution (la_conv.hip),
+// rotary positions (la_rope.hip) and the state space scan (ssm_scan.hip) share: argument blocks, host
+// checks, the 8-bit block format and the rows' types. Not part of the C ABI.
 #pragma once
 
 #include "rgdr_common.h"
@@ -55,6 +56,51 @@ __device__ __forceinline__ float mx_larger(float top, float x) {
     return __builtin_elementwise_maximum(top, __builtin_fabsf(x));
 }
 __device__ __forceinline__ uint32_t mx_top_bits(float top) { return __float_as_uint(top) & 0x7FFFFFFFu; }
+
+// ---- rows of fp32, fp16 (_Float16) or bf16 (uint16_t) values ------------------------------
+
+// 16 bytes of a row as fp32 values, and back.
+template <typename E>
+struct RowVec {
+    static constexpr int N = 16 / sizeof(E);
+    static __device__ __forceinline__ void get(float (&x)[N], const u32x4 &w) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            if constexpr (sizeof(E) == 4)
+                x[c] = __uint_as_float(w[c]);
+            else if constexpr (__is_same(E, _Float16))
+                x[c] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[c / 2] >> (c % 2 * 16))));
+            else
+                x[c] = c & 1 ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2]);
+        }
+    }
+    static __device__ __forceinline__ u32x4 put(const float (&x)[N]) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(E) == 4)
+                w[i] = __float_as_uint(x[i]);
+            else if constexpr (__is_same(E, _Float16))
+                w[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i])) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i + 1])) << 16;
+            else
+                w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        }
+        return w;
+    }
+};
+
+// One such value as fp32, and back.
+__device__ __forceinline__ float row_value(float x) { return x; }
+__device__ __forceinline__ float row_value(_Float16 x) { return static_cast<float>(x); }
+__device__ __forceinline__ float row_value(uint16_t x) { return bf16_to_f32(x); }
+template <typename E>
+__device__ __forceinline__ E row_store(float x) {
+    if constexpr (__is_same(E, uint16_t))
+        return f32_to_bf16(x);
+    else
+        return static_cast<E>(x);
+}
 
 // ---- linear attention: arguments ------------------------------------------------------------
 
@@ -137,6 +183,10 @@ inline bool la_rows_distinct(const LaStrides &s, int B, int H, int T, int D) {
 inline bool la_extent_ok(const LaStrides &s, int B, int H, int T, int D) {
     const __int128 e = (__int128)s.b * (B - 1) + (__int128)s.h * (H - 1) + (__int128)s.t * (T - 1) + D;
     return e < ((__int128)1 << 60);
+}
+
+inline bool la_index_aligned(const int32_t *lens, const int32_t *idx, const int32_t *nacc) {
+    return aligned(lens, 4) && aligned(idx, 4) && aligned(nacc, 4);
 }
 
 // The argument checks of la_decode and la_prefill (T up to max_t), and the kernels' argument

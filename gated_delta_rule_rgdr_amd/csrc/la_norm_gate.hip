@@ -16,37 +16,6 @@ struct NormArgs {
     int B, H, T, D, sigmoid;
 };
 
-// 16 bytes of a row as fp32 values, and back.
-template <typename E>
-struct NormVec {
-    static constexpr int N = 16 / sizeof(E);
-    static __device__ __forceinline__ void get(float (&x)[N], const u32x4 &w) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            if constexpr (sizeof(E) == 4)
-                x[c] = __uint_as_float(w[c]);
-            else if constexpr (__is_same(E, _Float16))
-                x[c] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[c / 2] >> (c % 2 * 16))));
-            else
-                x[c] = c & 1 ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2]);
-        }
-    }
-    static __device__ __forceinline__ u32x4 put(const float (&x)[N]) {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(E) == 4)
-                w[i] = __float_as_uint(x[i]);
-            else if constexpr (__is_same(E, _Float16))
-                w[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i])) |
-                       (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(x[2 * i + 1])) << 16;
-            else
-                w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        }
-        return w;
-    }
-};
-
 // Sum over aligned groups of LPR lanes, in each of them.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -68,7 +37,7 @@ __device__ __forceinline__ float row_sum(float x) {
 // 4096 rows (4.9 TB/s).
 template <typename E, int LPR, int NV, int U, bool GATED>
 __global__ __launch_bounds__(256) void la_norm_gate_kernel(const NormArgs a, int hr_log, int h_blocks, int t_blocks) {
-    using V = NormVec<E>;
+    using V = RowVec<E>;
     const int hb = blockIdx.x % h_blocks, tb = blockIdx.x / h_blocks % t_blocks;
     const int b = blockIdx.x / h_blocks / t_blocks;
     const int group = threadIdx.x / LPR, tr = (256 / LPR) >> hr_log;
@@ -178,7 +147,7 @@ static rgdr_status launch_norm_lanes(const NormArgs &a, hipStream_t stream) {
 // The fewest lanes that hold a row in one piece each; of long rows a wave holds several.
 template <typename E>
 static rgdr_status launch_norm(const NormArgs &a, hipStream_t stream) {
-    const int pieces = a.D / NormVec<E>::N;
+    const int pieces = a.D / RowVec<E>::N;
     if (pieces <= 8) return launch_norm_lanes<E, 8>(a, stream);
     if (pieces <= 16) return launch_norm_lanes<E, 16>(a, stream);
     if (pieces <= 32) return launch_norm_lanes<E, 32>(a, stream);

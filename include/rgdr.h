@@ -34,6 +34,13 @@
  *   la_norm_gate The gate's other end: the per-head root-mean-square norm of the attention's
  *                outputs times silu (or sigmoid) of a gate, written in the layout that the
  *                output projection reads.
+ *   la_conv      The short causal convolution between the input projection and a recurrence, over
+ *                [B, T, C], on a pool of each sequence's last inputs.
+ *   la_rope      Rotary positions of the queries and keys, whole heads or part of them.
+ *   ssm_decode, ssm_prefill
+ *                The selective state space scan (a decay for each channel and state, where la_decode
+ *                has one for each head), for a few tokens and for whole prompts, on pools of fp32 or
+ *                bf16 states.
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers to row-major, contiguous buffers owned by
@@ -516,6 +523,163 @@ rgdr_status la_norm_gate(const void *x, const la_strides *x_strides, const void 
                          const int32_t *actual_seq_lengths, float eps, uint32_t flags, int32_t B,
                          int32_t H, int32_t T, int32_t D, void *out,
                          const la_strides *out_strides, hipStream_t stream);
+
+/* Option bits of la_conv. */
+enum { LA_CONV_SILU = 1u /* silu of the sum */ };
+
+/*
+ * la_conv -- the short causal convolution of each channel. For every entry b, channel c and valid
+ * token t, on the line of tokens that the slot's W - 1 inputs and the call's x make up:
+ *     y[b,t,c] = f(bias[c] + sum_j weight[c,j] line[t - (W - 1) + j, c]),   0 <= j < W,
+ * f the identity or silu; weight[c, W - 1] meets the token itself. fp32, rounded once.
+ *
+ *   x          [B, T, C] of dtype (RGDR_F32, RGDR_F16 or RGDR_BF16) with x_strides (h unused; NULL:
+ *              contiguous), so that it may be columns of a wider projection.
+ *   weight     fp32 [C, W], bias fp32 [C] or NULL; 16-byte aligned.
+ *   state_pool [N_slots, W - 1, C] of dtype: the inputs before the call, the latest one last.
+ *   actual_seq_lengths, ssm_state_indices, num_accepted_tokens
+ *              int32 [B], each may be NULL, as in la_decode.
+ *   flags      0 or LA_CONV_SILU.
+ *   B, T, C, W, N_slots   B >= 0 (0: nothing is read or launched); 1 <= T <= 65536; C a multiple
+ *              of 8; W in {2, 3, 4}.
+ *   out        as x with out_strides (NULL: contiguous; rows must not overlap), written entirely:
+ *              rows of tokens past an entry's length, and of skipped entries, are +0.0. It overlaps
+ *              no input (a call whose out is x itself is refused).
+ *   state_out  receives the last W - 1 inputs after num_accepted_tokens tokens in every slot that an
+ *              entry names; other slots are not touched. It may be state_pool (in place); any other
+ *              overlap is undefined.
+ * Rows start at multiples of 8 elements, bases are 16-byte aligned. Padded tokens and skipped
+ * entries are never read; a token's NaN or infinity shows in its own output and in those of the
+ * W - 1 tokens behind it.
+ * Errors: RGDR_ERR_NULL, RGDR_ERR_SHAPE (sizes, strides, overlapping out rows, out = x, no slot
+ * indices with N_slots < B), RGDR_ERR_UNSUPPORTED (C, W, an unknown option bit), RGDR_ERR_DTYPE,
+ * RGDR_ERR_ALIGN, RGDR_ERR_HIP.
+ */
+rgdr_status la_conv(const void *x, const la_strides *x_strides, const float *weight,
+                    const float *bias, rgdr_dtype dtype, const void *state_pool,
+                    const int32_t *actual_seq_lengths, const int32_t *ssm_state_indices,
+                    const int32_t *num_accepted_tokens, uint32_t flags, int32_t B, int32_t T,
+                    int32_t C, int32_t W, int32_t N_slots, void *out,
+                    const la_strides *out_strides, void *state_out, hipStream_t stream);
+
+/* Option bits of la_rope. */
+enum {
+    LA_ROPE_INTERLEAVED = 1u,   /* pair i is columns 2i and 2i + 1, not i and i + R / 2 */
+    LA_ROPE_EACH_POSITION = 2u  /* positions is [B, T], not [B] */
+};
+
+/*
+ * la_rope -- rotary positions. Pair i < R / 2 of each query and key row's first R columns is turned
+ * by its token's angle a = position * inv_freq[i]:
+ *     (u, v) -> factor (u cos a - v sin a, u sin a + v cos a);
+ * the other D - R columns are copied. The angle is a 64-bit product, so that far positions lose
+ * nothing; the rest is fp32, rounded once.
+ *
+ *   query      [B, H_q, T, D], key [B, H_k, T, D] of dtype (RGDR_F32, RGDR_F16 or RGDR_BF16) with
+ *              their strides (NULL: contiguous), the layout of la_decode's. key may be NULL if
+ *              H_k = 0.
+ *   inv_freq   fp32 [R / 2], radians for each position; any scaling for long contexts is in them.
+ *              Finite.
+ *   positions  int32 [B]: the position of each entry's first token, those of the others follow; or
+ *              [B, T] (LA_ROPE_EACH_POSITION). NULL: entries start at 0.
+ *   actual_seq_lengths  int32 [B] or NULL: rows of tokens past an entry's length are written as
+ *              +0.0 and not read.
+ *   factor     multiplies cosines and sines.
+ *   B, H_q, H_k, T, D, R   sizes >= 0 (B, T or H_q + H_k = 0: nothing is read or launched); D a
+ *              multiple of 8 up to 1024, R even and at most D.
+ *   query_out, key_out  as query and key with their strides (NULL: contiguous; rows must not
+ *              overlap). They may be query's and key's buffers with the same strides; any other
+ *              overlap is undefined.
+ * Rows start at multiples of 8 elements, bases are 16-byte aligned.
+ * Errors: RGDR_ERR_NULL, RGDR_ERR_SHAPE (sizes, strides, overlapping out rows, in place with other
+ * strides), RGDR_ERR_UNSUPPORTED (D, R, an unknown option bit), RGDR_ERR_DTYPE, RGDR_ERR_ALIGN,
+ * RGDR_ERR_HIP.
+ */
+rgdr_status la_rope(const void *query, const la_strides *query_strides, const void *key,
+                    const la_strides *key_strides, const float *inv_freq,
+                    const int32_t *positions, rgdr_dtype dtype,
+                    const int32_t *actual_seq_lengths, float factor, uint32_t flags, int32_t B,
+                    int32_t H_q, int32_t H_k, int32_t T, int32_t D, int32_t R, void *query_out,
+                    const la_strides *query_out_strides, void *key_out,
+                    const la_strides *key_out_strides, hipStream_t stream);
+
+/* Option bits of ssm_decode and ssm_prefill. */
+enum { SSM_DT_SOFTPLUS = 1u /* the step is softplus(dt + dt_bias), not dt + dt_bias */ };
+
+/*
+ * ssm_decode -- the selective state space scan over T <= 8 tokens per batch entry. For every entry
+ * b, channel c of group g = c / (C / G) and valid token t, in token order, on the channel's N states
+ * h:
+ *     d = softplus(dt[b,t,c] + dt_bias[c])
+ *     h[n] = exp(d A[c,n]) h[n] + d x[b,t,c] Bm[b,t,g,n]
+ *     y[b,t,c] = (sum_n Cm[b,t,g,n] h[n] + D[c] x[b,t,c]) * silu(z[b,t,c]).
+ *
+ *   x, dt, z   [B, T, C] of dtype (RGDR_F32, RGDR_F16 or RGDR_BF16) with their strides (h unused;
+ *              NULL: contiguous). z may be NULL: no gate.
+ *   A          fp32 [C, N], <= 0 in use (not checked); 16-byte aligned.
+ *   Bm, Cm     [B, T, G, N] of dtype with their strides (h: the groups'; NULL: contiguous).
+ *   D          fp32 [C] or NULL; dt_bias fp32 [C] or NULL.
+ *   state_pool [N_slots, C, N] of state_dtype (RGDR_F32 or RGDR_BF16), 16-byte aligned.
+ *   actual_seq_lengths, ssm_state_indices, num_accepted_tokens
+ *              int32 [B], each may be NULL, as in la_decode.
+ *   flags      0 or SSM_DT_SOFTPLUS.
+ *   B, T, C, N, G, N_slots   B >= 0 (0: nothing is read or launched); C a multiple of 8 and of G;
+ *              N in {8, 16, 32}.
+ *   out        as x with out_strides (NULL: contiguous; rows must not overlap), written entirely:
+ *              rows of tokens past an entry's length, and of skipped entries, are +0.0. It overlaps
+ *              no input.
+ *   state_out  receives the state after the first num_accepted_tokens tokens in every slot that an
+ *              entry names; other slots are not touched. It may be state_pool (in place: then a slot
+ *              whose entry accepts no token keeps its bytes); any other overlap is undefined.
+ * Rows start at multiples of 8 elements, bases are 16-byte aligned. The arithmetic is fp32; the
+ * state is rounded once, when it is committed. Padded tokens and skipped entries are never read; a
+ * NaN or an infinity in a valid token shows in that token's outputs and in those of the tokens
+ * behind it, in its channel (x, dt, z) or its group (Bm, Cm), and in the state if the token is accepted.
+ * Errors: RGDR_ERR_NULL, RGDR_ERR_SHAPE (sizes, strides, overlapping out rows, no slot indices with
+ * N_slots < B), RGDR_ERR_UNSUPPORTED (C, N, an unknown option bit), RGDR_ERR_DTYPE, RGDR_ERR_ALIGN,
+ * RGDR_ERR_HIP.
+ */
+rgdr_status ssm_decode(const void *x, const la_strides *x_strides, const void *dt,
+                       const la_strides *dt_strides, const float *A, const void *Bm,
+                       const la_strides *Bm_strides, const void *Cm, const la_strides *Cm_strides,
+                       const float *D, const void *z, const la_strides *z_strides,
+                       const float *dt_bias, rgdr_dtype dtype, const void *state_pool,
+                       rgdr_dtype state_dtype, const int32_t *actual_seq_lengths,
+                       const int32_t *ssm_state_indices, const int32_t *num_accepted_tokens,
+                       uint32_t flags, int32_t B, int32_t T, int32_t C, int32_t N, int32_t G,
+                       int32_t N_slots, void *out, const la_strides *out_strides, void *state_out,
+                       hipStream_t stream);
+
+/*
+ * ssm_prefill_workspace_size -- the workspace with which ssm_prefill runs a call of these sizes on
+ * the current device in parallel over the tokens: *bytes = 0 when it needs none.
+ * Errors: RGDR_ERR_NULL (bytes NULL), RGDR_ERR_SHAPE, RGDR_ERR_UNSUPPORTED as ssm_prefill;
+ * RGDR_ERR_HIP if the device cannot be queried.
+ */
+rgdr_status ssm_prefill_workspace_size(int32_t B, int32_t T, int32_t C, int32_t N, int32_t G,
+                                       size_t *bytes);
+
+/*
+ * ssm_prefill -- ssm_decode over whole prompts: the same arguments, results and errors, with
+ * 1 <= T <= 65536.
+ *   workspace        device memory, 256-byte aligned, owned by the caller, written before it is
+ *                    read; used until the call completes on `stream`, so calls that share one
+ *                    must be ordered. With NULL, or fewer bytes than ssm_prefill_workspace_size
+ *                    says, an entry's tokens are worked through in order; with it, calls of few
+ *                    channels work on parts of a prompt at once. Both hold the same precision, and
+ *                    round differently.
+ *   workspace_bytes  its size.
+ */
+rgdr_status ssm_prefill(const void *x, const la_strides *x_strides, const void *dt,
+                        const la_strides *dt_strides, const float *A, const void *Bm,
+                        const la_strides *Bm_strides, const void *Cm, const la_strides *Cm_strides,
+                        const float *D, const void *z, const la_strides *z_strides,
+                        const float *dt_bias, rgdr_dtype dtype, const void *state_pool,
+                        rgdr_dtype state_dtype, const int32_t *actual_seq_lengths,
+                        const int32_t *ssm_state_indices, const int32_t *num_accepted_tokens,
+                        uint32_t flags, int32_t B, int32_t T, int32_t C, int32_t N, int32_t G,
+                        int32_t N_slots, void *out, const la_strides *out_strides, void *state_out,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * rgdr_validate_host -- checks the index arrays of one rgdr_decode call, given as HOST
