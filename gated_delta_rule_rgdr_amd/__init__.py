@@ -1131,7 +1131,7 @@ def ssm_decode(x, dt, A, B, C, state_pool, actual_seq_lengths=None, ssm_state_in
 
     x, dt, z ``[B,T,C]`` and B, C ``[B,T,G,N]`` (group g serves channels g C/G on) of one type,
     float32, float16 or bfloat16, any strides with the last axis contiguous and rows at multiples of
-    8 elements (columns of a wider projection are fine); channels a multiple of 8, N 8, 16 or 32. A
+    8 elements (columns of a wider projection are fine); C/G a multiple of 8, N 8, 16 or 32. A
     float32 ``[C,N]``, D and dt_bias float32 ``[C]``; D, z and dt_bias may be left out.
     ``dt_softplus=False`` takes ``d = dt + dt_bias``. state_pool float32 or bfloat16
     ``[N_slots,C,N]``, updated in place unless ``state_out`` is given; a new sequence's slot is

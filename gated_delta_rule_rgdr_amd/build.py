@@ -21,7 +21,7 @@ BINDING = os.path.join(PKG, "_la_binding.so")
 
 SOURCES = ["rgdr_decode.hip", "rgdr_prefill.hip", "la_gate.hip", "la_decode.hip",
            "la_prefill.hip", "la_state.hip", "la_norm_gate.hip", "la_conv.hip", "la_rope.hip",
-           "ssm_scan.hip", "rgdr_host.cpp"]
+           "ssm_decode.hip", "ssm_prefill.hip", "rgdr_host.cpp"]
 ARCH = "gfx950"
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

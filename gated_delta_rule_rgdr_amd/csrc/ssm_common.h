@@ -1,0 +1,109 @@
+// ssm_common.h -- what the selective state space scan's kernels for few tokens (ssm_decode.hip) and for
+// prompts (ssm_prefill.hip) share: the argument block, its checks, and the arithmetic of a token. Not
+// part of the C ABI.
+//
+// On the N states h of each channel, token by token:
+//     d = softplus(dt + dt_bias),  h[n] = exp(d A[n]) h[n] + d x B[n],
+//     y = (sum_n C[n] h[n] + D x) silu(z).
+// exp(d A) is exp2(d (A log2 e)), with A log2 e rounded once: the hardware's exponential is to base 2.
+#pragma once
+
+#include "la_common.h"
+
+namespace rgdr {
+
+struct SsmArgs {
+    const void *x, *dt, *z, *Bm, *Cm, *pool;
+    const float *A, *D, *dt_bias;  // z, D, dt_bias may be null
+    void *out, *pool_out;
+    const int32_t *lens, *idx, *nacc;  // each may be null
+    LaStrides sx, sdt, sz, sB, sC, so;
+    int B, T, C, G, N_slots;
+    bool softplus, in_place;
+};
+
+__device__ __forceinline__ LaEntry ssm_entry(const SsmArgs &a, int b) {
+    LaEntry e;
+    e.slot = a.idx ? a.idx[b] : b;
+    e.state = e.slot >= 0 && e.slot < a.N_slots;
+    const int L = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    e.L = e.state ? L : 0;
+    e.n = a.nacc ? min(max(a.nacc[b], 0), e.L) : e.L;
+    return e;
+}
+
+// A log2 e; minus infinity acts as a large negative number, so that a step of 0 keeps the state.
+__device__ __forceinline__ float ssm_log2_decay(float A) {
+    const float l = A * 1.44269504088896340736f;
+    return l < -3e38f ? -3e38f : l;
+}
+__device__ __forceinline__ float ssm_step(float dt, float bias, bool softplus) {
+    const float s = dt + bias;
+    return softplus ? softplus_fast(s) : s;
+}
+// (sum + D x) silu(z)
+__device__ __forceinline__ float ssm_out(float sum, float D, float x, bool gated, float z) {
+    const float y = __builtin_fmaf(D, x, sum);
+    return gated ? y * (z * sigmoid_fast(z)) : y;
+}
+
+// K values of E in a row from 2 K- or 4 K-byte aligned memory, as they are stored and as fp32.
+template <typename E, int K>
+struct Row {
+    static constexpr int BYTES = K * (int)sizeof(E), WORDS = BYTES / 4;
+    static_assert(BYTES % 4 == 0 && (WORDS <= 2 || WORDS % 4 == 0), "whole loads");
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const E *p) {
+        typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+        if constexpr (WORDS == 1) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else if constexpr (WORDS == 2) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+            w[0] = v[0];
+            w[1] = v[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const u32x4 v = *(reinterpret_cast<const u32x4 *>(p) + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(E) == 4)
+            return __uint_as_float(w[i]);
+        else if constexpr (__is_same(E, _Float16))
+            return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16))));
+        else
+            return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+};
+template <typename E, int K>
+__device__ __forceinline__ void row_put(E *p, const float (&y)[K]) {
+    constexpr int V = RowVec<E>::N;
+#pragma unroll
+    for (int i = 0; i < K / V; ++i) {
+        float part[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[j] = y[i * V + j];
+        *(reinterpret_cast<u32x4 *>(p) + i) = RowVec<E>::put(part);
+    }
+}
+
+// The argument checks of ssm_decode and ssm_prefill (T up to max_t), and the kernels' argument block.
+// B = 0 is RGDR_OK with nothing to launch.
+rgdr_status ssm_check_sizes(int max_t, int32_t B, int32_t T, int32_t C, int32_t N, int32_t G);
+rgdr_status ssm_check(SsmArgs &a, int max_t, const void *x, const la_strides *x_strides, const void *dt,
+                      const la_strides *dt_strides, const float *A, const void *Bm, const la_strides *Bm_strides,
+                      const void *Cm, const la_strides *Cm_strides, const float *D, const void *z,
+                      const la_strides *z_strides, const float *dt_bias, int dtype, const void *state_pool,
+                      int state_dtype, const int32_t *lens, const int32_t *idx, const int32_t *nacc, uint32_t flags,
+                      int32_t B, int32_t T, int32_t C, int32_t N, int32_t G, int32_t N_slots, void *out,
+                      const la_strides *out_strides, void *state_out);
+
+}  // namespace rgdr

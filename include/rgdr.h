@@ -623,8 +623,8 @@ enum { SSM_DT_SOFTPLUS = 1u /* the step is softplus(dt + dt_bias), not dt + dt_b
  *   actual_seq_lengths, ssm_state_indices, num_accepted_tokens
  *              int32 [B], each may be NULL, as in la_decode.
  *   flags      0 or SSM_DT_SOFTPLUS.
- *   B, T, C, N, G, N_slots   B >= 0 (0: nothing is read or launched); C a multiple of 8 and of G;
- *              N in {8, 16, 32}.
+ *   B, T, C, N, G, N_slots   B >= 0 (0: nothing is read or launched); C a multiple of G, C / G of
+ *              8; N in {8, 16, 32}.
  *   out        as x with out_strides (NULL: contiguous; rows must not overlap), written entirely:
  *              rows of tokens past an entry's length, and of skipped entries, are +0.0. It overlaps
  *              no input.

@@ -104,7 +104,7 @@ BAD_SCAN = [
     (dict(xs=(-256, 0, 64)), SHAPE), (dict(dts=(1 << 61, 0, 64)), SHAPE), (dict(Bs=(-8, 16, 32)), SHAPE),
     (dict(Cs=(1 << 61, 16, 32)), SHAPE), (dict(os=(256, 0, 32)), SHAPE), (dict(os=(0, 0, 64)), SHAPE),
     (dict(B=1 << 24, C=1024, G=1), SHAPE),
-    (dict(C=60), UNSUP), (dict(N=12), UNSUP), (dict(N=64), UNSUP), (dict(fl=2), UNSUP),
+    (dict(C=60), UNSUP), (dict(G=16), UNSUP), (dict(N=12), UNSUP), (dict(N=64), UNSUP), (dict(fl=2), UNSUP),
     (dict(ty=MXI8), DTYPE), (dict(ty=7), DTYPE), (dict(st=F16), DTYPE), (dict(st=MXI8), DTYPE),
     (dict(x=P + 8), ALIGN), (dict(dt=P + 2), ALIGN), (dict(A=P + 4), ALIGN), (dict(Bm=P + 8), ALIGN),
     (dict(Cm=P + 2), ALIGN), (dict(D=P + 4), ALIGN), (dict(z=P + 8), ALIGN), (dict(bias=P + 8), ALIGN),
