@@ -140,6 +140,19 @@ __device__ __forceinline__ LaEntry la_entry(const LaArgs &a, int b) {
     return e;
 }
 
+// The entry with the rank-th most tokens (of up to 64 entries; else entry `rank`).
+__device__ __forceinline__ int entry_of_rank(const int32_t *lens, int B, int T, int rank) {
+    if (!lens || B < 2 || B > 64) return rank;
+    const int lane = threadIdx.x & 63;
+    const int L = lane < B ? min(max(lens[lane], 0), T) : -1;
+    int r = 0;  // of this lane's entry: how many are longer, or as long and before it
+    for (int j = 0; j < B; ++j) {
+        const int other = __builtin_amdgcn_readlane(L, j);
+        r += other > L || (other == L && j < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < B && r == rank));
+}
+
 // Log decays below this act as this: exp of it is zero even in fp64, and sums of them stay far
 // from the range's end, so differences of such sums are never infinity minus infinity. NaN passes.
 constexpr float kMinLogDecay = -1024.0f;
@@ -183,6 +196,17 @@ inline bool la_rows_distinct(const LaStrides &s, int B, int H, int T, int D) {
 inline bool la_extent_ok(const LaStrides &s, int B, int H, int T, int D) {
     const __int128 e = (__int128)s.b * (B - 1) + (__int128)s.h * (H - 1) + (__int128)s.t * (T - 1) + D;
     return e < ((__int128)1 << 60);
+}
+
+// The current device's compute units; 0 if it cannot be asked.
+inline int la_compute_units() {
+    static int known[64];  // zero: not asked yet; every writer writes the same number
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED))) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+    return n;
 }
 
 inline bool la_index_aligned(const int32_t *lens, const int32_t *idx, const int32_t *nacc) {

@@ -165,18 +165,6 @@ struct LaItem {
     bool live;
 };
 
-__device__ __forceinline__ int entry_of_rank(const LaArgs &a, int rank) {
-    if (!a.lens || a.B < 2 || a.B > 64) return rank;
-    const int lane = threadIdx.x & 63;
-    const int L = lane < a.B ? min(max(a.lens[lane], 0), a.T) : -1;
-    int r = 0;  // of this lane's entry: how many are longer, or as long and before it
-    for (int j = 0; j < a.B; ++j) {
-        const int other = __builtin_amdgcn_readlane(L, j);
-        r += other > L || (other == L && j < lane);
-    }
-    return __builtin_ctzll(__ballot(lane < a.B && r == rank));
-}
-
 template <bool SEGMENTS>
 __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
     const int local = blockIdx.x / kXcds, share = a.group * p.tiles;  // workgroups of a query/key head
@@ -192,7 +180,7 @@ __device__ __forceinline__ LaItem la_item(const LaArgs &a, const LaPlan &p) {
     const int hq = unit % a.Hq;
     unit /= a.Hq;
     m.seg = SEGMENTS ? unit % p.nseg : 0;
-    m.b = entry_of_rank(a, m.live ? (SEGMENTS ? unit / p.nseg : unit) : 0);
+    m.b = entry_of_rank(a.lens, a.B, a.T, m.live ? (SEGMENTS ? unit / p.nseg : unit) : 0);
     m.h = hq * a.group + in_group;
     return m;
 }
@@ -813,16 +801,6 @@ __global__ __launch_bounds__(256) void la_scan_kernel(const LaArgs a, const LaPl
     ws[last * step] = S;
 }
 
-static int cu_count() {
-    static int known[64];  // zero: not asked yet; every writer writes the same number
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 0;
-    if (dev >= 0 && dev < 64 && (n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED))) return n;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-    if (dev >= 0 && dev < 64) __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
-    return n;
-}
-
 // How many segments: as many as fill the device's resident workgroups (two on a compute unit, one
 // with D_k = 256), of at least two chunks; and whether they pay. With `fill` the share of the
 // resident workgroups that the segments take, a chunk of a segment costs about 1.4 + 1.1 fill
@@ -836,7 +814,7 @@ static bool plan_segments(int B, int H_v, int T, int D_k, int D_v, LaPlan &p, si
     bytes = 0;
     p.nseg = 1;
     p.seg_len = T;
-    const int cus = cu_count();
+    const int cus = la_compute_units();
     if (cus <= 0) return false;
     const long long tiles = (D_v + kCols - 1) / kCols;
     const long long items = (long long)B * H_v * tiles;

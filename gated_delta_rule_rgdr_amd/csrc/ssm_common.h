@@ -37,14 +37,24 @@ __device__ __forceinline__ float ssm_log2_decay(float A) {
     const float l = A * 1.44269504088896340736f;
     return l < -3e38f ? -3e38f : l;
 }
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|). u = 1 + e rounded loses w = e - (u - 1), at most
+// 2^-24: log1p(e) = log(u) + log(1 + w / u), and w instead of the last term is off by w (1 - 1 / u) at
+// most, below 2^-24 of the sum. u is in [1, 2], so the hardware's logarithm needs no scaling. NaN and
+// infinities pass.
+__device__ __forceinline__ float ssm_softplus(float x) {
+    const float e = __builtin_amdgcn_exp2f(-1.44269504088896340736f * __builtin_fabsf(x));
+    const float u = 1.0f + e, w = e - (u - 1.0f);
+    return __builtin_fmaf(__builtin_amdgcn_logf(u), 0.693147180559945309417f, __builtin_fmaxf(x, 0.f)) + w;
+}
 __device__ __forceinline__ float ssm_step(float dt, float bias, bool softplus) {
     const float s = dt + bias;
-    return softplus ? softplus_fast(s) : s;
+    return softplus ? ssm_softplus(s) : s;
 }
 // (sum + D x) silu(z)
 __device__ __forceinline__ float ssm_out(float sum, float D, float x, bool gated, float z) {
     const float y = __builtin_fmaf(D, x, sum);
-    return gated ? y * (z * sigmoid_fast(z)) : y;
+    if (!gated) return y;
+    return y * (z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z)));
 }
 
 // K values of E in a row from 2 K- or 4 K-byte aligned memory, as they are stored and as fp32.

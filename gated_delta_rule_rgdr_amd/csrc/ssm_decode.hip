@@ -164,10 +164,11 @@ rgdr_status ssm_check(SsmArgs &a, int max_t, const void *x, const la_strides *x_
     a.so = la_strides_or(out_strides, (long long)T * C, 0, C);
     a.sB = la_strides_or(Bm_strides, (long long)T * G * N, N, (long long)G * N);
     a.sC = la_strides_or(Cm_strides, (long long)T * G * N, N, (long long)G * N);
+    const long long max_stride = dtype == RGDR_F32 ? kMaxTokenStride / 2 : kMaxTokenStride;
     for (const LaStrides *s : {&a.sx, &a.sdt, &a.sz, &a.so})
-        if (!la_strides_ok(*s) || !la_extent_ok(*s, B, 1, T, C)) return RGDR_ERR_SHAPE;
+        if (!la_strides_ok(*s) || (T > 1 && s->t > max_stride) || !la_extent_ok(*s, B, 1, T, C)) return RGDR_ERR_SHAPE;
     for (const LaStrides *s : {&a.sB, &a.sC})
-        if (!la_strides_ok(*s) || !la_extent_ok(*s, B, G, T, N)) return RGDR_ERR_SHAPE;
+        if (!la_strides_ok(*s) || (T > 1 && s->t > max_stride) || !la_extent_ok(*s, B, G, T, N)) return RGDR_ERR_SHAPE;
     if (!la_rows_distinct(a.so, B, 1, T, C) || (!idx && N_slots < B)) return RGDR_ERR_SHAPE;
     for (const LaStrides *s : {&a.sx, &a.sdt, &a.so})
         if (!la_strides_aligned(*s, B, 1, T)) return RGDR_ERR_ALIGN;

@@ -3,14 +3,25 @@
 
 namespace rgdr {
 
-constexpr int kTC = 32;  // tokens of a chunk
-constexpr int kCH = 64;  // channels of a workgroup
-constexpr int kRow = kTC + 4;                           // floats of a channel's row in LDS: d, or d x and then y
-constexpr int kRows = kCH * kRow + (kCH / 8 - 1) * 4;   // rows of eight channels start 4 floats further
-__device__ __forceinline__ int ssm_at(int c, int t) { return c * kRow + (c >> 3) * 4 + t; }
+constexpr int kPieces = 256;  // a workgroup's threads: (token, 8 channels) pieces of a chunk
+
+// The sizes that go with WAYS lanes for each channel's states.
+template <int N, int WAYS>
+struct SsmShape {
+    static constexpr int NP = N / WAYS;                // states of a lane
+    static constexpr int CW = 64 / WAYS, CH = 4 * CW;  // channels of a wave, of a workgroup
+    static constexpr int TPT = CH / 8, TC = kPieces / TPT;  // threads for each token, tokens of a chunk
+    static constexpr int ROW = TC + 4;                 // floats of a channel's row in LDS
+    static constexpr int ROWS = CH * ROW + (CH / 8 - 1) * 4;  // rows of 8 channels start 4 floats further
+    static constexpr int NV = 2 * N / TPT;             // values of B or C that a thread stages
+    static constexpr bool BY_TOKEN = NP >= 4;          // B and C in LDS: [t][n], else [n][t]
+    static constexpr int BC = BY_TOKEN ? TC * N : N * ROW;
+    static __device__ __forceinline__ int at(int c, int t) { return c * ROW + (c >> 3) * 4 + t; }
+    static __device__ __forceinline__ int bc_at(int t, int n) { return BY_TOKEN ? t * N + n : n * ROW + t; }
+};
 
 struct SsmPlan {
-    int c_blocks, groups;  // groups of B and C that a workgroup's channels may belong to
+    int ways, c_blocks;
     int segs, seg_len;
     float *ends;  // [B][segs][C][N]: a segment's end state from zero, then its incoming state
     float *sums;  // [B][segs][C]: its sum of d
@@ -18,45 +29,107 @@ struct SsmPlan {
 
 enum SsmPass { kSsmWhole, kSsmEnds, kSsmSegment };
 
-// A workgroup has 64 channels of one entry and works through chunks of 32 tokens (of the entry, or of one
+// WAYS values of each lane, one for each token; lane l = w CW + c is left with the sum of value w over the
+// WAYS lanes of channel c. Each step halves the values: lanes of one half take the first half of them,
+// the others the second.
+template <int WAYS>
+__device__ __forceinline__ float ssm_meet(float (&y)[WAYS]) {
+    const auto bits = [](float x) { return __float_as_int(x); };
+#pragma unroll
+    for (int i = 0; i < WAYS / 2; ++i) {
+        const auto r = __builtin_amdgcn_permlane32_swap(bits(y[i]), bits(y[i + WAYS / 2]), false, false);
+        y[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < WAYS / 4; ++i) {
+        const auto r = __builtin_amdgcn_permlane16_swap(bits(y[i]), bits(y[i + WAYS / 4]), false, false);
+        y[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (WAYS >= 8) {
+#pragma unroll
+        for (int i = 0; i < WAYS / 8; ++i) {  // lane ^ 8: the first value in lanes without that bit
+            const float v = y[i], w = y[i + WAYS / 8];
+            y[i] = __int_as_float(__builtin_amdgcn_update_dpp(bits(w), bits(v), 0x128, 0xF, 0x3, false)) +
+                   __int_as_float(__builtin_amdgcn_update_dpp(bits(v), bits(w), 0x128, 0xF, 0xC, false));
+        }
+    }
+    if constexpr (WAYS >= 16) {  // lane ^ 4
+        const float v = y[0], w = y[1];
+        y[0] = __int_as_float(__builtin_amdgcn_update_dpp(bits(w), bits(v), 0x104, 0xF, 0x5, false)) +
+               __int_as_float(__builtin_amdgcn_update_dpp(bits(v), bits(w), 0x114, 0xF, 0xA, false));
+    }
+    return y[0];
+}
+
+// What WAYS tokens bring to a lane.
+template <int N, int WAYS, bool WITH_C>
+struct SsmBatch {
+    using S = SsmShape<N, WAYS>;
+    float d[WAYS], u[WAYS], B[WAYS][S::NP], C[WAYS][S::NP];
+    __device__ __forceinline__ void read(const float *d_row, const float *u_row, const float *tB, const float *tC, int t) {
+#pragma unroll
+        for (int k = 0; k < WAYS; k += 4) {
+            *reinterpret_cast<f32x4 *>(d + k) = *reinterpret_cast<const f32x4 *>(d_row + t + k);
+            *reinterpret_cast<f32x4 *>(u + k) = *reinterpret_cast<const f32x4 *>(u_row + t + k);
+        }
+#pragma unroll
+        for (int i = 0; i < S::NP; ++i) {
+#pragma unroll
+            for (int j = 0; j < WAYS; ++j) {
+                B[j][i] = tB[S::bc_at(t + j, i)];
+                if (WITH_C) C[j][i] = tC[S::bc_at(t + j, i)];
+            }
+        }
+    }
+};
+
+// A workgroup has up to CH channels of one entry and group and works through chunks of TC tokens (of the entry, or of one
 // of its segments). What is done once for each token and channel (softplus, d x, the gate) and all memory
-// access goes by (token, 8 channels) for each thread, whole 16-byte pieces; the states go by channel:
-// four lanes, 16 apart, hold a channel's N states, so that a lane has N / 4 of them in registers for
-// all tokens. d, d x and the sums over the states pass between the two through LDS, as do B and C in fp32.
-// The four lanes' sums of four tokens meet in three register swaps, which leave each lane with one
-// token's.
-template <typename E, int N, int PASS>
-__global__ __launch_bounds__(256) void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {
-    constexpr int NP = N / 4;
-    extern __shared__ __align__(16) float lds[];
-    float *sd = lds, *su = lds + kRows, *sB = su + kRows, *sC = sB + p.groups * kTC * N;
+// access of them goes by (token, 8 channels) for each thread, whole 16-byte pieces; the states go by
+// channel: WAYS lanes hold a channel's N states, so that a lane has N / WAYS of them in registers for all
+// tokens. d, d x and the sums over the states pass between the two through LDS, as do B and C in fp32.
+template <typename E, int N, int WAYS, int PASS>
+__global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4) : 2) void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {
+    using S = SsmShape<N, WAYS>;
+    constexpr int NP = S::NP, TC = S::TC;
+    __shared__ __align__(16) float sd[S::ROWS], su[S::ROWS];
+    __shared__ __align__(16) float sB[S::BC], sC[S::BC];
+    __shared__ __align__(16) float s_bias[S::CH], s_D[S::CH];
     const int cb = blockIdx.x % p.c_blocks, s = blockIdx.x / p.c_blocks % p.segs;
-    const int b = blockIdx.x / p.c_blocks / p.segs;
-    const int c0 = cb * kCH, Cg = a.C / a.G;
+    const int b = entry_of_rank(a.lens, a.B, a.T, blockIdx.x / p.c_blocks / p.segs);
     const LaEntry e = ssm_entry(a, b);
     const int t_begin = s * p.seg_len, t_end = min(e.L, t_begin + p.seg_len);
     if (PASS == kSsmEnds && t_begin + p.seg_len >= e.L) return;
 
-    // by token and 8 channels
-    const int st = threadIdx.x / 8, sc = threadIdx.x % 8 * 8, cs = c0 + sc;
-    const bool c_ok = cs < a.C;
-    const E *px = static_cast<const E *>(a.x) + b * a.sx.b + cs;
-    const E *pdt = static_cast<const E *>(a.dt) + b * a.sdt.b + cs;
-    const E *pz = static_cast<const E *>(a.z) + b * a.sz.b + cs;
+    // by token and 8 channels: a uniform address, which moves on by chunks, and a thread's own 32-bit offset
+    // (127 tokens at strides of at most 2^25 bytes)
+    const int st = threadIdx.x / S::TPT, sc = threadIdx.x % S::TPT * 8;
+    const int Cg = a.C / a.G, per = (Cg + S::CH - 1) / S::CH, g = cb / per;  // this workgroup's group,
+    const int c0 = g * Cg + cb % per * S::CH, channels = min(S::CH, Cg - cb % per * S::CH);  // and channels
+    const int cs = c0 + sc;
+    const bool c_ok = sc < channels;
+    const auto first = [&](const void *p, const LaStrides &s) {
+        return static_cast<const char *>(p) + (b * s.b + t_begin * s.t) * (long long)sizeof(E);
+    };
+    const auto step = [&](const LaStrides &s) { return (uint32_t)s.t * (uint32_t)sizeof(E); };  // a token's bytes
+    const uint32_t dx = step(a.sx), ddt = step(a.sdt), dz = step(a.sz), dB = step(a.sB), dC = step(a.sC);
+    const char *px = first(a.x, a.sx) + c0 * sizeof(E), *pdt = first(a.dt, a.sdt) + c0 * sizeof(E);
+    const char *pz = first(a.z, a.sz) + c0 * sizeof(E);
+    const char *pB = first(a.Bm, a.sB) + g * a.sB.h * sizeof(E), *pC = first(a.Cm, a.sC) + g * a.sC.h * sizeof(E);
     E *pout = static_cast<E *>(a.out) + b * a.so.b + cs;
     if (PASS != kSsmEnds && c_ok) {
         const float none[8] = {};
-        for (int t = max(e.L, t_begin) + st; t < min(a.T, t_begin + p.seg_len); t += kTC)
-            row_put(pout + (long long)t * a.so.t, none);
+        for (int t = max(e.L, t_begin); t < min(a.T, t_begin + p.seg_len) - st; t += TC)
+            row_put(pout + (t + st) * a.so.t, none);
     }
 
-    // by channel and a quarter of its states
-    const int q = threadIdx.x / 16 % 4, c = threadIdx.x / 64 * 16 + threadIdx.x % 16, cc = c0 + c;
-    const int g0 = c0 / Cg, gl = min(cc, a.C - 1) / Cg - g0;
+    // by channel and a part of its states
+    const int q = threadIdx.x % 64 / S::CW, c = threadIdx.x / 64 * S::CW + threadIdx.x % S::CW, cc = c0 + c;
+    const bool mine = c < channels;
     const size_t slot_at = ((size_t)(e.state ? e.slot : 0) * a.C + cc) * N + q * NP;
     const size_t seg_at = ((size_t)(b * p.segs + s) * a.C + cc) * N + q * NP;
     const auto commit = [&](const float (&h)[NP]) {
-        if (cc >= a.C) return;
+        if (!mine) return;
         if (state_f32) {
             float *to = static_cast<float *>(a.pool_out) + slot_at;
 #pragma unroll
@@ -69,114 +142,185 @@ __global__ __launch_bounds__(256) void ssm_prefill_kernel(const SsmArgs a, const
     };
     float h[NP], A[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        h[i] = A[i] = 0.f;
-        if (cc >= a.C || !e.state) continue;
-        A[i] = ssm_log2_decay(a.A[(size_t)cc * N + q * NP + i]);
-        if (PASS == kSsmWhole)
-            h[i] = state_f32 ? static_cast<const float *>(a.pool)[slot_at + i]
-                             : bf16_to_f32(static_cast<const uint16_t *>(a.pool)[slot_at + i]);
-        if (PASS == kSsmSegment && t_begin < max(e.L, 1)) h[i] = p.ends[seg_at + i];
+    for (int i = 0; i < NP; ++i) h[i] = A[i] = 0.f;
+    if (mine && e.state) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            A[i] = ssm_log2_decay(a.A[(size_t)cc * N + q * NP + i]);
+            if (PASS == kSsmWhole)
+                h[i] = state_f32 ? static_cast<const float *>(a.pool)[slot_at + i]
+                                 : bf16_to_f32(static_cast<const uint16_t *>(a.pool)[slot_at + i]);
+            if (PASS == kSsmSegment && t_begin < max(e.L, 1)) h[i] = p.ends[seg_at + i];
+        }
     }
     if (PASS != kSsmEnds && s == 0 && e.state && e.n == 0 && !a.in_place) commit(h);
 
-    float bias[8], D[8];
+    if (st == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = c_ok && a.dt_bias ? a.dt_bias[cs + i] : 0.f;
-        D[i] = c_ok && a.D ? a.D[cs + i] : 0.f;
-    }
-    Row<E, 8> x, dt, z, nx, ndt, nz;
-    Row<E, NP> bc, nbc;
-    const bool is_C = threadIdx.x % 8 >= 4;
-    const int col = threadIdx.x % 4 * NP;
-    const auto bc_row = [&](int t, int g) {
-        return is_C ? static_cast<const E *>(a.Cm) + b * a.sC.b + (long long)t * a.sC.t + g * a.sC.h + col
-                    : static_cast<const E *>(a.Bm) + b * a.sB.b + (long long)t * a.sB.t + g * a.sB.h + col;
-    };
-    const auto load = [&](int t0, Row<E, 8> &x, Row<E, 8> &dt, Row<E, 8> &z, Row<E, NP> &bc) {
-        x.zero();
-        dt.zero();
-        z.zero();
-        bc.zero();
-        const int t = t0 + st;
-        if (t >= t_end) return;
-        if (c_ok) {
-            x.load(px + (long long)t * a.sx.t);
-            dt.load(pdt + (long long)t * a.sdt.t);
-            if (PASS != kSsmEnds && a.z) z.load(pz + (long long)t * a.sz.t);
+        for (int i = 0; i < 8; ++i) {
+            s_bias[sc + i] = c_ok && a.dt_bias ? a.dt_bias[cs + i] : 0.f;
+            s_D[sc + i] = c_ok && a.D ? a.D[cs + i] : 0.f;
         }
-        if (PASS != kSsmEnds || !is_C) bc.load(bc_row(t, g0));
+    }
+    __syncthreads();
+    Row<E, 8> x, dt, z, nx, nz;
+    nx.zero();
+    dt.zero();
+    nz.zero();
+    Row<E, S::NV> bc;
+    bc.zero();
+    const bool is_C = threadIdx.x % S::TPT >= S::TPT / 2;
+    const int col = threadIdx.x % (S::TPT / 2) * S::NV;
+    // (a thread without a token or channels keeps what it has: it is masked, or never stored)
+    const auto load = [&](int left) {
+        if (st >= left) return;
+        const auto at = [](const char *p, uint32_t offset) { return reinterpret_cast<const E *>(p + offset); };
+        const uint32_t o = sc * (uint32_t)sizeof(E);
+        if (c_ok) {
+            nx.load(at(px, st * dx + o));
+            dt.load(at(pdt, st * ddt + o));
+            if (PASS != kSsmEnds && a.z) nz.load(at(pz, st * dz + o));
+        }
+        if (!is_C)
+            bc.load(at(pB, st * dB + col * (uint32_t)sizeof(E)));
+        else if (PASS != kSsmEnds)
+            bc.load(at(pC, st * dC + col * (uint32_t)sizeof(E)));
     };
-    load(t_begin, x, dt, z, bc);
+    // What a thread stages of the chunk of nt tokens that was loaded last: computed before the chunk before
+    // it is stored, since a wait for loads behind a store would wait for the store.
+    float d[8], u[8], f[S::NV];
+    const auto prepare = [&](int nt) {
+        const bool live = st < nt;
+        Row<float, 8> bias;
+        bias.load(s_bias + sc);
+        if (a.softplus) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = ssm_softplus(dt.get(i) + bias.get(i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = dt.get(i) + bias.get(i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = d[i] * nx.get(i);
+#pragma unroll
+        for (int i = 0; i < S::NV; ++i) f[i] = bc.get(i);
+        if (nt < TC) {  // tokens past the chunk's end leave the state as it is
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] = live ? d[i] : 0.f;
+                u[i] = live ? u[i] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < S::NV; ++i) f[i] = live ? f[i] : 0.f;
+        }
+    };
+    // (the accepted tokens end a chunk, so that the state after them is the one at its end)
+    const auto tokens = [&](int t0) { return min(min(TC, t_end - t0), t0 < e.n ? e.n - t0 : TC); };
+    int nt = tokens(t_begin);
+    load(t_end - t_begin);
+    prepare(nt);
 
     float sum = 0.f;
     for (int t0 = t_begin; t0 < t_end;) {
-        // (the accepted tokens end a chunk, so that the state after them is the one at its end)
-        int t1 = min(t0 + kTC, t_end);
-        if (t0 < e.n) t1 = min(t1, e.n);
-        const bool live = t0 + st < t1;
+        const bool live = st < nt;
+        x = nx;
+        z = nz;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float d = live ? ssm_step(dt.get(i), bias[i], a.softplus) : 0.f;
-            sd[ssm_at(sc + i, st)] = d;
-            su[ssm_at(sc + i, st)] = live ? d * x.get(i) : 0.f;
+            sd[S::at(sc + i, st)] = d[i];
+            su[S::at(sc + i, st)] = u[i];
         }
-        for (int g = 0; g < p.groups; ++g) {
-            if (g > 0) {
-                bc.zero();
-                if (live && g0 + g < a.G) bc.load(bc_row(t0 + st, g0 + g));
-            }
-            float *to = (is_C ? sC : sB) + (g * kTC + st) * N + col;
+        float *to = (is_C ? sC : sB) + S::bc_at(st, col);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) to[i] = live ? bc.get(i) : 0.f;
-        }
+        for (int i = 0; i < S::NV; ++i) to[S::bc_at(0, i)] = f[i];
         __syncthreads();
-        load(t1, nx, ndt, nz, nbc);
-        const float *tB = sB + gl * kTC * N + q * NP, *tC = sC + gl * kTC * N + q * NP;
-        const int groups4 = (t1 - t0 + 3) / 4;
-        for (int k = 0; k < groups4; ++k) {
-            const f32x4 d4 = *reinterpret_cast<const f32x4 *>(sd + ssm_at(c, 4 * k));
-            const f32x4 u4 = *reinterpret_cast<const f32x4 *>(su + ssm_at(c, 4 * k));
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float *rB = tB + (4 * k + j) * N, *rC = tC + (4 * k + j) * N;
-                y[j] = 0.f;
+        px += (uint32_t)nt * dx;
+        pdt += (uint32_t)nt * ddt;
+        pz += (uint32_t)nt * dz;
+        pB += (uint32_t)nt * dB;
+        pC += (uint32_t)nt * dC;
+        load(t_end - t0 - nt);
+        const float *d_row = sd + S::at(c, 0), *tB = sB + S::bc_at(0, q * NP), *tC = sC + S::bc_at(0, q * NP);
+        float *u_row = su + S::at(c, 0);
+        float part = 0.f;
+        if constexpr (WAYS == 4) {
+            // LDS reads go ahead: d and d x by four tokens, B and C by two
+            f32x4 d4[2], u4[2];
+            float B[4][NP], C[4][NP];
+            const auto read = [&](int t) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d4[j] * A[i]), h[i], u4[j] * rB[i]);
-                    if (PASS != kSsmEnds) y[j] = __builtin_fmaf(rC[i], h[i], y[j]);
+                    B[t % 4][i] = tB[S::bc_at(t, i)];
+                    if (PASS != kSsmEnds) C[t % 4][i] = tC[S::bc_at(t, i)];
                 }
+            };
+            d4[0] = *reinterpret_cast<const f32x4 *>(d_row);
+            u4[0] = *reinterpret_cast<const f32x4 *>(u_row);
+            read(0);
+            read(1);
+#pragma unroll
+            for (int t = 0; t < TC; t += 4) {
+                if (t >= nt) break;
+                float y[4];
+                const int now = t / 4 % 2;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (t + j + 2 < TC) read(t + j + 2);
+                    if (j == 0 && t + 4 < TC) {
+                        d4[1 - now] = *reinterpret_cast<const f32x4 *>(d_row + t + 4);
+                        u4[1 - now] = *reinterpret_cast<const f32x4 *>(u_row + t + 4);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    y[j] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d4[now][j] * A[i]), h[i],
+                                              u4[now][j] * B[(t + j) % 4][i]);
+                        if (PASS != kSsmEnds) y[j] = __builtin_fmaf(C[(t + j) % 4][i], h[i], y[j]);
+                    }
+                }
+                if (PASS == kSsmEnds)
+                    part += (d4[now][0] + d4[now][1]) + (d4[now][2] + d4[now][3]);
+                else
+                    u_row[t + q] = ssm_meet<4>(y);
             }
-            if (PASS == kSsmEnds) {
-                sum += (d4[0] + d4[1]) + (d4[2] + d4[3]);
-            } else {
-                // lanes 32 on take tokens 2 and 3, then odd rows of 16 lanes the odd tokens
-                const auto r0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[0]), __float_as_uint(y[2]), false, false);
-                const auto r1 = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[1]), __float_as_uint(y[3]), false, false);
-                const float s0 = __uint_as_float(r0[0]) + __uint_as_float(r0[1]);
-                const float s1 = __uint_as_float(r1[0]) + __uint_as_float(r1[1]);
-                const auto r2 = __builtin_amdgcn_permlane16_swap(__float_as_uint(s0), __float_as_uint(s1), false, false);
-                su[ssm_at(c, 4 * k + q)] = __uint_as_float(r2[0]) + __uint_as_float(r2[1]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < TC; t += WAYS) {
+                if (t >= nt) break;
+                SsmBatch<N, WAYS, PASS != kSsmEnds> now;
+                now.read(d_row, u_row, tB, tC, t);
+                float y[WAYS];
+#pragma unroll
+                for (int j = 0; j < WAYS; ++j) {
+                    y[j] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(now.d[j] * A[i]), h[i], now.u[j] * now.B[j][i]);
+                        y[j] = __builtin_fmaf(now.C[j][i], h[i], y[j]);
+                    }
+                }
+                u_row[t + q] = ssm_meet<WAYS>(y);
             }
         }
+        sum += part;
+        const int t1 = t0 + nt, nt1 = tokens(t1);
         if (PASS != kSsmEnds && t1 == e.n) commit(h);
         __syncthreads();
         if (PASS != kSsmEnds && live && c_ok) {
             float y[8];
+            Row<float, 8> D;
+            D.load(s_D + sc);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                y[i] = ssm_out(su[ssm_at(sc + i, st)], D[i], x.get(i), a.z != nullptr, z.get(i));
-            row_put(pout + (long long)(t0 + st) * a.so.t, y);
+                y[i] = ssm_out(su[S::at(sc + i, st)], D.get(i), x.get(i), a.z != nullptr, z.get(i));
+            row_put(pout + (t0 + st) * a.so.t, y);
         }
-        x = nx;
-        dt = ndt;
-        z = nz;
-        bc = nbc;
+        prepare(nt1);
         t0 = t1;
+        nt = nt1;
     }
-    if (PASS == kSsmEnds && cc < a.C) {
+    if (PASS == kSsmEnds && mine) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) p.ends[seg_at + i] = h[i];
         if (q == 0) p.sums[(size_t)(b * p.segs + s) * a.C + cc] = sum;
@@ -194,8 +338,10 @@ __global__ __launch_bounds__(256) void ssm_ends_kernel(const SsmArgs a, const Ss
     if (b >= a.B) return;
     const LaEntry e = ssm_entry(a, b);
     if (!e.state) return;
-    const int segs = max(1, (e.L + p.seg_len - 1) / p.seg_len);
-    const size_t slot_at = ((size_t)e.slot * a.C + c) * N + n0;
+    const int last = max(1, (e.L + p.seg_len - 1) / p.seg_len) - 1;
+    const size_t slot_at = ((size_t)e.slot * a.C + c) * N + n0, step = (size_t)a.C * N;
+    f32x4 *ends = reinterpret_cast<f32x4 *>(p.ends + ((size_t)b * p.segs * a.C + c) * N + n0);
+    const float *sums = p.sums + (size_t)b * p.segs * a.C + c;
     float h[4], A[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -203,48 +349,47 @@ __global__ __launch_bounds__(256) void ssm_ends_kernel(const SsmArgs a, const Ss
                          : bf16_to_f32(static_cast<const uint16_t *>(a.pool)[slot_at + k]);
         A[k] = ssm_log2_decay(a.A[(size_t)c * N + n0 + k]);
     }
-    float *ends = p.ends + ((size_t)b * p.segs * a.C + c) * N + n0;
-    const float *sums = p.sums + (size_t)b * p.segs * a.C + c;
-    const size_t step = (size_t)a.C * N;
-    for (int s = 0; s < segs; ++s) {
-        f32x4 *at = reinterpret_cast<f32x4 *>(ends + s * step);
-        f32x4 end = {0, 0, 0, 0};
-        float sum = 0.f;
-        if (s + 1 < segs) {
-            end = *at;
-            sum = sums[(size_t)s * a.C];
-        }
-        *at = f32x4{h[0], h[1], h[2], h[3]};
+    constexpr int U = 8;  // loads in flight
+    for (int s0 = 0; s0 < last; s0 += U) {
+        f32x4 end[U];
+        float sum[U];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(sum * A[k]), h[k], end[k]);
+        for (int k = 0; k < U; ++k) {
+            const int s = min(s0 + k, last - 1);
+            end[k] = ends[s * step / 4];
+            sum[k] = sums[(size_t)s * a.C];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (s0 + k >= last) break;
+            ends[(s0 + k) * step / 4] = f32x4{h[0], h[1], h[2], h[3]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[k] * A[i]), h[i], end[k][i]);
+        }
     }
+    ends[last * step / 4] = f32x4{h[0], h[1], h[2], h[3]};
 }
 
-static int ssm_groups(int C, int G) {
-    const int Cg = C / G;
-    const int most = Cg % kCH == 0 ? 1 : kCH % Cg == 0 ? kCH / Cg : (kCH - 2) / Cg + 2;
-    return most < G ? most : G;
-}
-
-template <typename E, int N, int PASS>
+template <typename E, int N, int WAYS, int PASS>
 static rgdr_status launch_ssm_pass(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
-    const size_t lds = sizeof(float) * (2 * kRows + 2 * p.groups * kTC * N);
     if ((__int128)p.c_blocks * p.segs * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
-    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, PASS>), dim3((unsigned)((long long)p.c_blocks * p.segs * a.B)),
-                       dim3(256), lds, stream, a, p, f32);
+    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS>), dim3((unsigned)((long long)p.c_blocks * p.segs * a.B)),
+                       dim3(256), 0, stream, a, p, f32);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 template <typename E, int N>
 static rgdr_status launch_ssm_prefill(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
-    if (p.segs == 1) return launch_ssm_pass<E, N, kSsmWhole>(a, p, f32, stream);
+    constexpr int MOST = N < 16 ? N : 16;
+    if (p.ways == MOST) return launch_ssm_pass<E, N, MOST, kSsmWhole>(a, p, f32, stream);
+    if (p.segs == 1) return launch_ssm_pass<E, N, 4, kSsmWhole>(a, p, f32, stream);
     const long long threads = (long long)a.B * a.C * (N / 4), blocks = (threads + 255) / 256;
     if (blocks > kMaxGroups) return RGDR_ERR_SHAPE;
-    rgdr_status rc = launch_ssm_pass<E, N, kSsmEnds>(a, p, f32, stream);
+    rgdr_status rc = launch_ssm_pass<E, N, 4, kSsmEnds>(a, p, f32, stream);
     if (rc != RGDR_OK) return rc;
     hipLaunchKernelGGL(ssm_ends_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a, p, N, f32);
     if (hipGetLastError() != hipSuccess) return RGDR_ERR_HIP;
-    return launch_ssm_pass<E, N, kSsmSegment>(a, p, f32, stream);
+    return launch_ssm_pass<E, N, 4, kSsmSegment>(a, p, f32, stream);
 }
 
 template <typename E>
@@ -254,25 +399,52 @@ static rgdr_status launch_ssm_states(const SsmArgs &a, const SsmPlan &p, int N, 
     return launch_ssm_prefill<E, 32>(a, p, f32, stream);
 }
 
-// How many segments.
-static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool whole) {
+// The plan of a call in `ways` lanes for each channel and segments of seg_len tokens.
+static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
     SsmPlan p;
-    p.c_blocks = (C + kCH - 1) / kCH;
-    p.groups = ssm_groups(C, G);
-    p.segs = 1;
-    p.seg_len = T;
+    const int CH = 256 / ways;
+    p.ways = ways;
+    p.c_blocks = G * ((C / G + CH - 1) / CH);
+    p.seg_len = seg_len;
+    p.segs = (T + seg_len - 1) / seg_len;
     p.ends = p.sums = nullptr;
-    if (whole) return p;
-    const long long items = (long long)p.c_blocks * B;
-    if (items >= 512) return p;
-    const long long want = (1024 + items - 1) / items;
-    long long len = (T + want - 1) / want;
-    len = (len + kTC - 1) / kTC * kTC;
-    if (len < 2 * kTC) len = 2 * kTC;
-    if (len * 2 > T) return p;
-    p.seg_len = (int)len;
-    p.segs = (int)((T + len - 1) / len);
     return p;
+}
+
+// How many lanes for each channel, and how many segments: what costs least by the model below, in ns, whose
+// rates were measured with N = 16. A chunk's tokens take a workgroup alone on its compute unit 92 ns each
+// with four lanes for each channel and 32 with 16; the vector units allow 62 for each workgroup there with
+// four lanes, the LDS 24 with 16 (a quarter of the channels); the older waves of a compute unit go first,
+// so that the last workgroup is alone for a while. Of a segment's two passes the first takes
+// three quarters of the second; they and the scan between them are three launches.
+// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/260/224 (256);
+// C=8192 760/395/420 (256); C=512 760/260/67 (256); C=2048, T=2048 194/68/52 (128); B=2, T=300, C=4096
+// 34/26/35 (64); B=4, T=1024 105/103/120 (128); B=16 250/350/375 (256).
+static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
+    const int most = N < 16 ? N : 16;
+    const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
+    const auto cost = [&](const SsmPlan &p, double alone, double beside) {
+        const double here = (double)p.c_blocks * B * p.segs / cus;  // workgroups for each compute unit
+        const double token = here * beside + (alone - beside) / 2;
+        return size * p.seg_len * (token > alone ? token : alone);
+    };
+    SsmPlan best = ssm_plan_of(most, T, T, C, G);
+    double least = cost(best, 32, 24);
+    const SsmPlan four = ssm_plan_of(4, T, T, C, G);
+    const double c4 = cost(four, 92, 62);
+    if (c4 < least) {
+        best = four;
+        least = c4;
+    }
+    for (int len = 64; !one_pass && len * 2 <= T; len *= 2) {
+        const SsmPlan p = ssm_plan_of(4, len, T, C, G);
+        const double c = cost(p, 92 + 75, 62 + 47) + 8000 + 150.0 * p.segs;
+        if (c < least && (__int128)p.c_blocks * p.segs * B <= kMaxGroups) {
+            best = p;
+            least = c;
+        }
+    }
+    return best;
 }
 static size_t ssm_workspace(const SsmPlan &p, int B, int C, int N) {
     if (p.segs == 1) return 0;
@@ -287,7 +459,11 @@ extern "C" rgdr_status ssm_prefill_workspace_size(int32_t B, int32_t T, int32_t 
     if (!bytes) return RGDR_ERR_NULL;
     const rgdr_status rc = ssm_check_sizes(65536, B, T, C, N, G);
     if (rc != RGDR_OK) return rc;
-    *bytes = B == 0 ? 0 : ssm_workspace(ssm_plan(B, T, C, N, G, false), B, C, N);
+    *bytes = 0;
+    if (B == 0) return RGDR_OK;
+    const int cus = la_compute_units();
+    if (cus == 0) return RGDR_ERR_HIP;
+    *bytes = ssm_workspace(ssm_plan(B, T, C, N, G, false, cus), B, C, N);
     return RGDR_OK;
 }
 
@@ -309,8 +485,11 @@ extern "C" rgdr_status ssm_prefill(const void *x, const la_strides *x_strides, c
                   B, T, C, N, G, N_slots, out, out_strides, state_out);
     if (rc != RGDR_OK || B == 0) return rc;
     if (workspace && !aligned(workspace, 256)) return RGDR_ERR_ALIGN;
-    SsmPlan p = ssm_plan(B, T, C, N, G, false);
-    if (!workspace || workspace_bytes < ssm_workspace(p, B, C, N)) p = ssm_plan(B, T, C, N, G, true);
+    if ((__int128)ssm_plan_of(4, T, T, C, G).c_blocks * B > kMaxGroups) return RGDR_ERR_SHAPE;
+    const int cus = la_compute_units();
+    if (cus == 0) return RGDR_ERR_HIP;
+    SsmPlan p = ssm_plan(B, T, C, N, G, false, cus);
+    if (!workspace || workspace_bytes < ssm_workspace(p, B, C, N)) p = ssm_plan(B, T, C, N, G, true, cus);
     if (p.segs > 1) {
         p.ends = static_cast<float *>(workspace);
         p.sums = p.ends + (size_t)B * p.segs * C * N;

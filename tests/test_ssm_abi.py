@@ -103,6 +103,7 @@ BAD_SCAN = [
     (dict(G=3), SHAPE), (dict(slots=0), SHAPE), (dict(idx=None, slots=1), SHAPE),
     (dict(xs=(-256, 0, 64)), SHAPE), (dict(dts=(1 << 61, 0, 64)), SHAPE), (dict(Bs=(-8, 16, 32)), SHAPE),
     (dict(Cs=(1 << 61, 16, 32)), SHAPE), (dict(os=(256, 0, 32)), SHAPE), (dict(os=(0, 0, 64)), SHAPE),
+    (dict(xs=(1 << 30, 0, (1 << 24) + 8)), SHAPE), (dict(Bs=(1 << 30, 16, (1 << 24) + 8)), SHAPE),
     (dict(B=1 << 24, C=1024, G=1), SHAPE),
     (dict(C=60), UNSUP), (dict(G=16), UNSUP), (dict(N=12), UNSUP), (dict(N=64), UNSUP), (dict(fl=2), UNSUP),
     (dict(ty=MXI8), DTYPE), (dict(ty=7), DTYPE), (dict(st=F16), DTYPE), (dict(st=MXI8), DTYPE),
