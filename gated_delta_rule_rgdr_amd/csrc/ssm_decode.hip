@@ -110,20 +110,138 @@ __global__ __launch_bounds__(256) void ssm_decode_kernel(const SsmArgs a, int c_
     }
 }
 
-template <typename E, int N, bool F32, int TMAX, int U>
-static rgdr_status launch_ssm_decode(const SsmArgs &a, hipStream_t stream) {
-    constexpr int CH = 256 / (N * (F32 ? 4 : 2) / 16);
-    const long long c_blocks = ((long long)a.C + CH - 1) / CH, b_blocks = ((long long)a.B + U - 1) / U;
-    if ((__int128)c_blocks * b_blocks > kMaxGroups) return RGDR_ERR_SHAPE;
-    hipLaunchKernelGGL((ssm_decode_kernel<E, N, F32, TMAX, U>), dim3((unsigned)(c_blocks * b_blocks)), dim3(256), 0,
-                       stream, a, (int)c_blocks);
-    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
+// Several tokens and groups of at least CH channels: a workgroup has up to CH channels of one entry and
+// group. Its threads load the tokens' x, dt and z in pieces of 16 bytes of one token, compute each d and d x once,
+// and pass them on in LDS, with B and C; the sums over the states come back the same way. (Without it
+// each lane loads two bytes of them for each token, five loads in all, and computes the same d in LPC lanes.)
+template <typename E, int N, bool F32>
+__global__ __launch_bounds__(256) void ssm_decode_tokens_kernel(const SsmArgs a, int c_blocks) {
+    using S = typename StateType<F32>::E;
+    constexpr int P = 16 / sizeof(S), LPC = N / P, CH = 256 / LPC, PIECES = CH / 8;
+    __shared__ __align__(16) float sd[kMaxT][CH], su[kMaxT][CH], sB[kMaxT][N], sC[kMaxT][N];
+    const int b = blockIdx.x / c_blocks, cb = blockIdx.x % c_blocks;
+    const int Cg = a.C / a.G, per = (Cg + CH - 1) / CH, g = cb / per;
+    const int c0 = g * Cg + cb % per * CH, channels = min(CH, Cg - cb % per * CH);
+    const LaEntry e = ssm_entry(a, b);
+
+    const int c = threadIdx.x / LPC, n0 = threadIdx.x % LPC * P;
+    const bool mine = e.state && c < channels;
+    const size_t at = ((size_t)(e.state ? e.slot : 0) * a.C + c0 + c) * N + n0;
+    Row<S, P> h0;
+    Row<float, P> Ar;
+    h0.zero();
+    Ar.zero();
+    if (mine) {
+        h0.load(static_cast<const S *>(a.pool) + at);
+        Ar.load(a.A + (size_t)(c0 + c) * N + n0);
+    }
+    // pieces of tokens: PIECES threads for each, 256 / PIECES tokens at once
+    constexpr int AT_ONCE = 256 / PIECES, SETS = (kMaxT + AT_ONCE - 1) / AT_ONCE;
+    const int pc = threadIdx.x % PIECES * 8, pt = threadIdx.x / PIECES;
+    const bool p_ok = pc < channels;
+    Row<E, 8> x[SETS], dt[SETS], z[SETS];
+    Row<float, 8> bias, D;
+    bias.zero();
+    D.zero();
+    if (p_ok && a.dt_bias) bias.load(a.dt_bias + c0 + pc);
+    if (p_ok && a.D) D.load(a.D + c0 + pc);
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+        const int t = pt + s * AT_ONCE;
+        x[s].zero();
+        dt[s].zero();
+        z[s].zero();
+        if (t < e.L && p_ok) {
+            x[s].load(static_cast<const E *>(a.x) + b * a.sx.b + t * a.sx.t + c0 + pc);
+            dt[s].load(static_cast<const E *>(a.dt) + b * a.sdt.b + t * a.sdt.t + c0 + pc);
+            if (a.z) z[s].load(static_cast<const E *>(a.z) + b * a.sz.b + t * a.sz.t + c0 + pc);
+        }
+    }
+    constexpr int BC = kMaxT * 2 * N / 8;  // pieces of 8 values of B and C
+    static_assert(BC <= 256, "one for each thread");
+    if (threadIdx.x < BC) {
+        const int t = threadIdx.x / (2 * N / 8), i = threadIdx.x % (2 * N / 8) * 8;
+        if (t < e.L) {
+            Row<E, 8> r;
+            if (i < N)
+                r.load(static_cast<const E *>(a.Bm) + b * a.sB.b + t * a.sB.t + g * a.sB.h + i);
+            else
+                r.load(static_cast<const E *>(a.Cm) + b * a.sC.b + t * a.sC.t + g * a.sC.h + i - N);
+            float *to = i < N ? &sB[t][i] : &sC[t][i - N];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[k] = r.get(k);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+        const int t = pt + s * AT_ONCE;
+        if (t >= e.L) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float d = ssm_step(dt[s].get(k), bias.get(k), a.softplus);
+            sd[t][pc + k] = d;
+            su[t][pc + k] = d * x[s].get(k);
+        }
+    }
+    __syncthreads();
+    float h[P], A[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        h[i] = h0.get(i);
+        A[i] = ssm_log2_decay(Ar.get(i));
+    }
+    S *to = static_cast<S *>(a.pool_out) + at;
+    if (mine && e.n == 0 && !a.in_place) row_put(to, h);
+#pragma unroll
+    for (int t = 0; t < kMaxT; ++t) {
+        if (t >= e.L) break;
+        const float d = sd[t][c], u = su[t][c];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A[i]), h[i], u * sB[t][n0 + i]);
+            y = __builtin_fmaf(sC[t][n0 + i], h[i], y);
+        }
+        y = lanes_sum<LPC>(y);
+        if (n0 == 0) su[t][c] = y;
+        if (t + 1 == e.n && mine) row_put(to, h);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+        const int t = pt + s * AT_ONCE;
+        if (t >= a.T || !p_ok) continue;
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = t < e.L ? ssm_out(su[t][pc + k], D.get(k), x[s].get(k), a.z != nullptr, z[s].get(k)) : 0.f;
+        row_put(static_cast<E *>(a.out) + b * a.so.b + t * a.so.t + c0 + pc, y);
+    }
 }
 
+// One token: two entries for each workgroup, which read the channels' A, D and biases once (B=256, C=4096,
+// N=16, fp32 states: 25.7 us, 5.6 TB/s, against 28.7 with one and 25.7 with four; B=64 9.0, 10.3 and 9.5).
+// Several tokens by way of LDS where that saves more than its barriers cost: from 5 tokens, or 3 in large
+// calls. us, by way of LDS against each lane's own loads, C=4096, N=16, fp32 states: 8 tokens B=1 5.4/5.5, B=8
+// 5.8/7.0, B=32 10.5/16.1; 4 tokens B=1 4.8/4.1, B=16 6.4/6.3; 3 tokens B=16 6.1/5.5, B=128 23.2/27.6; 2
+// tokens B=32 8.1/7.4, B=256 40.6/41.7. B=32, up to 8 tokens, bf16 states, G=8: 8.8/10.4.
 template <typename E, int N, bool F32>
 static rgdr_status launch_ssm_tokens(const SsmArgs &a, hipStream_t stream) {
-    if (a.T > 1) return launch_ssm_decode<E, N, F32, kMaxT, 1>(a, stream);
-    return launch_ssm_decode<E, N, F32, 1, 1>(a, stream);
+    constexpr int CH = 256 / (N * (F32 ? 4 : 2) / 16);
+    const int Cg = a.C / a.G;
+    const bool large = (long long)a.B * a.G * (Cg / CH) >= 2048;
+    const bool tokens = Cg >= CH && (a.T >= 5 || (a.T >= 3 && large));
+    const long long c_blocks = tokens ? (long long)a.G * ((Cg + CH - 1) / CH) : ((long long)a.C + CH - 1) / CH;
+    const long long b_blocks = a.T > 1 ? a.B : ((long long)a.B + 1) / 2;
+    if ((__int128)c_blocks * b_blocks > kMaxGroups) return RGDR_ERR_SHAPE;
+    const dim3 grid((unsigned)(c_blocks * b_blocks)), block(256);
+    if (tokens)
+        hipLaunchKernelGGL((ssm_decode_tokens_kernel<E, N, F32>), grid, block, 0, stream, a, (int)c_blocks);
+    else if (a.T > 1)
+        hipLaunchKernelGGL((ssm_decode_kernel<E, N, F32, kMaxT, 1>), grid, block, 0, stream, a, (int)c_blocks);
+    else
+        hipLaunchKernelGGL((ssm_decode_kernel<E, N, F32, 1, 2>), grid, block, 0, stream, a, (int)c_blocks);
+    return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 template <typename E>
