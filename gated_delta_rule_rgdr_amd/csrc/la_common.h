@@ -90,6 +90,67 @@ struct RowVec {
     }
 };
 
+// K values of E in a row, as they are stored (in whole 32-bit words, aligned as a load of them wants it:
+// 4, 8 or 16 bytes).
+template <typename E, int K>
+struct Row {
+    static constexpr int WORDS = K * (int)sizeof(E) / 4, PIECE = WORDS < 4 ? WORDS : 4;
+    static_assert(K * sizeof(E) % 4 == 0 && WORDS % PIECE == 0 && PIECE != 3, "whole loads");
+    typedef unsigned int Piece __attribute__((ext_vector_type(PIECE)));
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const E *p) {
+#pragma unroll
+        for (int i = 0; i < WORDS / PIECE; ++i) {
+            const Piece v = *(reinterpret_cast<const Piece *>(p) + i);
+#pragma unroll
+            for (int j = 0; j < PIECE; ++j) w[PIECE * i + j] = v[j];
+        }
+    }
+    template <bool ONCE = false>  // written once and not read soon
+    __device__ __forceinline__ void store(E *p) const {
+#pragma unroll
+        for (int i = 0; i < WORDS / PIECE; ++i) {
+            Piece v;
+#pragma unroll
+            for (int j = 0; j < PIECE; ++j) v[j] = w[PIECE * i + j];
+            if (ONCE)
+                __builtin_nontemporal_store(v, reinterpret_cast<Piece *>(p) + i);
+            else
+                *(reinterpret_cast<Piece *>(p) + i) = v;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(E) == 4)
+            return __uint_as_float(w[i]);
+        else if constexpr (__is_same(E, _Float16))
+            return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16))));
+        else
+            return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+    __device__ __forceinline__ void set(const float (&y)[K]) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(E) == 4)
+                w[i] = __float_as_uint(y[i]);
+            else if constexpr (__is_same(E, _Float16))
+                w[i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(y[2 * i])) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(y[2 * i + 1])) << 16;
+            else
+                w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+        }
+    }
+};
+template <typename E, int K>
+__device__ __forceinline__ void row_put(E *p, const float (&y)[K]) {
+    Row<E, K> r;
+    r.set(y);
+    r.store(p);
+}
+
 // One such value as fp32, and back.
 __device__ __forceinline__ float row_value(float x) { return x; }
 __device__ __forceinline__ float row_value(_Float16 x) { return static_cast<float>(x); }

@@ -16,14 +16,18 @@ struct ConvArgs {
     int B, T, C, N_slots, silu;
 };
 
-// A thread has the V channels of 16 bytes and TT tokens in a row, whose inputs (with the W - 1 before
-// them) it holds in registers: W - 1 + TT loads in flight at once. TT >= W - 1 or T = 1, so the
-// slot's inputs are read by the thread of the first tokens alone, which also writes the slot: the
-// pool can be updated in place.
+constexpr int kConvChannels = 4;  // of a thread
+
+// A thread has four channels and TT tokens in a row, whose inputs (with the W - 1 before them) it holds in
+// registers: W - 1 + TT loads in flight at once. TT >= W - 1 or T = 1, so the slot's inputs are read by the
+// thread of the first tokens alone, which also writes the slot: the pool can be updated in place. Bound:
+// the bytes. B=16, T=1024 ragged, C=8192, W=4, bf16: 85.8 us (5.1 TB/s); with 8 tokens for each thread 93.7,
+// which reads more rows twice, and with eight channels for each (more registers, fewer waves) 95.3; with
+// loads that pass the caches by 101. One sequence of 8192 tokens 52.0.
 template <typename E, int W, int TT>
 __global__ __launch_bounds__(256) void la_conv_kernel(const ConvArgs a, int cl_log, int c_blocks, int t_blocks) {
-    using V = RowVec<E>;
-    constexpr int N = V::N, H = W - 1;
+    constexpr int N = kConvChannels, H = W - 1;
+    using V = Row<E, N>;
     const int cb = blockIdx.x % c_blocks, tb = blockIdx.x / c_blocks % t_blocks;
     const int b = blockIdx.x / c_blocks / t_blocks;
     const int c = ((cb << cl_log) + (threadIdx.x & ((1 << cl_log) - 1))) * N;
@@ -38,15 +42,15 @@ __global__ __launch_bounds__(256) void la_conv_kernel(const ConvArgs a, int cl_l
     const size_t at = (size_t)(state ? slot : 0) * H * a.C + c;
     const E *pool = static_cast<const E *>(a.pool) + at;
 
-    u32x4 line[H + TT];
+    V line[H + TT];
 #pragma unroll
     for (int i = 0; i < H + TT; ++i) {
         const long long t = t0 + i - H;
-        line[i] = u32x4{0, 0, 0, 0};
+        line[i].zero();
         if (t >= 0 && t < L)
-            line[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + t * a.sx.t));
+            line[i].load(x + t * a.sx.t);
         else if (i < H && t0 == 0 && state)
-            line[i] = *reinterpret_cast<const u32x4 *>(pool + (size_t)i * a.C);
+            line[i].load(pool + (size_t)i * a.C);
     }
     float w[N * W], bias[N];
 #pragma unroll
@@ -56,18 +60,18 @@ __global__ __launch_bounds__(256) void la_conv_kernel(const ConvArgs a, int cl_l
     for (int i = 0; i < N / 4; ++i)
         *reinterpret_cast<f32x4 *>(bias + 4 * i) =
             a.bias ? *reinterpret_cast<const f32x4 *>(a.bias + c + 4 * i) : f32x4{0, 0, 0, 0};
-
     // (a slot whose entry accepts no token keeps its bytes when the pool is updated in place)
     if (t0 == 0 && state && (n > 0 || a.pool_out != a.pool)) {
         E *to = static_cast<E *>(a.pool_out) + at;
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int i = n + j;  // of the line
-            u32x4 v = line[0];
+            V v = line[0];
 #pragma unroll
-            for (int k = 1; k < H; ++k) v = i == k ? line[k] : v;
-            if (i >= H) v = *reinterpret_cast<const u32x4 *>(x + (i - H) * a.sx.t);
-            *reinterpret_cast<u32x4 *>(to + (size_t)j * a.C) = v;
+            for (int k = 1; k < H; ++k)
+                if (i == k) v = line[k];
+            if (i >= H) v.load(x + (i - H) * a.sx.t);
+            v.store(to + (size_t)j * a.C);
         }
     }
 #pragma unroll
@@ -79,23 +83,23 @@ __global__ __launch_bounds__(256) void la_conv_kernel(const ConvArgs a, int cl_l
         for (int k = 0; k < N; ++k) y[k] = bias[k];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float v[N];
-            V::get(v, line[u + j]);
 #pragma unroll
-            for (int k = 0; k < N; ++k) y[k] = __builtin_fmaf(w[k * W + j], v[k], y[k]);
+            for (int k = 0; k < N; ++k) y[k] = __builtin_fmaf(w[k * W + j], line[u + j].get(k), y[k]);
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             if (a.silu) y[k] *= sigmoid_fast(y[k]);
             y[k] = t < L ? y[k] : 0.f;
         }
-        __builtin_nontemporal_store(V::put(y), reinterpret_cast<u32x4 *>(out + t * a.so.t));
+        V o;
+        o.set(y);
+        o.template store<true>(out + t * a.so.t);
     }
 }
 
 template <typename E, int W, int TT>
 static rgdr_status launch_conv_rows(const ConvArgs &a, hipStream_t stream) {
-    const int pieces = a.C / RowVec<E>::N;
+    const int pieces = a.C / kConvChannels;
     int cl_log = 0;
     while (cl_log < 8 && (1 << cl_log) < pieces) ++cl_log;
     const long long c_blocks = ((long long)pieces + (1 << cl_log) - 1) >> cl_log;
@@ -109,7 +113,7 @@ static rgdr_status launch_conv_rows(const ConvArgs &a, hipStream_t stream) {
 template <typename E, int W>
 static rgdr_status launch_conv_taps(const ConvArgs &a, hipStream_t stream) {
     if (a.T == 1) return launch_conv_rows<E, W, 1>(a, stream);
-    return launch_conv_rows<E, W, 8>(a, stream);
+    return launch_conv_rows<E, W, 16>(a, stream);
 }
 
 template <typename E>

@@ -57,54 +57,6 @@ __device__ __forceinline__ float ssm_out(float sum, float D, float x, bool gated
     return y * (z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z)));
 }
 
-// K values of E in a row from 2 K- or 4 K-byte aligned memory, as they are stored and as fp32.
-template <typename E, int K>
-struct Row {
-    static constexpr int BYTES = K * (int)sizeof(E), WORDS = BYTES / 4;
-    static_assert(BYTES % 4 == 0 && (WORDS <= 2 || WORDS % 4 == 0), "whole loads");
-    uint32_t w[WORDS];
-    __device__ __forceinline__ void load(const E *p) {
-        typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-        if constexpr (WORDS == 1) {
-            w[0] = *reinterpret_cast<const uint32_t *>(p);
-        } else if constexpr (WORDS == 2) {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-            w[0] = v[0];
-            w[1] = v[1];
-        } else {
-#pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-                const u32x4 v = *(reinterpret_cast<const u32x4 *>(p) + i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-            }
-        }
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = 0;
-    }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (sizeof(E) == 4)
-            return __uint_as_float(w[i]);
-        else if constexpr (__is_same(E, _Float16))
-            return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16))));
-        else
-            return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-    }
-};
-template <typename E, int K>
-__device__ __forceinline__ void row_put(E *p, const float (&y)[K]) {
-    constexpr int V = RowVec<E>::N;
-#pragma unroll
-    for (int i = 0; i < K / V; ++i) {
-        float part[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) part[j] = y[i * V + j];
-        *(reinterpret_cast<u32x4 *>(p) + i) = RowVec<E>::put(part);
-    }
-}
-
 // The argument checks of ssm_decode and ssm_prefill (T up to max_t), and the kernels' argument block.
 // B = 0 is RGDR_OK with nothing to launch.
 rgdr_status ssm_check_sizes(int max_t, int32_t B, int32_t T, int32_t C, int32_t N, int32_t G);
