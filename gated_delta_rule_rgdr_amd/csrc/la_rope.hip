@@ -27,129 +27,174 @@ __device__ __forceinline__ float2 rope_turn(double pos, float freq, float factor
 
 enum RopeLayout { kRopeHalves, kRopePairs, kRopeAny };
 
+// The place of a thread's row and unit.
+template <typename E>
+struct RopeRow {
+    const E *x;
+    E *out;
+    int u;            // its token, of the workgroup's
+    bool here, live;  // there is such a row; its token is valid
+};
+template <typename E>
+__device__ __forceinline__ RopeRow<E> rope_row(const RopeArgs &a, int b, int t0, int h0, int r, int rows, int tb_log,
+                                               int L) {
+    RopeRow<E> w;
+    w.u = r & ((1 << tb_log) - 1);
+    const int t = t0 + w.u, h = h0 + (r >> tb_log);
+    w.here = r < rows && t < a.T;
+    w.live = w.here && t < L;
+    const bool key = h >= a.Hq;
+    const LaStrides &si = key ? a.sk : a.sq, &so = key ? a.sko : a.sqo;
+    const int hh = key ? h - a.Hq : h;
+    w.x = static_cast<const E *>(key ? a.k : a.q) + b * si.b + hh * si.h + t * si.t;
+    w.out = static_cast<E *>(key ? a.k_out : a.q_out) + b * so.b + hh * so.h + t * so.t;
+    return w;
+}
+
 // A workgroup has 2^tb_log tokens of one entry, and hb of the H heads. It computes the tokens'
-// cosines and sines once, into LDS, for all heads. A row is split into units over 2^ul_log threads:
-//   kRopeHalves: 16 bytes of the first half with their partners in the second (R / 2 whole pieces
-//                of 16 bytes), and 16 bytes of the columns past R;
+// cosines and sines once, into LDS, for all heads, while its first rows are on their way. A row is split
+// into units, one for each of 2^ul_log threads:
+//   kRopeHalves: N columns of the first half with their partners in the second, and N of the columns past
+//                R; N is the most that makes pieces of up to 16 bytes and divides R / 2;
 //   kRopePairs:  interleaved pairs, 16 bytes;
-//   kRopeAny:    halves of any length: one pair, or one column past R.
+//   kRopeAny:    halves of an odd number of 16-bit values: one pair, or one column past R (several units for
+//                each thread where there are more than 256).
 // A thread writes the columns that it reads and no other thread reads, so it can be done in place.
-template <typename E, int LAYOUT>
+// Bound: the bytes. B=16, T=1024 ragged, 16 + 16 heads of 128, bf16: 41.1 us (5.3
+// TB/s; with stores that stay in the caches 45.5); T=8192, 32 + 8 heads, 64 of 128 interleaved, fp16: 32.3.
+template <typename E, int LAYOUT, int N>
 __global__ __launch_bounds__(256) void la_rope_kernel(const RopeArgs a, int tb_log, int hb, int ul_log, int units,
                                                       int h_blocks, int t_blocks) {
-    using V = RowVec<E>;
-    constexpr int N = V::N;
+    constexpr int AHEAD = 4;          // rows of a thread in flight
     extern __shared__ float2 turn[];  // [2^tb_log][R / 2]
     const int hblk = blockIdx.x % h_blocks, tblk = blockIdx.x / h_blocks % t_blocks;
     const int b = blockIdx.x / h_blocks / t_blocks;
     const int half = a.R / 2, tb = 1 << tb_log, t0 = tblk << tb_log;
     const int L = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-    for (int i = threadIdx.x; i < tb * half; i += 256) {
-        const int u = i / half, t = t0 + u;
-        if (t >= L) break;
-        const double pos = !a.pos ? (double)t : a.each ? (double)a.pos[(size_t)b * a.T + t] : (double)a.pos[b] + t;
-        turn[i] = rope_turn(pos, a.freq[i - u * half], a.factor);
-    }
-    __syncthreads();
-    const int unit0 = threadIdx.x & ((1 << ul_log) - 1), rows = 256 >> ul_log;
-    const int h0 = hblk * hb, nh = min(hb, a.H - h0);
-    for (int r = threadIdx.x >> ul_log; r < nh << tb_log; r += rows) {
-        const int u = r & (tb - 1), t = t0 + u, h = h0 + (r >> tb_log);
-        if (t >= a.T) continue;
-        const bool key = h >= a.Hq;
-        const LaStrides &si = key ? a.sk : a.sq, &so = key ? a.sko : a.sqo;
-        const int hh = key ? h - a.Hq : h;
-        const E *x = static_cast<const E *>(key ? a.k : a.q) + b * si.b + hh * si.h + t * si.t;
-        E *out = static_cast<E *>(key ? a.k_out : a.q_out) + b * so.b + hh * so.h + t * so.t;
-        const float2 *cs = turn + u * half;
-        const bool live = t < L;
-        for (int unit = unit0; unit < units; unit += 1 << ul_log) {
-            if constexpr (LAYOUT == kRopeAny) {
+    const int unit0 = threadIdx.x & ((1 << ul_log) - 1), at_once = 256 >> ul_log;
+    const int h0 = hblk * hb, rows = min(hb, a.H - h0) << tb_log;
+    const auto turns = [&] {
+        for (int i = threadIdx.x; i < tb * half; i += 256) {
+            const int u = i / half, t = t0 + u;
+            if (t >= L) break;
+            const double pos = !a.pos ? (double)t : a.each ? (double)a.pos[(size_t)b * a.T + t] : (double)a.pos[b] + t;
+            turn[i] = rope_turn(pos, a.freq[i - u * half], a.factor);
+        }
+        __syncthreads();
+    };
+    if constexpr (LAYOUT == kRopeAny) {
+        turns();
+        for (int r = threadIdx.x >> ul_log; r < rows; r += at_once) {
+            const RopeRow<E> w = rope_row<E>(a, b, t0, h0, r, rows, tb_log, L);
+            if (!w.here) continue;
+            const float2 *cs = turn + w.u * half;
+            for (int unit = unit0; unit < units; unit += 1 << ul_log) {
                 if (unit < half) {
                     float p = 0.f, q = 0.f;
-                    if (live) {
-                        const float y = row_value(x[unit]), z = row_value(x[unit + half]);
+                    if (w.live) {
+                        const float y = row_value(w.x[unit]), z = row_value(w.x[unit + half]);
                         p = y * cs[unit].x - z * cs[unit].y;
                         q = y * cs[unit].y + z * cs[unit].x;
                     }
-                    out[unit] = row_store<E>(p);
-                    out[unit + half] = row_store<E>(q);
+                    w.out[unit] = row_store<E>(p);
+                    w.out[unit + half] = row_store<E>(q);
                 } else {
-                    out[unit + half] = live ? x[unit + half] : E(0);
+                    w.out[unit + half] = w.live ? w.x[unit + half] : E(0);
                 }
-            } else if constexpr (LAYOUT == kRopePairs) {
-                u32x4 w = {0, 0, 0, 0};
-                if (live) {
-                    w = *reinterpret_cast<const u32x4 *>(x + unit * N);
-                    float y[N];
-                    V::get(y, w);
+            }
+        }
+    } else {
+        const bool pair = LAYOUT == kRopePairs || unit0 * N < half;
+        const int c0 = pair ? unit0 * N : unit0 * N + half;  // the unit's first column
+        const bool in_row = unit0 < units;
+        for (int r0 = 0; r0 < rows; r0 += AHEAD * at_once) {
+            RopeRow<E> w[AHEAD];
+            Row<E, N> y[AHEAD], z[AHEAD];
 #pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        const int pair = unit * (N / 2) + i;
-                        if (pair < half) {
-                            const float2 c = cs[pair];
-                            const float p = y[2 * i], q = y[2 * i + 1];
-                            y[2 * i] = p * c.x - q * c.y;
-                            y[2 * i + 1] = p * c.y + q * c.x;
-                        }
-                    }
-                    w = V::put(y);
+            for (int k = 0; k < AHEAD; ++k) {
+                w[k] = rope_row<E>(a, b, t0, h0, r0 + k * at_once + (threadIdx.x >> ul_log), rows, tb_log, L);
+                y[k].zero();
+                z[k].zero();
+                if (w[k].live && in_row) {
+                    y[k].load(w[k].x + c0);
+                    if (LAYOUT == kRopeHalves && pair) z[k].load(w[k].x + c0 + half);
                 }
-                *reinterpret_cast<u32x4 *>(out + unit * N) = w;
-            } else {
-                const bool pair = unit * N < half;
-                const int c0 = pair ? unit * N : unit * N + half;
-                u32x4 w = {0, 0, 0, 0}, w2 = {0, 0, 0, 0};
-                if (live) {
-                    w = *reinterpret_cast<const u32x4 *>(x + c0);
-                    if (pair) {
-                        w2 = *reinterpret_cast<const u32x4 *>(x + c0 + half);
-                        float y[N], z[N];
-                        V::get(y, w);
-                        V::get(z, w2);
+            }
+            if (r0 == 0) turns();
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (!w[k].here || !in_row) continue;
+                if (pair && w[k].live) {
+                    const float2 *cs = turn + w[k].u * half;
+                    float p[N], q[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        p[i] = y[k].get(i);
+                        q[i] = z[k].get(i);
+                    }
+                    if constexpr (LAYOUT == kRopePairs) {
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) {
+                            const int n = c0 / 2 + i;
+                            if (n >= half) continue;
+                            const float2 c = cs[n];
+                            const float u = p[2 * i], v = p[2 * i + 1];
+                            p[2 * i] = u * c.x - v * c.y;
+                            p[2 * i + 1] = u * c.y + v * c.x;
+                        }
+                    } else {
 #pragma unroll
                         for (int i = 0; i < N; ++i) {
                             const float2 c = cs[c0 + i];
-                            const float p = y[i], q = z[i];
-                            y[i] = p * c.x - q * c.y;
-                            z[i] = p * c.y + q * c.x;
+                            const float u = p[i], v = q[i];
+                            p[i] = u * c.x - v * c.y;
+                            q[i] = u * c.y + v * c.x;
                         }
-                        w = V::put(y);
-                        w2 = V::put(z);
+                        z[k].set(q);
                     }
+                    y[k].set(p);
                 }
-                *reinterpret_cast<u32x4 *>(out + c0) = w;
-                if (pair) *reinterpret_cast<u32x4 *>(out + c0 + half) = w2;
+                y[k].template store<true>(w[k].out + c0);
+                if (LAYOUT == kRopeHalves && pair) z[k].template store<true>(w[k].out + c0 + half);
             }
         }
     }
 }
 
-template <typename E, int LAYOUT>
+static int rope_units(int layout, int N, int D, int R) {
+    return layout == kRopeAny ? D - R / 2 : layout == kRopePairs ? D / N : (D - R / 2) / N;
+}
+
+template <typename E, int LAYOUT, int N>
 static rgdr_status launch_rope(const RopeArgs &a, hipStream_t stream) {
-    const int units = LAYOUT == kRopeAny ? a.D - a.R / 2
-                      : LAYOUT == kRopePairs ? a.D / RowVec<E>::N
-                                             : (a.D - a.R / 2) / RowVec<E>::N;
+    const int units = rope_units(LAYOUT, N, a.D, a.R);
     int ul_log = 0;
     while (ul_log < 8 && (1 << ul_log) < units) ++ul_log;
     int tb_log = 0;
     while (tb_log < 2 && (1 << tb_log) < a.T) ++tb_log;
-    const long long t_blocks = (a.T + (1 << tb_log) - 1) >> tb_log;
-    const int hb = a.H < 64 ? a.H : 64;
-    const long long h_blocks = (a.H + hb - 1) / hb;
+    const long long t_blocks = ((long long)a.T + (1 << tb_log) - 1) >> tb_log;
+    const long long h_blocks = ((long long)a.H + 63) / 64;
+    const int hb = (int)((a.H + h_blocks - 1) / h_blocks);
     if ((__int128)h_blocks * t_blocks * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
     const dim3 grid((unsigned)(h_blocks * t_blocks * a.B)), block(256);
     const size_t lds = sizeof(float2) * (a.R / 2) << tb_log;
-    hipLaunchKernelGGL((la_rope_kernel<E, LAYOUT>), grid, block, lds, stream, a, tb_log, hb, ul_log, units,
+    hipLaunchKernelGGL((la_rope_kernel<E, LAYOUT, N>), grid, block, lds, stream, a, tb_log, hb, ul_log, units,
                        (int)h_blocks, (int)t_blocks);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
+// Halves in pieces of up to 16 bytes. (R = 24 of 96 columns, bf16, 2000 tokens of 16 heads: 7.9 us in pieces
+// of 8 bytes, 30 column by column.)
 template <typename E>
 static rgdr_status launch_rope_layout(const RopeArgs &a, bool interleaved, hipStream_t stream) {
-    if (interleaved) return launch_rope<E, kRopePairs>(a, stream);
-    if (a.R / 2 % RowVec<E>::N == 0) return launch_rope<E, kRopeHalves>(a, stream);
-    return launch_rope<E, kRopeAny>(a, stream);
+    constexpr int MOST = 16 / sizeof(E);
+    const int half = a.R / 2;
+    const auto fits = [&](int N) { return half % N == 0 && rope_units(kRopeHalves, N, a.D, a.R) <= 256; };
+    if (interleaved) return launch_rope<E, kRopePairs, MOST>(a, stream);
+    if (fits(MOST)) return launch_rope<E, kRopeHalves, MOST>(a, stream);
+    if (fits(MOST / 2)) return launch_rope<E, kRopeHalves, MOST / 2>(a, stream);
+    if (fits(MOST / 4)) return launch_rope<E, kRopeHalves, MOST / 4>(a, stream);
+    return launch_rope<E, kRopeAny, 1>(a, stream);
 }
 
 static bool rope_in_place(const LaStrides &s, const LaStrides &o, int B, int H, int T) {
