@@ -61,6 +61,22 @@ __device__ __forceinline__ float ssm_meet(float (&y)[WAYS]) {
     return y[0];
 }
 
+// The wave's priority by the quarter of the tokens that it still has before it. Of waves alike the oldest
+// goes first, so that the last workgroup of a compute unit would run the longer alone, at half of the vector units'
+// rate: B=16, T=1024, C=4096 257 us without and 240 with, ragged 191 and 183.
+__device__ __forceinline__ void ssm_priority(int now, int &quarter) {
+    if (now == quarter) return;
+    quarter = now;
+    if (now == 3)
+        __builtin_amdgcn_s_setprio(3);
+    else if (now == 2)
+        __builtin_amdgcn_s_setprio(2);
+    else if (now == 1)
+        __builtin_amdgcn_s_setprio(1);
+    else
+        __builtin_amdgcn_s_setprio(0);
+}
+
 // What WAYS tokens bring to a lane.
 template <int N, int WAYS, bool WITH_C>
 struct SsmBatch {
@@ -221,7 +237,9 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
     prepare(nt);
 
     float sum = 0.f;
+    int quarter = -1;
     for (int t0 = t_begin; t0 < t_end;) {
+        ssm_priority((int)((t_end - t0) * 4LL / (p.seg_len + 1)), quarter);
         const bool live = st < nt;
         x = nx;
         z = nz;
@@ -417,9 +435,9 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
 // four lanes, the LDS 24 with 16 (a quarter of the channels); the older waves of a compute unit go first,
 // so that the last workgroup is alone for a while. Of a segment's two passes the first takes
 // three quarters of the second; they and the scan between them are three launches.
-// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/260/224 (256);
-// C=8192 760/395/420 (256); C=512 760/260/67 (256); C=2048, T=2048 194/68/52 (128); B=2, T=300, C=4096
-// 34/26/35 (64); B=4, T=1024 105/103/120 (128); B=16 250/350/375 (256).
+// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 770/268/222 (256);
+// C=8192 760/375/452 (256); C=512 760/270/60 (256); C=2048, T=2048 194/70/48 (128); B=2, T=300, C=4096
+// 34/26/35 (64); B=4, T=1024 104/94/120 (128); B=16 240/366/375 (256).
 static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
     const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
