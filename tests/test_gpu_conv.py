@@ -238,3 +238,16 @@ def test_empty_batch(rg):
     c = Case(2, 4, 64, 4, "bf16", 18)
     out, _ = rg.la_conv(c.x[:0], c.w, c.pool)
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype,W", [("bf16", 4), ("f16", 3), ("f32", 2)])
+def test_many_rows(rg, dtype, W):
+    """Enough rows for 16 tokens to each thread; ragged, counts of all sorts, columns of a wider buffer."""
+    c = Case(16, 130, 4104, W, dtype, 19, pad=8)
+    ref = c.reference()
+    new = torch.zeros_like(c.pool)
+    out, after = c.call(rg, state_out=new)
+    check(out, ref[0], ref[1], "apart")
+    for b in range(c.B):
+        assert torch.equal(new[int(c.idx[b])].double().cpu(), ref[2][int(c.idx[b])])
+    c.check(*c.call(rg), ref, "in place")
