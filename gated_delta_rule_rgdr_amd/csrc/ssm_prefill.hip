@@ -22,6 +22,7 @@ struct SsmShape {
 
 struct SsmPlan {
     int ways, c_blocks;
+    bool roles;
     int segs, seg_len;
     float *ends;  // [B][segs][C][N]: a segment's end state from zero, then its incoming state
     float *sums;  // [B][segs][C]: its sum of d
@@ -77,40 +78,29 @@ __device__ __forceinline__ void ssm_priority(int now, int &quarter) {
         __builtin_amdgcn_s_setprio(0);
 }
 
-// What WAYS tokens bring to a lane.
-template <int N, int WAYS, bool WITH_C>
-struct SsmBatch {
-    using S = SsmShape<N, WAYS>;
-    float d[WAYS], u[WAYS], B[WAYS][S::NP], C[WAYS][S::NP];
-    __device__ __forceinline__ void read(const float *d_row, const float *u_row, const float *tB, const float *tC, int t) {
-#pragma unroll
-        for (int k = 0; k < WAYS; k += 4) {
-            *reinterpret_cast<f32x4 *>(d + k) = *reinterpret_cast<const f32x4 *>(d_row + t + k);
-            *reinterpret_cast<f32x4 *>(u + k) = *reinterpret_cast<const f32x4 *>(u_row + t + k);
-        }
-#pragma unroll
-        for (int i = 0; i < S::NP; ++i) {
-#pragma unroll
-            for (int j = 0; j < WAYS; ++j) {
-                B[j][i] = tB[S::bc_at(t + j, i)];
-                if (WITH_C) C[j][i] = tC[S::bc_at(t + j, i)];
-            }
-        }
-    }
-};
-
-// A workgroup has up to CH channels of one entry and group and works through chunks of TC tokens (of the entry, or of one
-// of its segments). What is done once for each token and channel (softplus, d x, the gate) and all memory
-// access of them goes by (token, 8 channels) for each thread, whole 16-byte pieces; the states go by
-// channel: WAYS lanes hold a channel's N states, so that a lane has N / WAYS of them in registers for all
+// A workgroup has up to CH channels of one entry and group and works through chunks of TC tokens (of the
+// entry, or of one of its segments). What is done once for each token and channel (softplus, d x, the gate) and
+// all memory access of them goes by (token, 8 channels) for each thread, whole 16-byte pieces; the states go
+// by channel: WAYS lanes hold a channel's N states, so that a lane has N / WAYS of them in registers for all
 // tokens. d, d x and the sums over the states pass between the two through LDS, as do B and C in fp32.
-template <typename E, int N, int WAYS, int PASS>
-__global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4) : 2) void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {
+//
+// A workgroup's four waves do both in turn, and waves of other workgroups fill in: with four on a compute
+// unit the vector units are busy for 90 to 97% of the time (B=16, T=1024, C=4096, N=16, bf16: 236 us; ragged
+// 164). Where a compute unit has one workgroup at most (ROLES), four waves do the one and four others the other,
+// a chunk apart, in two sets of buffers: B=1, T=8192, C=512 206 us, and 276 with both in the same waves;
+// C=4096, T=300 15.4 and 17.0; with two workgroups there it is the other way round, 443 and 381 (C=8192).
+template <typename E, int N, int WAYS, int PASS, bool ROLES>
+__global__ __launch_bounds__(ROLES ? 512 : 256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4) : 2)
+void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {
     using S = SsmShape<N, WAYS>;
     constexpr int NP = S::NP, TC = S::TC;
-    __shared__ __align__(16) float sd[S::ROWS], su[S::ROWS];
-    __shared__ __align__(16) float sB[S::BC], sC[S::BC];
+    constexpr int SETS = ROLES ? 2 : 1;
+    __shared__ __align__(16) float sd[SETS][S::ROWS], su[SETS][S::ROWS];
+    __shared__ __align__(16) float sB[SETS][S::BC], sC[SETS][S::BC];
     __shared__ __align__(16) float s_bias[S::CH], s_D[S::CH];
+    const int role = ROLES ? __builtin_amdgcn_readfirstlane(threadIdx.x / 256) : 0;
+    const int tid = ROLES ? threadIdx.x % 256 : threadIdx.x;
+    const bool by_channel = !ROLES || role == 0, by_token = !ROLES || role == 1;
     const int cb = blockIdx.x % p.c_blocks, s = blockIdx.x / p.c_blocks % p.segs;
     const int b = entry_of_rank(a.lens, a.B, a.T, blockIdx.x / p.c_blocks / p.segs);
     const LaEntry e = ssm_entry(a, b);
@@ -119,7 +109,7 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
 
     // by token and 8 channels: a uniform address, which moves on by chunks, and a thread's own 32-bit offset
     // (127 tokens at strides of at most 2^25 bytes)
-    const int st = threadIdx.x / S::TPT, sc = threadIdx.x % S::TPT * 8;
+    const int st = tid / S::TPT, sc = tid % S::TPT * 8;
     const int Cg = a.C / a.G, per = (Cg + S::CH - 1) / S::CH, g = cb / per;  // this workgroup's group,
     const int c0 = g * Cg + cb % per * S::CH, channels = min(S::CH, Cg - cb % per * S::CH);  // and channels
     const int cs = c0 + sc;
@@ -133,14 +123,14 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
     const char *pz = first(a.z, a.sz) + c0 * sizeof(E);
     const char *pB = first(a.Bm, a.sB) + g * a.sB.h * sizeof(E), *pC = first(a.Cm, a.sC) + g * a.sC.h * sizeof(E);
     E *pout = static_cast<E *>(a.out) + b * a.so.b + cs;
-    if (PASS != kSsmEnds && c_ok) {
+    if (PASS != kSsmEnds && c_ok && by_token) {
         const float none[8] = {};
         for (int t = max(e.L, t_begin); t < min(a.T, t_begin + p.seg_len) - st; t += TC)
             row_put(pout + (t + st) * a.so.t, none);
     }
 
     // by channel and a part of its states
-    const int q = threadIdx.x % 64 / S::CW, c = threadIdx.x / 64 * S::CW + threadIdx.x % S::CW, cc = c0 + c;
+    const int q = tid % 64 / S::CW, c = tid / 64 * S::CW + tid % S::CW, cc = c0 + c;
     const bool mine = c < channels;
     const size_t slot_at = ((size_t)(e.state ? e.slot : 0) * a.C + cc) * N + q * NP;
     const size_t seg_at = ((size_t)(b * p.segs + s) * a.C + cc) * N + q * NP;
@@ -159,7 +149,7 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
     float h[NP], A[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) h[i] = A[i] = 0.f;
-    if (mine && e.state) {
+    if (mine && e.state && by_channel) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             A[i] = ssm_log2_decay(a.A[(size_t)cc * N + q * NP + i]);
@@ -169,9 +159,9 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
             if (PASS == kSsmSegment && t_begin < max(e.L, 1)) h[i] = p.ends[seg_at + i];
         }
     }
-    if (PASS != kSsmEnds && s == 0 && e.state && e.n == 0 && !a.in_place) commit(h);
+    if (PASS != kSsmEnds && s == 0 && e.state && e.n == 0 && !a.in_place && by_channel) commit(h);
 
-    if (st == 0) {
+    if (st == 0 && by_token) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s_bias[sc + i] = c_ok && a.dt_bias ? a.dt_bias[cs + i] : 0.f;
@@ -179,14 +169,14 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
         }
     }
     __syncthreads();
-    Row<E, 8> x, dt, z, nx, nz;
+    Row<E, 8> nx, dt, nz;
     nx.zero();
     dt.zero();
     nz.zero();
     Row<E, S::NV> bc;
     bc.zero();
-    const bool is_C = threadIdx.x % S::TPT >= S::TPT / 2;
-    const int col = threadIdx.x % (S::TPT / 2) * S::NV;
+    const bool is_C = tid % S::TPT >= S::TPT / 2;
+    const int col = tid % (S::TPT / 2) * S::NV;
     // (a thread without a token or channels keeps what it has: it is masked, or never stored)
     const auto load = [&](int left) {
         if (st >= left) return;
@@ -202,11 +192,10 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
         else if (PASS != kSsmEnds)
             bc.load(at(pC, st * dC + col * (uint32_t)sizeof(E)));
     };
-    // What a thread stages of the chunk of nt tokens that was loaded last: computed before the chunk before
-    // it is stored, since a wait for loads behind a store would wait for the store.
-    float d[8], u[8], f[S::NV];
-    const auto prepare = [&](int nt) {
+    // The chunk of nt tokens that was loaded last into LDS.
+    const auto stage = [&](int set, int nt) {
         const bool live = st < nt;
+        float d[8], u[8], f[S::NV];
         Row<float, 8> bias;
         bias.load(s_bias + sc);
         if (a.softplus) {
@@ -229,37 +218,28 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
 #pragma unroll
             for (int i = 0; i < S::NV; ++i) f[i] = live ? f[i] : 0.f;
         }
-    };
-    // (the accepted tokens end a chunk, so that the state after them is the one at its end)
-    const auto tokens = [&](int t0) { return min(min(TC, t_end - t0), t0 < e.n ? e.n - t0 : TC); };
-    int nt = tokens(t_begin);
-    load(t_end - t_begin);
-    prepare(nt);
-
-    float sum = 0.f;
-    int quarter = -1;
-    for (int t0 = t_begin; t0 < t_end;) {
-        ssm_priority((int)((t_end - t0) * 4LL / (p.seg_len + 1)), quarter);
-        const bool live = st < nt;
-        x = nx;
-        z = nz;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            sd[S::at(sc + i, st)] = d[i];
-            su[S::at(sc + i, st)] = u[i];
+            sd[set][S::at(sc + i, st)] = d[i];
+            su[set][S::at(sc + i, st)] = u[i];
         }
-        float *to = (is_C ? sC : sB) + S::bc_at(st, col);
+        float *to = (is_C ? sC[set] : sB[set]) + S::bc_at(st, col);
 #pragma unroll
         for (int i = 0; i < S::NV; ++i) to[S::bc_at(0, i)] = f[i];
-        __syncthreads();
+    };
+    const auto advance = [&](int nt) {
         px += (uint32_t)nt * dx;
         pdt += (uint32_t)nt * ddt;
         pz += (uint32_t)nt * dz;
         pB += (uint32_t)nt * dB;
         pC += (uint32_t)nt * dC;
-        load(t_end - t0 - nt);
-        const float *d_row = sd + S::at(c, 0), *tB = sB + S::bc_at(0, q * NP), *tC = sC + S::bc_at(0, q * NP);
-        float *u_row = su + S::at(c, 0);
+    };
+    float sum = 0.f;
+    // The states over nt tokens; the sums over the states take the place of d x.
+    const auto scan = [&](int set, int nt) {
+        const float *d_row = sd[set] + S::at(c, 0);
+        const float *tB = sB[set] + S::bc_at(0, q * NP), *tC = sC[set] + S::bc_at(0, q * NP);
+        float *u_row = su[set] + S::at(c, 0);
         float part = 0.f;
         if constexpr (WAYS == 4) {
             // LDS reads go ahead: d and d x by four tokens, B and C by two
@@ -306,37 +286,103 @@ __global__ __launch_bounds__(256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4
 #pragma unroll
             for (int t = 0; t < TC; t += WAYS) {
                 if (t >= nt) break;
-                SsmBatch<N, WAYS, PASS != kSsmEnds> now;
-                now.read(d_row, u_row, tB, tC, t);
-                float y[WAYS];
+                float d[WAYS], u[WAYS], B[WAYS][NP], C[WAYS][NP], y[WAYS];
+#pragma unroll
+                for (int k = 0; k < WAYS; k += 4) {
+                    *reinterpret_cast<f32x4 *>(d + k) = *reinterpret_cast<const f32x4 *>(d_row + t + k);
+                    *reinterpret_cast<f32x4 *>(u + k) = *reinterpret_cast<const f32x4 *>(u_row + t + k);
+                }
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+#pragma unroll
+                    for (int j = 0; j < WAYS; ++j) {
+                        B[j][i] = tB[S::bc_at(t + j, i)];
+                        C[j][i] = tC[S::bc_at(t + j, i)];
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < WAYS; ++j) {
                     y[j] = 0.f;
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
-                        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(now.d[j] * A[i]), h[i], now.u[j] * now.B[j][i]);
-                        y[j] = __builtin_fmaf(now.C[j][i], h[i], y[j]);
+                        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A[i]), h[i], u[j] * B[j][i]);
+                        y[j] = __builtin_fmaf(C[j][i], h[i], y[j]);
                     }
                 }
                 u_row[t + q] = ssm_meet<WAYS>(y);
             }
         }
         sum += part;
-        const int t1 = t0 + nt, nt1 = tokens(t1);
-        if (PASS != kSsmEnds && t1 == e.n) commit(h);
-        __syncthreads();
-        if (PASS != kSsmEnds && live && c_ok) {
-            float y[8];
-            Row<float, 8> D;
-            D.load(s_D + sc);
+    };
+    // The outputs of nt tokens from t0 on.
+    const auto finish = [&](int set, int t0, int nt, const Row<E, 8> &x, const Row<E, 8> &z) {
+        if (PASS == kSsmEnds || st >= nt || !c_ok) return;
+        float y[8];
+        Row<float, 8> D;
+        D.load(s_D + sc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = ssm_out(su[S::at(sc + i, st)], D.get(i), x.get(i), a.z != nullptr, z.get(i));
-            row_put(pout + (t0 + st) * a.so.t, y);
+        for (int i = 0; i < 8; ++i)
+            y[i] = ssm_out(su[set][S::at(sc + i, st)], D.get(i), x.get(i), a.z != nullptr, z.get(i));
+        row_put(pout + (t0 + st) * a.so.t, y);
+    };
+    // (the accepted tokens end a chunk, so that the state after them is the one at its end)
+    const auto tokens = [&](int t0) { return min(min(TC, t_end - t0), t0 < e.n ? e.n - t0 : TC); };
+
+    int quarter = -1;
+    if constexpr (!ROLES) {
+        load(t_end - t_begin);
+        for (int t0 = t_begin; t0 < t_end;) {
+            const int nt = tokens(t0);
+            ssm_priority((int)((t_end - t0) * 4LL / (p.seg_len + 1)), quarter);
+            stage(0, nt);
+            const Row<E, 8> x = nx, z = nz;
+            __syncthreads();
+            advance(nt);
+            load(t_end - t0 - nt);
+            scan(0, nt);
+            if (PASS != kSsmEnds && t0 + nt == e.n) commit(h);
+            __syncthreads();
+            finish(0, t0, nt, x, z);  // each thread's own place in LDS, which it alone stages next
+            t0 += nt;
         }
-        prepare(nt1);
-        t0 = t1;
-        nt = nt1;
+    } else if (t_begin < t_end) {
+        // While one role scans a chunk, the other finishes the one before it and stages the one behind it, in
+        // the same buffers: a thread reads and writes its own place there.
+        Row<E, 8> x = nx, z = nz, x1 = nx, z1 = nz;  // of the chunk before, and of the one being scanned
+        int nt = tokens(t_begin), nt_before = 0, set = 0;
+        if (by_token) {
+            load(t_end - t_begin);
+            stage(0, nt);
+            x1 = nx;
+            z1 = nz;
+            advance(nt);
+            load(t_end - t_begin - nt);
+        }
+        __syncthreads();
+        for (int t0 = t_begin; t0 < t_end; set ^= 1) {
+            const int next = t0 + nt, nt_next = next < t_end ? tokens(next) : 0;
+            if (by_channel) {
+                ssm_priority((int)((t_end - t0) * 4LL / (p.seg_len + 1)), quarter);
+                scan(set, nt);
+                if (next == e.n) commit(h);
+            } else {
+                if (nt_before) finish(set ^ 1, t0 - nt_before, nt_before, x, z);
+                x = x1;
+                z = z1;
+                if (nt_next) {
+                    stage(set ^ 1, nt_next);
+                    x1 = nx;
+                    z1 = nz;
+                    advance(nt_next);
+                    load(t_end - next - nt_next);
+                }
+            }
+            __syncthreads();
+            t0 = next;
+            nt_before = nt;
+            nt = nt_next;
+        }
+        if (by_token) finish(set ^ 1, t_end - nt_before, nt_before, x, z);
     }
     if (PASS == kSsmEnds && mine) {
 #pragma unroll
@@ -388,17 +434,18 @@ __global__ __launch_bounds__(256) void ssm_ends_kernel(const SsmArgs a, const Ss
     ends[last * step / 4] = f32x4{h[0], h[1], h[2], h[3]};
 }
 
-template <typename E, int N, int WAYS, int PASS>
+template <typename E, int N, int WAYS, int PASS, bool ROLES = false>
 static rgdr_status launch_ssm_pass(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
     if ((__int128)p.c_blocks * p.segs * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
-    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS>), dim3((unsigned)((long long)p.c_blocks * p.segs * a.B)),
-                       dim3(256), 0, stream, a, p, f32);
+    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS, ROLES>), dim3((unsigned)((long long)p.c_blocks * p.segs * a.B)),
+                       dim3(ROLES ? 512 : 256), 0, stream, a, p, f32);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
 template <typename E, int N>
 static rgdr_status launch_ssm_prefill(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
     constexpr int MOST = N < 16 ? N : 16;
+    if (p.ways == MOST && p.roles) return launch_ssm_pass<E, N, MOST, kSsmWhole, true>(a, p, f32, stream);
     if (p.ways == MOST) return launch_ssm_pass<E, N, MOST, kSsmWhole>(a, p, f32, stream);
     if (p.segs == 1) return launch_ssm_pass<E, N, 4, kSsmWhole>(a, p, f32, stream);
     const long long threads = (long long)a.B * a.C * (N / 4), blocks = (threads + 255) / 256;
@@ -425,19 +472,20 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
     p.c_blocks = G * ((C / G + CH - 1) / CH);
     p.seg_len = seg_len;
     p.segs = (T + seg_len - 1) / seg_len;
+    p.roles = false;
     p.ends = p.sums = nullptr;
     return p;
 }
 
 // How many lanes for each channel, and how many segments: what costs least by the model below, in ns, whose
-// rates were measured with N = 16. A chunk's tokens take a workgroup alone on its compute unit 92 ns each
-// with four lanes for each channel and 32 with 16; the vector units allow 62 for each workgroup there with
-// four lanes, the LDS 24 with 16 (a quarter of the channels); the older waves of a compute unit go first,
-// so that the last workgroup is alone for a while. Of a segment's two passes the first takes
-// three quarters of the second; they and the scan between them are three launches.
-// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 770/268/222 (256);
-// C=8192 760/375/452 (256); C=512 760/270/60 (256); C=2048, T=2048 194/70/48 (128); B=2, T=300, C=4096
-// 34/26/35 (64); B=4, T=1024 104/94/120 (128); B=16 240/366/375 (256).
+// rates were measured with N = 16. A chunk's tokens take a workgroup alone on its compute unit 97 ns each
+// with four lanes for each channel and 32 with 16, or 28.5 with roles; the vector units allow 58 for each
+// workgroup there with four lanes, the LDS 22.5 with 16 (a quarter of the channels); the last workgroup is alone
+// for a while. Of a segment's two passes the first takes three quarters of the second; they and the scan
+// between them are three launches.
+// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 770/224/216 (256);
+// C=8192 760/381/416 (256); C=512 760/206/60 (256); C=2048, T=2048 194/57/46 (128); B=2, T=300, C=4096
+// 34/26/35 (64); B=4, T=1024 100/94/120 (128); B=8 135/187; B=16 236/362/375 (256).
 static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
     const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
@@ -447,16 +495,17 @@ static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cu
         return size * p.seg_len * (token > alone ? token : alone);
     };
     SsmPlan best = ssm_plan_of(most, T, T, C, G);
-    double least = cost(best, 32, 24);
+    best.roles = (long long)best.c_blocks * B <= cus;
+    double least = cost(best, best.roles ? 28.5 : 32, 22.5);
     const SsmPlan four = ssm_plan_of(4, T, T, C, G);
-    const double c4 = cost(four, 92, 62);
+    const double c4 = cost(four, 97, 58);
     if (c4 < least) {
         best = four;
         least = c4;
     }
     for (int len = 64; !one_pass && len * 2 <= T; len *= 2) {
         const SsmPlan p = ssm_plan_of(4, len, T, C, G);
-        const double c = cost(p, 92 + 75, 62 + 47) + 8000 + 150.0 * p.segs;
+        const double c = cost(p, 97 + 75, 58 + 44) + 4000 + 250.0 * p.segs;
         if (c < least && (__int128)p.c_blocks * p.segs * B <= kMaxGroups) {
             best = p;
             least = c;
