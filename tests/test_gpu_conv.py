@@ -251,3 +251,14 @@ def test_many_rows(rg, dtype, W):
     for b in range(c.B):
         assert torch.equal(new[int(c.idx[b])].double().cpu(), ref[2][int(c.idx[b])])
     c.check(*c.call(rg), ref, "in place")
+
+
+def test_longest_prompt(rg):
+    x = torch.randn(1, 65536, 16, generator=torch.Generator().manual_seed(20))
+    w, pool = torch.randn(16, 4), torch.randn(1, 3, 16)
+    want = torch.cat([pool, x], 1).double().unfold(1, 4, 1)
+    # five roundings of the terms' magnitudes
+    err = 5 * 2.0 ** -24 * (want * w.double()).abs().sum(-1)
+    out, after = rg.la_conv(x.cuda(), w.cuda(), pool.cuda(), silu=False)
+    check(out, (want * w.double()).sum(-1), err, "65536 tokens")
+    assert torch.equal(after.cpu(), x[:, -3:])

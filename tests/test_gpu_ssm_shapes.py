@@ -115,3 +115,11 @@ def test_groups_of_channels(rg):  # noqa: F811
         assert torch.equal(o, out[..., s])
         named = c.idx.long()
         assert torch.equal(one[named], after[named][:, s])
+
+
+def test_longest_prompt(rg):  # noqa: F811
+    c = Case(1, 65536, 8, 8, 1, "bf16", "f32", 23, lens=[65536], acc=[65536], slow=0.02)
+    ref = c.reference()
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+        out, after = c.call(rg, "ssm_prefill", pool=c.pool.clone(), workspace=ws)
+        c.check(out, after, ref, "65536 tokens")
