@@ -1,8 +1,9 @@
-// la_binding.cpp -- the quick half of the Python binding of the linear-attention entries: a CPython
-// module that looks whether a call's tensors are what the entry takes, allocates what is returned,
-// and makes the C call. It says nothing about a call that does not fit: it returns None, and the
-// package's Python checks then name what is wrong. (Through ctypes, with the checks in Python, a
-// call took 8 to 12 us of host time; a step for one sequence takes the GPU 3.4 us.)
+// la_binding.cpp -- the quick half of the Python binding of the linear-attention entries and of those
+// beside them (convolution, rotary positions, state space scan): a CPython module that looks whether a
+// call's tensors are what the entry takes, allocates what is returned, and makes the C call. It says
+// nothing about a call that does not fit: it returns None, and the package's Python checks then name what
+// is wrong. (Through ctypes, with the checks in Python, a call took 8 to 12 us of host time; a step for
+// one sequence takes the GPU 3.4 us.)
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

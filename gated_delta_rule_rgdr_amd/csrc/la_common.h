@@ -1,7 +1,7 @@
 // la_common.h -- what the linear-attention kernels (la_decode.hip, la_prefill.hip), the 8-bit
 // state pools (la_state.hip), the gated norm (la_norm_gate.hip), the short convolution (la_conv.hip),
-// rotary positions (la_rope.hip) and the state space scan (ssm_scan.hip) share: argument blocks, host
-// checks, the 8-bit block format and the rows' types. Not part of the C ABI.
+// rotary positions (la_rope.hip) and the state space scan (ssm_decode.hip, ssm_prefill.hip) share: argument
+// blocks, host checks, the 8-bit block format and the rows' types. Not part of the C ABI.
 #pragma once
 
 #include "rgdr_common.h"
