@@ -3,6 +3,7 @@
 
 namespace rgdr {
 
+constexpr int kXcds = 8;        // of the device, each with its own L2
 constexpr int kPieces = 256;  // a workgroup's threads: (token, 8 channels) pieces of a chunk
 
 // The sizes that go with WAYS lanes for each channel's states.
@@ -10,6 +11,7 @@ template <int N, int WAYS>
 struct SsmShape {
     static constexpr int NP = N / WAYS;                // states of a lane
     static constexpr int CW = 64 / WAYS, CH = 4 * CW;  // channels of a wave, of a workgroup
+    static constexpr int SHARE = 64 / CH;              // workgroups on a line of 128 bytes (of 16-bit rows)
     static constexpr int TPT = CH / 8, TC = kPieces / TPT;  // threads for each token, tokens of a chunk
     static constexpr int ROW = TC + 4;                 // floats of a channel's row in LDS
     static constexpr int ROWS = CH * ROW + (CH / 8 - 1) * 4;  // rows of 8 channels start 4 floats further
@@ -87,8 +89,9 @@ __device__ __forceinline__ void ssm_priority(int now, int &quarter) {
 // A workgroup's four waves do both in turn, and waves of other workgroups fill in: with four on a compute
 // unit the vector units are busy for 90 to 97% of the time (B=16, T=1024, C=4096, N=16, bf16: 236 us; ragged
 // 164). Where a compute unit has one workgroup at most (ROLES), four waves do the one and four others the other,
-// a chunk apart, in two sets of buffers: B=1, T=8192, C=512 206 us, and 276 with both in the same waves;
-// C=4096, T=300 15.4 and 17.0; with two workgroups there it is the other way round, 443 and 381 (C=8192).
+// a chunk apart, in two sets of buffers: B=1, T=8192, C=512 199 us, and 276 with both in the same waves;
+// C=4096, T=300 14.0 and 17.0; with two workgroups there it is the other way round, 443 and 381 (C=8192). Workgroups
+// of 16 channels that share lines run on one XCD: C=4096 211 us, and 233 when they go round the XCDs.
 template <typename E, int N, int WAYS, int PASS, bool ROLES>
 __global__ __launch_bounds__(ROLES ? 512 : 256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4) : 2)
 void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {
@@ -101,8 +104,14 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
     const int role = ROLES ? __builtin_amdgcn_readfirstlane(threadIdx.x / 256) : 0;
     const int tid = ROLES ? threadIdx.x % 256 : threadIdx.x;
     const bool by_channel = !ROLES || role == 0, by_token = !ROLES || role == 1;
-    const int cb = blockIdx.x % p.c_blocks, s = blockIdx.x / p.c_blocks % p.segs;
-    const int b = entry_of_rank(a.lens, a.B, a.T, blockIdx.x / p.c_blocks / p.segs);
+    int item = blockIdx.x;
+    if constexpr (S::SHARE > 1) {  // workgroups that share lines run on one XCD, and meet in its L2
+        const int local = item / kXcds;
+        item = (local / S::SHARE * kXcds + item % kXcds) * S::SHARE + local % S::SHARE;
+        if (item >= p.c_blocks * a.B) return;
+    }
+    const int cb = item % p.c_blocks, s = item / p.c_blocks % p.segs;
+    const int b = entry_of_rank(a.lens, a.B, a.T, item / p.c_blocks / p.segs);
     const LaEntry e = ssm_entry(a, b);
     const int t_begin = s * p.seg_len, t_end = min(e.L, t_begin + p.seg_len);
     if (PASS == kSsmEnds && t_begin + p.seg_len >= e.L) return;
@@ -437,8 +446,11 @@ __global__ __launch_bounds__(256) void ssm_ends_kernel(const SsmArgs a, const Ss
 template <typename E, int N, int WAYS, int PASS, bool ROLES = false>
 static rgdr_status launch_ssm_pass(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
     if ((__int128)p.c_blocks * p.segs * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
-    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS, ROLES>), dim3((unsigned)((long long)p.c_blocks * p.segs * a.B)),
-                       dim3(ROLES ? 512 : 256), 0, stream, a, p, f32);
+    using S = SsmShape<N, WAYS>;
+    constexpr int ROUND = S::SHARE > 1 ? S::SHARE * kXcds : 1;
+    const long long groups = ((long long)p.c_blocks * p.segs * a.B + ROUND - 1) / ROUND * ROUND;
+    hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS, ROLES>), dim3((unsigned)groups), dim3(ROLES ? 512 : 256), 0,
+                       stream, a, p, f32);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
 }
 
@@ -479,13 +491,13 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
 
 // How many lanes for each channel, and how many segments: what costs least by the model below, in ns, whose
 // rates were measured with N = 16. A chunk's tokens take a workgroup alone on its compute unit 97 ns each
-// with four lanes for each channel and 32 with 16, or 28.5 with roles; the vector units allow 58 for each
-// workgroup there with four lanes, the LDS 22.5 with 16 (a quarter of the channels); the last workgroup is alone
+// with four lanes for each channel and 30 with 16, or 26 with roles; the vector units allow 58 for each
+// workgroup there with four lanes, the LDS 20 with 16 (a quarter of the channels); the last workgroup is alone
 // for a while. Of a segment's two passes the first takes three quarters of the second; they and the scan
 // between them are three launches.
-// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 770/224/216 (256);
-// C=8192 760/381/416 (256); C=512 760/206/60 (256); C=2048, T=2048 194/57/46 (128); B=2, T=300, C=4096
-// 34/26/35 (64); B=4, T=1024 100/94/120 (128); B=8 135/187; B=16 236/362/375 (256).
+// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/211/214 (256);
+// C=8192 760/367/416 (256); C=512 760/199/50 (128); C=2048, T=2048 194/55/45 (128); B=2, T=300, C=4096
+// 34/24/35 (64); B=4, T=1024 100/82/120 (128); B=8 135/165; B=16 236/330/375 (256).
 static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
     const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
@@ -496,7 +508,7 @@ static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cu
     };
     SsmPlan best = ssm_plan_of(most, T, T, C, G);
     best.roles = (long long)best.c_blocks * B <= cus;
-    double least = cost(best, best.roles ? 28.5 : 32, 22.5);
+    double least = cost(best, best.roles ? 26 : 30, 20);
     const SsmPlan four = ssm_plan_of(4, T, T, C, G);
     const double c4 = cost(four, 97, 58);
     if (c4 < least) {
