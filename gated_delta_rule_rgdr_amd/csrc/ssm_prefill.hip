@@ -170,14 +170,6 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
     }
     if (PASS != kSsmEnds && s == 0 && e.state && e.n == 0 && !a.in_place && by_channel) commit(h);
 
-    if (st == 0 && by_token) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s_bias[sc + i] = c_ok && a.dt_bias ? a.dt_bias[cs + i] : 0.f;
-            s_D[sc + i] = c_ok && a.D ? a.D[cs + i] : 0.f;
-        }
-    }
-    __syncthreads();
     Row<E, 8> nx, dt, nz;
     nx.zero();
     dt.zero();
@@ -201,6 +193,19 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
         else if (PASS != kSsmEnds)
             bc.load(at(pC, st * dC + col * (uint32_t)sizeof(E)));
     };
+    Row<float, 8> bias0, D0;
+    bias0.zero();
+    D0.zero();
+    if (st == 0 && by_token && c_ok) {
+        if (a.dt_bias) bias0.load(a.dt_bias + cs);
+        if (a.D) D0.load(a.D + cs);
+    }
+    if (by_token) load(t_end - t_begin);  // on its way before the barrier
+    if (st == 0 && by_token) {
+        bias0.store(s_bias + sc);
+        D0.store(s_D + sc);
+    }
+    __syncthreads();
     // The chunk of nt tokens that was loaded last into LDS.
     const auto stage = [&](int set, int nt) {
         const bool live = st < nt;
@@ -339,7 +344,6 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
 
     int quarter = -1;
     if constexpr (!ROLES) {
-        load(t_end - t_begin);
         for (int t0 = t_begin; t0 < t_end;) {
             const int nt = tokens(t0);
             ssm_priority((int)((t_end - t0) * 4LL / (p.seg_len + 1)), quarter);
@@ -360,7 +364,6 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
         Row<E, 8> x = nx, z = nz, x1 = nx, z1 = nz;  // of the chunk before, and of the one being scanned
         int nt = tokens(t_begin), nt_before = 0, set = 0;
         if (by_token) {
-            load(t_end - t_begin);
             stage(0, nt);
             x1 = nx;
             z1 = nz;
