@@ -1052,8 +1052,9 @@ def la_rope_frequencies(rotary_dim, base=10000.0, *, scaling=None, scale=1.0, or
 
         def index(turns):  # of the pair that turns this often within original_length tokens
             return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
-        low, high = max(math.floor(index(fast_turns)), 0), min(math.ceil(index(slow_turns)), half - 1)
-        divided = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        low = max(math.floor(index(fast_turns)), 0)
+        high = min(math.ceil(index(slow_turns)), rotary_dim - 1)
+        divided = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0) if high > 0 else torch.ones_like(i)
         freq = freq * (1 - divided) + freq / scale * divided
         factor = 0.1 * math.log(scale) + 1.0
     return freq.to(torch.float32).to(device), factor

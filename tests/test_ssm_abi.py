@@ -173,3 +173,24 @@ def test_python_refuses_host_tensors():
     for call in (lambda: rg.la_conv([1.0], w, s), lambda: rg.la_rope(3, None, w), lambda: rg.ssm_decode(None, x, w, b, b, h)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_rope_frequencies_of_long_contexts():
+    """Where every pair turns often enough, none is divided; where none does, all are; and the ends of the
+    range between."""
+    i = torch.arange(16, dtype=torch.float64)
+    plain = 10000.0 ** (-i / 16)
+
+    def ratio(length):
+        freq, factor = rg.la_rope_frequencies(32, scaling="blend", scale=8.0, original_length=length, device="cpu")
+        assert abs(factor - 1.2079441541679836) < 1e-12  # 0.1 ln 8 + 1
+        return freq.double() / plain
+    few = ratio(4)        # pair 0 turns 4 / (2 pi) times
+    assert torch.allclose(few, torch.full_like(few, 0.125), rtol=1e-6)
+    many = ratio(10 ** 9)
+    assert torch.allclose(many, torch.ones_like(many), rtol=1e-6)
+    some = ratio(4096)
+    turns = 4096 * plain / (2 * torch.pi)
+    # the range between is widened to whole pairs, neighbours of which turn 1.78 times as often
+    assert torch.all(some[turns > 32 * 1.8] > 0.999) and torch.all(some[turns < 1 / 1.8] < 0.1251)
+    assert torch.all(some[1:] <= some[:-1] + 1e-6)
