@@ -123,3 +123,27 @@ def test_longest_prompt(rg):  # noqa: F811
     for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
         out, after = c.call(rg, "ssm_prefill", pool=c.pool.clone(), workspace=ws)
         c.check(out, after, ref, "65536 tokens")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("shape", [(1, 1000, 64, 16, 1), (2, 200, 128, 16, 2), (64, 37, 512, 16, 1), (1, 900, 64, 8, 1)], ids=str)
+def test_rejected_values_that_are_not_finite(rg, shape, value):  # noqa: F811
+    """In segments, with roles, with four lanes: the values of a rejected token stay out of the state, of the
+    outputs before it and, but for B, out of other channels."""
+    B, T, C, N, G = shape
+    t0 = T // 3 * 2
+    c = Case(*shape, "bf16", "f32", 24, lens=[T] * B, acc=[t0] * B, slow=0.05)
+    want, after = c.call(rg, "ssm_prefill", pool=c.pool.clone())
+    c.x[:, t0, 3] = value
+    c.dt[:, t0 + 1, 5] = value
+    c.z[:, t0 + 2, 6] = value
+    keep = c.pool.clone()
+    out, got = c.call(rg, "ssm_prefill")
+    assert torch.equal(got, after)
+    others = [i for i in range(C) if i not in (3, 5, 6)]
+    assert torch.equal(out[..., others], want[..., others])
+    assert torch.equal(out[:, :t0], want[:, :t0]) and not torch.isfinite(out[:, t0, 3]).any()
+    assert torch.equal(out[:, t0 + 3:, 6], want[:, t0 + 3:, 6])
+    c.Bm[:, t0] = value
+    out, got = c.call(rg, "ssm_prefill", pool=keep)
+    assert torch.equal(got, after) and torch.equal(out[:, :t0], want[:, :t0])
