@@ -500,17 +500,20 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
 // between them are three launches.
 // bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/211/214 (256);
 // C=8192 760/367/416 (256); C=512 760/199/50 (128); C=2048, T=2048 194/55/45 (128); B=2, T=300, C=4096
-// 34/24/35 (64); B=4, T=1024 100/82/120 (128); B=8 135/165; B=16 236/330/375 (256).
+// 34/24/35 (64); B=4, T=1024 100/82/120 (128); B=8 135/165; B=16 236/330/375 (256); B=3, C=1448 (273
+// workgroups of 16 lanes for each channel), T=6801 628/294/204 (512).
 static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
     const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
     const auto cost = [&](const SsmPlan &p, double alone, double beside) {
-        const double here = (double)p.c_blocks * B * p.segs / cus;  // workgroups for each compute unit
+        const long long groups = (long long)p.c_blocks * B * p.segs;
+        // workgroups for each compute unit; of few, those of the unit that has the most
+        const double here = groups < 8LL * cus ? (double)((groups + cus - 1) / cus) : (double)groups / cus;
         const double token = here * beside + (alone - beside) / 2;
         return size * p.seg_len * (token > alone ? token : alone);
     };
     SsmPlan best = ssm_plan_of(most, T, T, C, G);
-    best.roles = (long long)best.c_blocks * B <= cus;
+    best.roles = (long long)best.c_blocks * B <= cus && T > 8 * most;  // (one chunk has nothing to overlap)
     double least = cost(best, best.roles ? 26 : 30, 20);
     const SsmPlan four = ssm_plan_of(4, T, T, C, G);
     const double c4 = cost(four, 97, 58);
