@@ -552,6 +552,22 @@ extern "C" rgdr_status ssm_prefill_workspace_size(int32_t B, int32_t T, int32_t 
     return RGDR_OK;
 }
 
+// The form that a call of these sizes takes on `cus` compute units, for tests: lanes for each channel,
+// whether in roles, segments, tokens of a segment.
+extern "C" rgdr_status ssm_prefill_form(int32_t B, int32_t T, int32_t C, int32_t N, int32_t G, int32_t one_pass,
+                                        int32_t cus, int32_t form[4]) {
+    using namespace rgdr;
+    const rgdr_status rc = ssm_check_sizes(65536, B, T, C, N, G);
+    if (rc != RGDR_OK) return rc;
+    if (B < 1 || cus < 1) return RGDR_ERR_SHAPE;
+    const SsmPlan p = ssm_plan(B, T, C, N, G, one_pass != 0, cus);
+    form[0] = p.ways;
+    form[1] = p.roles;
+    form[2] = p.segs;
+    form[3] = p.seg_len;
+    return RGDR_OK;
+}
+
 extern "C" rgdr_status ssm_prefill(const void *x, const la_strides *x_strides, const void *dt,
                                    const la_strides *dt_strides, const float *A, const void *Bm,
                                    const la_strides *Bm_strides, const void *Cm, const la_strides *Cm_strides,
