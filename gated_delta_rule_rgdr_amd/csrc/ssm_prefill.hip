@@ -241,12 +241,12 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
 #pragma unroll
         for (int i = 0; i < S::NV; ++i) to[S::bc_at(0, i)] = f[i];
     };
-    const auto advance = [&](int nt) {
-        px += (uint32_t)nt * dx;
-        pdt += (uint32_t)nt * ddt;
-        pz += (uint32_t)nt * dz;
-        pB += (uint32_t)nt * dB;
-        pC += (uint32_t)nt * dC;
+    const auto advance = [&](int nt) {  // (up to 128 tokens of 2^25 bytes: 2^32)
+        px += (size_t)nt * dx;
+        pdt += (size_t)nt * ddt;
+        pz += (size_t)nt * dz;
+        pB += (size_t)nt * dB;
+        pC += (size_t)nt * dC;
     };
     float sum = 0.f;
     // The states over nt tokens; the sums over the states take the place of d x.

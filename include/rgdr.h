@@ -631,7 +631,8 @@ enum { SSM_DT_SOFTPLUS = 1u /* the step is softplus(dt + dt_bias), not dt + dt_b
  *   state_out  receives the state after the first num_accepted_tokens tokens in every slot that an
  *              entry names; other slots are not touched. It may be state_pool (in place: then a slot
  *              whose entry accepts no token keeps its bytes); any other overlap is undefined.
- * Rows start at multiples of 8 elements, bases are 16-byte aligned. The arithmetic is fp32; the
+ * Rows start at multiples of 8 elements, bases are 16-byte aligned; with T > 1, x, dt, z, Bm, Cm and
+ * out step at most 2^25 bytes from one token to the next. The arithmetic is fp32; the
  * state is rounded once, when it is committed. Padded tokens and skipped entries are never read; a
  * NaN or an infinity in a valid token shows in that token's outputs and in those of the tokens
  * behind it, in its channel (x, dt, z) or its group (Bm, Cm), and in the state if the token is accepted.
