@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void ssm_decode_tokens_kernel(const SsmArgs a,
     constexpr int P = 16 / sizeof(S), LPC = N / P, CH = 256 / LPC, PIECES = CH / 8;
     __shared__ __align__(16) float sd[kMaxT][CH], su[kMaxT][CH], sB[kMaxT][N], sC[kMaxT][N];
     const int b = blockIdx.x / c_blocks, cb = blockIdx.x % c_blocks;
-    const int Cg = a.C / a.G, per = (Cg + CH - 1) / CH, g = cb / per;
+    const int Cg = a.C / a.G, per = (Cg - 1) / CH + 1, g = cb / per;
     const int c0 = g * Cg + cb % per * CH, channels = min(CH, Cg - cb % per * CH);
     const LaEntry e = ssm_entry(a, b);
 
@@ -231,7 +231,7 @@ static rgdr_status launch_ssm_tokens(const SsmArgs &a, hipStream_t stream) {
     const int Cg = a.C / a.G;
     const bool large = (long long)a.B * a.G * (Cg / CH) >= 2048;
     const bool tokens = Cg >= CH && (a.T >= 5 || (a.T >= 3 && large));
-    const long long c_blocks = tokens ? (long long)a.G * ((Cg + CH - 1) / CH) : ((long long)a.C + CH - 1) / CH;
+    const long long c_blocks = tokens ? (long long)a.G * ((Cg - 1) / CH + 1) : ((long long)a.C + CH - 1) / CH;
     const long long b_blocks = a.T > 1 ? a.B : ((long long)a.B + 1) / 2;
     if ((__int128)c_blocks * b_blocks > kMaxGroups) return RGDR_ERR_SHAPE;
     const dim3 grid((unsigned)(c_blocks * b_blocks)), block(256);

@@ -119,7 +119,7 @@ void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) 
     // by token and 8 channels: a uniform address, which moves on by chunks, and a thread's own 32-bit offset
     // (127 tokens at strides of at most 2^25 bytes)
     const int st = tid / S::TPT, sc = tid % S::TPT * 8;
-    const int Cg = a.C / a.G, per = (Cg + S::CH - 1) / S::CH, g = cb / per;  // this workgroup's group,
+    const int Cg = a.C / a.G, per = (Cg - 1) / S::CH + 1, g = cb / per;  // this workgroup's group,
     const int c0 = g * Cg + cb % per * S::CH, channels = min(S::CH, Cg - cb % per * S::CH);  // and channels
     const int cs = c0 + sc;
     const bool c_ok = sc < channels;
@@ -484,7 +484,7 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
     SsmPlan p;
     const int CH = 256 / ways;
     p.ways = ways;
-    p.c_blocks = G * ((C / G + CH - 1) / CH);
+    p.c_blocks = G * ((C / G - 1) / CH + 1);
     p.seg_len = seg_len;
     p.segs = (T + seg_len - 1) / seg_len;
     p.roles = false;
