@@ -446,12 +446,18 @@ __global__ __launch_bounds__(256) void ssm_ends_kernel(const SsmArgs a, const Ss
     ends[last * step / 4] = f32x4{h[0], h[1], h[2], h[3]};
 }
 
+// The workgroups of a launch: with more than four lanes for a channel, whole rounds of the XCDs of those that
+// share lines.
+static long long ssm_groups(const SsmPlan &p, int B) {
+    const long long round = p.ways > 4 ? (long long)p.ways / 4 * kXcds : 1;
+    const __int128 n = (__int128)p.c_blocks * p.segs * B;
+    return n > kMaxGroups ? kMaxGroups + 1 : ((long long)n + round - 1) / round * round;
+}
+
 template <typename E, int N, int WAYS, int PASS, bool ROLES = false>
 static rgdr_status launch_ssm_pass(const SsmArgs &a, const SsmPlan &p, bool f32, hipStream_t stream) {
-    if ((__int128)p.c_blocks * p.segs * a.B > kMaxGroups) return RGDR_ERR_SHAPE;
-    using S = SsmShape<N, WAYS>;
-    constexpr int ROUND = S::SHARE > 1 ? S::SHARE * kXcds : 1;
-    const long long groups = ((long long)p.c_blocks * p.segs * a.B + ROUND - 1) / ROUND * ROUND;
+    const long long groups = ssm_groups(p, a.B);
+    if (groups > kMaxGroups) return RGDR_ERR_SHAPE;
     hipLaunchKernelGGL((ssm_prefill_kernel<E, N, WAYS, PASS, ROLES>), dim3((unsigned)groups), dim3(ROLES ? 512 : 256), 0,
                        stream, a, p, f32);
     return hipGetLastError() == hipSuccess ? RGDR_OK : RGDR_ERR_HIP;
@@ -501,7 +507,8 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
 // bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/211/214 (256);
 // C=8192 760/367/416 (256); C=512 760/199/50 (128); C=2048, T=2048 194/55/45 (128); B=2, T=300, C=4096
 // 34/24/35 (64); B=4, T=1024 100/82/120 (128); B=8 135/165; B=16 236/330/375 (256); B=3, C=1448 (273
-// workgroups of 16 lanes for each channel), T=6801 628/294/204 (512).
+// workgroups of 16 lanes for each channel), T=6801 628/294/204 (512). A form whose workgroups are more than a
+// launch may have is no candidate.
 static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
     const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
@@ -517,14 +524,14 @@ static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cu
     double least = cost(best, best.roles ? 26 : 30, 20);
     const SsmPlan four = ssm_plan_of(4, T, T, C, G);
     const double c4 = cost(four, 97, 58);
-    if (c4 < least) {
+    if (c4 < least || ssm_groups(best, B) > kMaxGroups) {
         best = four;
         least = c4;
     }
     for (int len = 64; !one_pass && len * 2 <= T; len *= 2) {
         const SsmPlan p = ssm_plan_of(4, len, T, C, G);
         const double c = cost(p, 97 + 75, 58 + 44) + 4000 + 250.0 * p.segs;
-        if (c < least && (__int128)p.c_blocks * p.segs * B <= kMaxGroups) {
+        if (c < least && ssm_groups(p, B) <= kMaxGroups) {
             best = p;
             least = c;
         }
@@ -586,7 +593,7 @@ extern "C" rgdr_status ssm_prefill(const void *x, const la_strides *x_strides, c
                   B, T, C, N, G, N_slots, out, out_strides, state_out);
     if (rc != RGDR_OK || B == 0) return rc;
     if (workspace && !aligned(workspace, 256)) return RGDR_ERR_ALIGN;
-    if ((__int128)ssm_plan_of(4, T, T, C, G).c_blocks * B > kMaxGroups) return RGDR_ERR_SHAPE;
+    if (ssm_groups(ssm_plan_of(4, T, T, C, G), B) > kMaxGroups) return RGDR_ERR_SHAPE;
     const int cus = la_compute_units();
     if (cus == 0) return RGDR_ERR_HIP;
     SsmPlan p = ssm_plan(B, T, C, N, G, false, cus);

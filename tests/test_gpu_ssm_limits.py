@@ -44,3 +44,25 @@ def test_softplus_over_its_range(rg, fn):  # noqa: F811
     # a step below 2^-126 may be zero
     err = (out.double().cpu() - want).abs() - (3 * dt.double().abs() + 16) * U * want - TINY[torch.float32] - HALF[torch.float32] * want
     assert err.max() <= 0, f"off by {float(err.max()):.3g} more than the bound at dt = {float(dt.flatten()[err.argmax()])}"
+
+
+def test_more_workgroups_than_the_wider_form_may_have(rg):  # noqa: F811
+    """300000 entries of 2048 channels: 19 million workgroups with 8 lanes for each channel, 9.6 with four. All
+    entries but three have no slot; their rows are zeros."""
+    B, C, N = 300000, 2048, 8
+    assert prefill_form(B, 1, C, N, 1)[0] == 4
+    c = Case(3, 1, C, N, 1, "bf16", "f32", 32, slots=3, lens=[1] * 3, acc=[1] * 3, idx=[2, 0, 1], layout="whole")
+    ref = c.reference()
+    at = [0, 123457, B - 1]
+
+    def rows(t):
+        wide = torch.zeros(B, *t.shape[1:], dtype=t.dtype, device="cuda")
+        wide[at] = t
+        return wide
+    idx = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    idx[at] = c.idx.cuda()
+    out, after = rg.ssm_prefill(rows(c.x), rows(c.dt), c.A, rows(c.Bm), rows(c.Cm), c.pool, None, idx, D=c.D,
+                                z=rows(c.z), dt_bias=c.bias)
+    c.check(out[at], after, ref, "300000 entries")
+    out[at] = 0
+    assert not out.any()
