@@ -31,9 +31,11 @@ it finds that a call does not fit, the checks here say why. It is loaded by the 
 A non-OK status from the library raises ``RuntimeError`` (the page's error behaviour).
 
 With ``RGDR_VALIDATE=1`` in the environment (read at import; ``VALIDATE`` holds it), every
-decode call first checks its index arrays with ``rgdr_validate``: a synchronous copy to the
-host, for debugging only (it cannot run under graph capture). A bad length, count or slot
-then raises ``RuntimeError`` instead of being clamped or skipped by the kernel.
+call that takes lengths, accepted counts or slots of entries first checks them with
+``rgdr_validate``: a synchronous copy to the host, for debugging only (it cannot run under graph
+capture). A bad length, count or slot then raises ``RuntimeError`` instead of being clamped or
+skipped by the kernel. (``la_state_quantize`` and ``la_state_dequantize``, whose slots may be out
+of range, check nothing.)
 """
 import ctypes as C
 import math
@@ -828,6 +830,21 @@ def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
     return codes, scales
 
 
+def _norm_refuse(x, weight, gate, lens, out):
+    _rows(x, "x", tuple(_DTYPE_CODE))
+    B, H, T, D = x.shape
+    for nm, t in (("gate", gate), ("out", out)):
+        if t is not None:
+            _rows(t, nm, (x.dtype,))
+            if tuple(t.shape) != (B, T, H, D):
+                raise RuntimeError(f"{nm} must be [B, T, H, D]")
+    if not isinstance(weight, torch.Tensor) or tuple(weight.shape) not in ((D,), (H, D)):
+        raise RuntimeError("weight must be a [D] or [H, D] tensor")
+    _dev(weight, "weight", torch.float32)
+    _index(lens, "actual_seq_lengths", B)
+    _same_device(x, weight=weight, gate=gate, out=out, actual_seq_lengths=lens)
+
+
 def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_lengths=None,
                  out=None, stream=None):
     """The norm and gate behind the attention: ``weight * x / sqrt(mean(x^2) + eps) *
@@ -840,24 +857,17 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
     ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
     if _quick is None:
         _load_quick()
-    if stream is not None and out is None and isinstance(x, torch.Tensor) and x.dim() == 4:
+    if stream is not None or VALIDATE:
+        _norm_refuse(x, weight, gate, actual_seq_lengths, out)
         B, H, T, D = x.shape
-        out = _empty((B, T, H, D), x.dtype, x.device, stream)
+        if VALIDATE:
+            _validate_lengths(actual_seq_lengths, T)
+        if out is None and stream is not None:
+            out = _empty((B, T, H, D), x.dtype, x.device, stream)
     done = _quick.norm_gate(x, weight, gate, eps, LA_GATE_SIGMOID if sigmoid else 0,
                             actual_seq_lengths, out, _raw_stream(x, stream))
     if done is None:
-        _rows(x, "x", tuple(_DTYPE_CODE))
-        B, H, T, D = x.shape
-        for nm, t in (("gate", gate), ("out", out)):
-            if t is not None:
-                _rows(t, nm, (x.dtype,))
-                if tuple(t.shape) != (B, T, H, D):
-                    raise RuntimeError(f"{nm} must be [B, T, H, D]")
-        if not isinstance(weight, torch.Tensor) or tuple(weight.shape) not in ((D,), (H, D)):
-            raise RuntimeError("weight must be a [D] or [H, D] tensor")
-        _dev(weight, "weight", torch.float32)
-        _index(actual_seq_lengths, "actual_seq_lengths", B)
-        _same_device(x, weight=weight, gate=gate, out=out, actual_seq_lengths=actual_seq_lengths)
+        _norm_refuse(x, weight, gate, actual_seq_lengths, out)
         raise RuntimeError("la_norm_gate: unsupported arguments")
     rc, out = done
     if rc:
@@ -871,6 +881,12 @@ def _validate_given(lens, idx, nacc, B, T, N, device):
         return t if t is not None else torch.as_tensor(other, dtype=torch.int32, device=device)
     n = given(lens, [T] * B)
     _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N)
+
+
+def _validate_lengths(lens, T):
+    """The same of a call whose only index array is its lengths."""
+    if lens is not None and lens.shape[0] and T:
+        _validate_given(lens, None, None, lens.shape[0], T, lens.shape[0], lens.device)
 
 
 def _tokens(t, name, dtypes, shape):
@@ -1002,11 +1018,13 @@ def la_rope(query, key, inv_freq, positions=None, *, interleaved=False, factor=1
     ``actual_seq_lengths`` (int32 ``[B]``) are zero."""
     if _quick is None:
         _load_quick()
-    if stream is not None:
+    if stream is not None or VALIDATE:
         _rope_refuse(query, key, inv_freq, positions, actual_seq_lengths, query_out, key_out)
-        if query_out is None:
+        if VALIDATE:
+            _validate_lengths(actual_seq_lengths, query.shape[2])
+        if query_out is None and stream is not None:
             query_out = _empty(query.shape, query.dtype, query.device, stream)
-        if key_out is None and key is not None:
+        if key_out is None and key is not None and stream is not None:
             key_out = _empty(key.shape, key.dtype, key.device, stream)
     done = _quick.rope(query, key, inv_freq, positions, actual_seq_lengths, factor,
                        LA_ROPE_INTERLEAVED if interleaved else 0, query_out, key_out,
