@@ -30,6 +30,9 @@ it finds that a call does not fit, the checks here say why. It is loaded by the 
 
 A non-OK status from the library raises ``RuntimeError`` (the page's error behaviour).
 
+Calls run on the current stream, or on the one given as ``stream``: what they read has to be ready
+there, and their results are (tensors may be dropped as soon as a call returns).
+
 With ``RGDR_VALIDATE=1`` in the environment (read at import; ``VALIDATE`` holds it), every
 call that takes lengths, accepted counts or slots of entries first checks them with
 ``rgdr_validate``: a synchronous copy to the host, for debugging only (it cannot run under graph
@@ -181,8 +184,8 @@ def _same_device(ref, **tensors):
             raise RuntimeError(f"{name} is on {t.device}, expected {ref.device}")
 
 
-def _validate_indices(lens, idx, nacc, T, N):
-    code = rgdr_validate(lens, idx, nacc, T, N)
+def _validate_indices(lens, idx, nacc, T, N, stream):
+    code = rgdr_validate(lens, idx, nacc, T, N, stream)
     _check(code, "index arrays (RGDR_VALIDATE)")
 
 
@@ -233,7 +236,7 @@ def rgdr_decode_snapshots(query, key, value, beta, state_pool, actual_seq_length
     its slot is valid, and holds the state after its first ``t + 1`` tokens; other entries
     keep what the buffer held.
     """
-    state_snapshots = _snapshot_buffer(query, value, state_pool, state_snapshots)
+    state_snapshots = _snapshot_buffer(query, value, state_pool, state_snapshots, stream)
     out, state_out = _plain_call("rgdr_decode_snapshots", query, key, value, beta, state_pool,
                                  actual_seq_lengths, ssm_state_indices, g, gk,
                                  num_accepted_tokens, scale, out, state_out, stream,
@@ -241,7 +244,7 @@ def rgdr_decode_snapshots(query, key, value, beta, state_pool, actual_seq_length
     return out, state_out, state_snapshots
 
 
-def _snapshot_buffer(query, value, state_pool, state_snapshots):
+def _snapshot_buffer(query, value, state_pool, state_snapshots, stream):
     """The per-token state buffer of a snapshot call: checked, or allocated uninitialised."""
     if not isinstance(query, torch.Tensor) or not isinstance(value, torch.Tensor) \
             or not isinstance(state_pool, torch.Tensor):
@@ -251,7 +254,7 @@ def _snapshot_buffer(query, value, state_pool, state_snapshots):
     B, _, T, Dk = query.shape
     Hv, Dv = value.shape[1], value.shape[3]
     if state_snapshots is None:
-        return torch.empty((B, T, Hv, Dk, Dv), dtype=torch.bfloat16, device=query.device)
+        return _empty((B, T, Hv, Dk, Dv), torch.bfloat16, query.device, stream)
     _dev(state_snapshots, "state_snapshots", torch.bfloat16, 5)
     if tuple(state_snapshots.shape) != (B, T, Hv, Dk, Dv):
         raise RuntimeError("state_snapshots must be [B, T, H_v, D_k, D_v]")
@@ -279,13 +282,13 @@ def rgdr_prefill_workspace_size(B, H_v, T, D_k, D_v, device=None):
     return n.value
 
 
-def _workspace(query, value, state_pool, workspace):
+def _workspace(query, value, state_pool, workspace, stream):
     """The caller's workspace (a uint8 CUDA tensor), or one allocated for the call."""
     if workspace is None:
         B, _, T, Dk = query.shape
         Hv, Dv = value.shape[1], value.shape[3]
         nbytes = rgdr_prefill_workspace_size(B, Hv, T, Dk, Dv, query.device)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=query.device)
+        workspace = _empty(max(nbytes, 1), torch.uint8, query.device, stream)
     if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise RuntimeError("workspace must be a contiguous uint8 CUDA tensor")
     return workspace
@@ -297,7 +300,7 @@ def rgdr_prefill_ws(query, key, value, beta, state_pool, actual_seq_lengths, ssm
     """``rgdr_prefill`` with a workspace (a uint8 CUDA tensor of at least
     ``rgdr_prefill_workspace_size`` bytes; allocated for the call when None). Calls of few
     sequences then evaluate all segments of a sequence at once."""
-    workspace = _workspace(query, value, state_pool, workspace)
+    workspace = _workspace(query, value, state_pool, workspace, stream)
     return _plain_call("rgdr_prefill_ws", query, key, value, beta, state_pool,
                        actual_seq_lengths, ssm_state_indices, g, gk, num_accepted_tokens, scale,
                        out, state_out, stream, workspace=workspace)
@@ -340,7 +343,7 @@ def _plain_call(fn, query, key, value, beta, state_pool, actual_seq_lengths, ssm
             or tuple(gk.shape) != (B, Hv, T, Dk) or tuple(state_pool.shape) != (N, Hv, Dk, Dv):
         raise RuntimeError(f"{fn}: inconsistent shapes")
     if out is None:
-        out = torch.empty((B, Hv, T, Dv), dtype=torch.bfloat16, device=query.device)
+        out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
     else:
         _dev(out, "out", torch.bfloat16, 4)
         if tuple(out.shape) != (B, Hv, T, Dv):
@@ -356,7 +359,8 @@ def _plain_call(fn, query, key, value, beta, state_pool, actual_seq_lengths, ssm
                  g=g, gk=gk, num_accepted_tokens=num_accepted_tokens, out=out,
                  state_out=state_out, **extra)
     if VALIDATE:
-        _validate_indices(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N)
+        _validate_indices(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N,
+                          stream)
     with torch.cuda.device(query.device):
         rc = getattr(lib, fn)(query.data_ptr(), key.data_ptr(), value.data_ptr(),
                               beta.data_ptr(), state_pool.data_ptr(),
@@ -366,6 +370,8 @@ def _plain_call(fn, query, key, value, beta, state_pool, actual_seq_lengths, ssm
                               state_out.data_ptr(), *[t.data_ptr() for t in extra.values()],
                               *_ws_args(workspace, query), _stream_handle(stream, query.device))
     _check(rc, fn)
+    _hold(stream, query, key, value, beta, state_pool, actual_seq_lengths, ssm_state_indices, g, gk,
+          num_accepted_tokens, out, state_out, workspace, *extra.values())
     return out, state_out
 
 
@@ -400,7 +406,7 @@ def rgdr_decode_gated_snapshots(query, key, value, a, b, dt_bias, decay_scale, s
     """``rgdr_decode_gated`` that also stores the state after every token, as
     ``rgdr_decode_snapshots`` extends ``rgdr_decode``; returns
     ``(out, state_out, state_snapshots)`` with the buffer as described there."""
-    state_snapshots = _snapshot_buffer(query, value, state_pool, state_snapshots)
+    state_snapshots = _snapshot_buffer(query, value, state_pool, state_snapshots, stream)
     out, state_out = _gated_call("rgdr_decode_gated_snapshots", query, key, value, a, b,
                                  dt_bias, decay_scale, state_pool, actual_seq_lengths,
                                  ssm_state_indices, gk, num_accepted_tokens, scale,
@@ -426,7 +432,7 @@ def rgdr_prefill_gated_ws(query, key, value, a, b, dt_bias, decay_scale, state_p
                           state_out=None, stream=None):
     """``rgdr_prefill_gated`` with a workspace, as ``rgdr_prefill_ws`` extends
     ``rgdr_prefill``."""
-    workspace = _workspace(query, value, state_pool, workspace)
+    workspace = _workspace(query, value, state_pool, workspace, stream)
     return _gated_call("rgdr_prefill_gated_ws", query, key, value, a, b, dt_bias, decay_scale,
                        state_pool, actual_seq_lengths, ssm_state_indices, gk,
                        num_accepted_tokens, scale, normalize_qk, out, state_out, stream,
@@ -464,7 +470,7 @@ def _gated_call(fn, query, key, value, a, b, dt_bias, decay_scale, state_pool,
             or dt_bias.shape[0] != Hv or decay_scale.shape[0] != Hv:
         raise RuntimeError(f"{fn}: inconsistent shapes")
     if out is None:
-        out = torch.empty((B, Hv, T, Dv), dtype=torch.bfloat16, device=query.device)
+        out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
     else:
         _dev(out, "out", torch.bfloat16, 4)
         if tuple(out.shape) != (B, Hv, T, Dv):
@@ -481,7 +487,8 @@ def _gated_call(fn, query, key, value, a, b, dt_bias, decay_scale, state_pool,
                  gk=gk, num_accepted_tokens=num_accepted_tokens, out=out, state_out=state_out,
                  **extra)
     if VALIDATE:
-        _validate_indices(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N)
+        _validate_indices(actual_seq_lengths, ssm_state_indices, num_accepted_tokens, T, N,
+                          stream)
     with torch.cuda.device(query.device):
         rc = getattr(lib, fn)(query.data_ptr(), key.data_ptr(), value.data_ptr(),
                               a.data_ptr(), b.data_ptr(), dt_bias.data_ptr(),
@@ -494,6 +501,8 @@ def _gated_call(fn, query, key, value, a, b, dt_bias, decay_scale, state_pool,
                               NORMALIZE_QK if normalize_qk else 0,
                               *_ws_args(workspace, query), _stream_handle(stream, query.device))
     _check(rc, fn)
+    _hold(stream, query, key, value, a, b, dt_bias, decay_scale, state_pool, actual_seq_lengths,
+          ssm_state_indices, gk, num_accepted_tokens, out, state_out, workspace, *extra.values())
     return out, state_out
 
 
@@ -538,13 +547,12 @@ def la_gate(a, dt_bias, decay_scale, b=None, *, want_beta=None, decay_dtype=None
             raise RuntimeError("b must have a's shape")
     decay_dtype = decay_dtype or a.dtype
     if decay_out is None:
-        decay_out = torch.empty(a.shape, dtype=decay_dtype, device=a.device)
+        decay_out = _empty(a.shape, decay_dtype, a.device, stream)
     _dev(decay_out, "decay_out", decay_dtype)
     beta_t = None
     if want_beta:
         beta_dtype = beta_dtype or a.dtype
-        beta_t = beta_out if beta_out is not None else torch.empty(a.shape, dtype=beta_dtype,
-                                                                   device=a.device)
+        beta_t = beta_out if beta_out is not None else _empty(a.shape, beta_dtype, a.device, stream)
         _dev(beta_t, "beta_out", beta_dtype)
     n_rows = a.numel() // H if H else 0
     _same_device(a, dt_bias=dt_bias, decay_scale=decay_scale, b=b, decay_out=decay_out,
@@ -557,6 +565,7 @@ def la_gate(a, dt_bias, decay_scale, b=None, *, want_beta=None, decay_dtype=None
                          _dtype_code(beta_dtype, "beta_out") if beta_t is not None else 0,
                          _stream_handle(stream, a.device))
     _check(rc, "la_gate")
+    _hold(stream, a, dt_bias, decay_scale, b, decay_out, beta_t)
     return decay_out, beta_t
 
 
@@ -585,15 +594,33 @@ def _index(t, name, n):
     return t.data_ptr()
 
 
+def _torch_stream(stream, device):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor for a kernel on `stream`. The allocator hands out memory whose earlier use is
-    over on the stream it allocates for, so it is asked with that stream current."""
+    over on the stream it allocates for, so it is asked with that stream current; what the caller
+    does with the tensor on the stream that is current now also ends before its memory is handed
+    out again."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _hold(stream, *tensors):
+    """A call on a stream of its own: the caller may drop the tensors once it returns (a slot array
+    made for the call), so their memory is not handed out again before the kernels are over."""
+    if stream is None:
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(_torch_stream(stream, t.device))
 
 
 _STATE_TYPES = (torch.float32, torch.bfloat16, torch.int8)
@@ -687,6 +714,9 @@ def _la_call(fn, query, key, value, g, state_pool, lens, idx, nacc, scale, state
     rc, out = done
     if rc:
         _check(rc, fn)
+    if stream is not None:
+        _hold(stream, query, key, value, g, state_pool, state_scales, lens, idx, nacc, out, state_out,
+              state_scales_out, workspace)
     return (out, state_out) if state_scales is None else (out, state_out, state_scales_out)
 
 
@@ -699,7 +729,7 @@ def _la_prepare(fn, query, key, value, g, state_pool, lens, idx, nacc, state_sca
     B, Hq, T, Dk = query.shape
     Hv, Dv = value.shape[1], value.shape[3]
     if VALIDATE and B:
-        _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], query.device)
+        _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], query.device, stream)
     if stream is not None:
         if out is None:
             out = _empty((B, Hv, T, Dv), torch.bfloat16, query.device, stream)
@@ -827,6 +857,7 @@ def _move(fn, state, codes, scales, src_slots, dst_slots, n, stream):
         raise RuntimeError(f"{fn}: unsupported arguments")
     if rc:
         _check(rc, fn)
+    _hold(stream, state, codes, scales, src_slots, dst_slots)
     return codes, scales
 
 
@@ -861,7 +892,7 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
         _norm_refuse(x, weight, gate, actual_seq_lengths, out)
         B, H, T, D = x.shape
         if VALIDATE:
-            _validate_lengths(actual_seq_lengths, T)
+            _validate_lengths(actual_seq_lengths, T, stream)
         if out is None and stream is not None:
             out = _empty((B, T, H, D), x.dtype, x.device, stream)
     done = _quick.norm_gate(x, weight, gate, eps, LA_GATE_SIGMOID if sigmoid else 0,
@@ -872,21 +903,24 @@ def la_norm_gate(x, weight, gate=None, *, eps=1e-6, sigmoid=False, actual_seq_le
     rc, out = done
     if rc:
         _check(rc, "la_norm_gate")
+    if stream is not None:
+        _hold(stream, x, weight, gate, actual_seq_lengths, out)
     return out
 
 
-def _validate_given(lens, idx, nacc, B, T, N, device):
+def _validate_given(lens, idx, nacc, B, T, N, device, stream):
     """rgdr_validate of a call's index arrays, any of which may be left out."""
     def given(t, other):
         return t if t is not None else torch.as_tensor(other, dtype=torch.int32, device=device)
     n = given(lens, [T] * B)
-    _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N)
+    _validate_indices(n, given(idx, range(B)), nacc if nacc is not None else n, T, N, stream)
 
 
-def _validate_lengths(lens, T):
+def _validate_lengths(lens, T, stream):
     """The same of a call whose only index array is its lengths."""
     if lens is not None and lens.shape[0] and T:
-        _validate_given(lens, None, None, lens.shape[0], T, lens.shape[0], lens.device)
+        _validate_given(lens, None, None, lens.shape[0], T, lens.shape[0], lens.device,
+                        stream)
 
 
 def _tokens(t, name, dtypes, shape):
@@ -961,7 +995,7 @@ def la_conv(x, weight, state_pool, actual_seq_lengths=None, ssm_state_indices=No
                      num_accepted_tokens, out, state_out)
         if VALIDATE and x.shape[0]:
             _validate_given(actual_seq_lengths, ssm_state_indices, num_accepted_tokens,
-                            x.shape[0], x.shape[1], state_pool.shape[0], x.device)
+                            x.shape[0], x.shape[1], state_pool.shape[0], x.device, stream)
         if out is None and stream is not None:
             out = _empty(x.shape, x.dtype, x.device, stream)
     done = _quick.conv(x, weight, bias, state_pool, actual_seq_lengths, ssm_state_indices,
@@ -974,6 +1008,9 @@ def la_conv(x, weight, state_pool, actual_seq_lengths=None, ssm_state_indices=No
     rc, out = done
     if rc:
         _check(rc, "la_conv")
+    if stream is not None:
+        _hold(stream, x, weight, bias, state_pool, actual_seq_lengths, ssm_state_indices,
+              num_accepted_tokens, out, state_out)
     return out, state_out
 
 
@@ -1021,7 +1058,7 @@ def la_rope(query, key, inv_freq, positions=None, *, interleaved=False, factor=1
     if stream is not None or VALIDATE:
         _rope_refuse(query, key, inv_freq, positions, actual_seq_lengths, query_out, key_out)
         if VALIDATE:
-            _validate_lengths(actual_seq_lengths, query.shape[2])
+            _validate_lengths(actual_seq_lengths, query.shape[2], stream)
         if query_out is None and stream is not None:
             query_out = _empty(query.shape, query.dtype, query.device, stream)
         if key_out is None and key is not None and stream is not None:
@@ -1035,6 +1072,8 @@ def la_rope(query, key, inv_freq, positions=None, *, interleaved=False, factor=1
     rc, query_out, key_out = done
     if rc:
         _check(rc, "la_rope")
+    if stream is not None:
+        _hold(stream, query, key, inv_freq, positions, actual_seq_lengths, query_out, key_out)
     return query_out, key_out
 
 
@@ -1120,7 +1159,7 @@ def _ssm_call(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, 
                     state_out, workspace)
         B, T, Ch = x.shape
         if VALIDATE and B:
-            _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], x.device)
+            _validate_given(lens, idx, nacc, B, T, state_pool.shape[0], x.device, stream)
         if stream is not None:
             if out is None:
                 out = _empty(x.shape, x.dtype, x.device, stream)
@@ -1138,6 +1177,9 @@ def _ssm_call(fn, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, 
     rc, out = done
     if rc:
         _check(rc, fn)
+    if stream is not None:
+        _hold(stream, x, dt, A, Bm, Cm, state_pool, lens, idx, nacc, D, z, dt_bias, out, state_out,
+              workspace)
     return out, state_out
 
 
