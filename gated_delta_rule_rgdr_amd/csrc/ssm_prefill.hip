@@ -498,39 +498,53 @@ static SsmPlan ssm_plan_of(int ways, int seg_len, int T, int C, int G) {
     return p;
 }
 
-// How many lanes for each channel, and how many segments: what costs least by the model below, in ns, whose
-// rates were measured with N = 16. A chunk's tokens take a workgroup alone on its compute unit 97 ns each
-// with four lanes for each channel and 30 with 16, or 26 with roles; the vector units allow 58 for each
-// workgroup there with four lanes, the LDS 20 with 16 (a quarter of the channels); the last workgroup is alone
-// for a while. Of a segment's two passes the first takes three quarters of the second; they and the scan
-// between them are three launches.
-// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 760/211/214 (256);
-// C=8192 760/367/416 (256); C=512 760/199/50 (128); C=2048, T=2048 194/55/45 (128); B=2, T=300, C=4096
-// 34/24/35 (64); B=4, T=1024 100/82/120 (128); B=8 135/165; B=16 236/330/375 (256); B=3, C=1448 (273
-// workgroups of 16 lanes for each channel), T=6801 628/294/204 (512). A form whose workgroups are more than a
-// launch may have is no candidate.
-static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool one_pass, int cus) {
+// What a token takes a workgroup in ns: alone on its compute unit (in roles), and each of several there.
+struct SsmRates {
+    double alone, roles, beside;
+};
+
+// How many lanes for each channel, and how many segments: what costs least by the model below, in ns. A chunk's
+// tokens take a workgroup alone on its compute unit 97 ns each with four lanes for each channel and 30 with 16,
+// or 26 with roles; the vector units allow 58 for each workgroup there with four lanes, the LDS 20 with 16 (a
+// quarter of the channels); the last workgroup is alone for a while. Of a segment's two passes the first takes
+// three quarters of the second; they and the scan between them are three launches. Those are N = 16's rates; N = 32
+// takes 5 / 3 of them. N = 8 has its own, for its wider form is one of eight lanes with half of the channels and a
+// state each: 72 and 42 with four lanes, 39, 32 and 22.5 with eight; in fp32, where a compute unit holds
+// fewer workgroups of four lanes, 63 in place of 42, and 30 of 22.5.
+// bf16, us, 4 lanes / 16 lanes / 4 lanes in segments (of tokens): B=1, C=4096, T=8192 751/203/220 (512);
+// C=8192 760/367/416 (256); C=512 758/194/52 (128); C=2048, T=2048 192/55/44 (128); B=2, T=300, C=4096
+// 33/19/30 (64); B=4, T=1024 100/80/108 (256); B=8 137/159; B=16 240/338/375 (256); B=3, C=1448 (273
+// workgroups of 16 lanes for each channel), T=6801 628/294/204 (512).
+// N=32: B=16, T=1024, C=4096 427/565; B=4 150/138/194 (256); B=1, T=8192 1149/323/378 (512); C=512 1152/315/75 (128).
+// N=8, 4 lanes / 8 lanes / segments: B=16, T=1024, C=4096 184/197 (fp32 274/248); B=8 105/93; B=4 78/57/78 (256);
+// B=64, T=300, C=1024 56/71 (fp32 87/78); B=1, T=8192, C=4096 585/263/158 (512); C=512 582/249/43 (128).
+// The segments go by 16-bit rows' rates, so that the workspace's size does not depend on the type. A form whose
+// workgroups are more than a launch may have is no candidate.
+static SsmPlan ssm_plan(int B, int T, int C, int N, int G, bool f32, bool one_pass, int cus) {
     const int most = N < 16 ? N : 16;
-    const double size = (8.0 + N) / 24;  // of a token's work, against N = 16
-    const auto cost = [&](const SsmPlan &p, double alone, double beside) {
+    const double size = N == 8 ? 1 : (8.0 + N) / 24;  // of a token's work, against N = 16
+    const auto wide = [&](bool f32) {
+        return N == 8 ? SsmRates{39, 32, f32 ? 30 : 22.5} : SsmRates{30, 26, 20};
+    };
+    const auto four = [&](bool f32) { return N == 8 ? SsmRates{72, 0, f32 ? 63.0 : 42.0} : SsmRates{97, 0, 58}; };
+    const SsmRates parts = N == 8 ? SsmRates{126, 0, 73.5} : SsmRates{97 + 75, 0, 58 + 44};
+    const auto cost = [&](const SsmPlan &p, const SsmRates &r) {
         const long long groups = (long long)p.c_blocks * B * p.segs;
         // workgroups for each compute unit; of few, those of the unit that has the most
         const double here = groups < 8LL * cus ? (double)((groups + cus - 1) / cus) : (double)groups / cus;
-        const double token = here * beside + (alone - beside) / 2;
+        const double alone = p.roles ? r.roles : r.alone, token = here * r.beside + (alone - r.beside) / 2;
         return size * p.seg_len * (token > alone ? token : alone);
     };
-    SsmPlan best = ssm_plan_of(most, T, T, C, G);
-    best.roles = (long long)best.c_blocks * B <= cus && T > 8 * most;  // (one chunk has nothing to overlap)
-    double least = cost(best, best.roles ? 26 : 30, 20);
-    const SsmPlan four = ssm_plan_of(4, T, T, C, G);
-    const double c4 = cost(four, 97, 58);
-    if (c4 < least || ssm_groups(best, B) > kMaxGroups) {
-        best = four;
-        least = c4;
-    }
+    SsmPlan in_wide = ssm_plan_of(most, T, T, C, G);
+    in_wide.roles = (long long)in_wide.c_blocks * B <= cus && T > 8 * most;  // (one chunk has nothing to overlap)
+    const SsmPlan in_four = ssm_plan_of(4, T, T, C, G);
+    const bool fits = ssm_groups(in_wide, B) <= kMaxGroups;
+    SsmPlan best = fits && cost(in_wide, wide(f32)) <= cost(in_four, four(f32)) ? in_wide : in_four;
+    double least = cost(in_four, four(false));
+    if (fits && cost(in_wide, wide(false)) < least) least = cost(in_wide, wide(false));
     for (int len = 64; !one_pass && len * 2 <= T; len *= 2) {
         const SsmPlan p = ssm_plan_of(4, len, T, C, G);
-        const double c = cost(p, 97 + 75, 58 + 44) + 4000 + 250.0 * p.segs;
+        const double c = cost(p, parts) + 4000 + 250.0 * p.segs;
         if (c < least && ssm_groups(p, B) <= kMaxGroups) {
             best = p;
             least = c;
@@ -555,19 +569,19 @@ extern "C" rgdr_status ssm_prefill_workspace_size(int32_t B, int32_t T, int32_t 
     if (B == 0) return RGDR_OK;
     const int cus = la_compute_units();
     if (cus == 0) return RGDR_ERR_HIP;
-    *bytes = ssm_workspace(ssm_plan(B, T, C, N, G, false, cus), B, C, N);
+    *bytes = ssm_workspace(ssm_plan(B, T, C, N, G, false, false, cus), B, C, N);
     return RGDR_OK;
 }
 
-// The form that a call of these sizes takes on `cus` compute units, for tests: lanes for each channel,
-// whether in roles, segments, tokens of a segment.
-extern "C" rgdr_status ssm_prefill_form(int32_t B, int32_t T, int32_t C, int32_t N, int32_t G, int32_t one_pass,
-                                        int32_t cus, int32_t form[4]) {
+// The form that a call of these sizes (with rows of fp32, or of 16 bits) takes on `cus` compute units, for tests:
+// lanes for each channel, whether in roles, segments, tokens of a segment.
+extern "C" rgdr_status ssm_prefill_form(int32_t B, int32_t T, int32_t C, int32_t N, int32_t G, int32_t f32,
+                                        int32_t one_pass, int32_t cus, int32_t form[4]) {
     using namespace rgdr;
     const rgdr_status rc = ssm_check_sizes(65536, B, T, C, N, G);
     if (rc != RGDR_OK) return rc;
     if (B < 1 || cus < 1) return RGDR_ERR_SHAPE;
-    const SsmPlan p = ssm_plan(B, T, C, N, G, one_pass != 0, cus);
+    const SsmPlan p = ssm_plan(B, T, C, N, G, f32 != 0, one_pass != 0, cus);
     form[0] = p.ways;
     form[1] = p.roles;
     form[2] = p.segs;
@@ -596,8 +610,9 @@ extern "C" rgdr_status ssm_prefill(const void *x, const la_strides *x_strides, c
     if (ssm_groups(ssm_plan_of(4, T, T, C, G), B) > kMaxGroups) return RGDR_ERR_SHAPE;
     const int cus = la_compute_units();
     if (cus == 0) return RGDR_ERR_HIP;
-    SsmPlan p = ssm_plan(B, T, C, N, G, false, cus);
-    if (!workspace || workspace_bytes < ssm_workspace(p, B, C, N)) p = ssm_plan(B, T, C, N, G, true, cus);
+    const bool wide_rows = dtype == RGDR_F32;
+    SsmPlan p = ssm_plan(B, T, C, N, G, wide_rows, false, cus);
+    if (!workspace || workspace_bytes < ssm_workspace(p, B, C, N)) p = ssm_plan(B, T, C, N, G, wide_rows, true, cus);
     if (p.segs > 1) {
         p.ends = static_cast<float *>(workspace);
         p.sums = p.ends + (size_t)B * p.segs * C * N;

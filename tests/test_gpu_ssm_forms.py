@@ -17,6 +17,7 @@ FORMS = [  # B, T, C, N, G; lanes for each channel, roles
     ((3, 300, 536, 16, 1), 16, True),
     ((2, 270, 520, 32, 1), 16, True),
     ((4, 210, 200, 8, 5), 8, True),
+    ((20, 75, 2056, 8, 1), 4, False),     # (in fp32 eight lanes)
 ]
 
 
@@ -25,7 +26,9 @@ FORMS = [  # B, T, C, N, G; lanes for each channel, roles
 def test_forms(rg, shape, ways, roles, types):  # noqa: F811
     """Full lengths (no count shortens a chunk), then ragged ones with counts within chunks."""
     B, T, C, N, G = shape
-    assert prefill_form(*shape, one_pass=True) == (ways, roles, 1, T)
+    if types[0] == "f32" and (N, ways) == (8, 4):
+        ways = 8
+    assert prefill_form(*shape, one_pass=True, f32=types[0] == "f32") == (ways, roles, 1, T)
     none = torch.empty(0, dtype=torch.uint8, device="cuda")
     for lens, acc in (([T] * B, [T] * B), ("ragged", "ragged")):
         c = Case(*shape, *types, seed=sum(shape), lens=lens, acc=acc, slow=0.05)
@@ -37,7 +40,7 @@ def test_forms(rg, shape, ways, roles, types):  # noqa: F811
 
 
 def test_four_lanes_for_few_states(rg):  # noqa: F811
-    """N = 8 in four lanes for each channel, several chunks: the form of calls whose grid would be too large with
+    """N = 8 in four lanes for each channel, several chunks, with more workgroups than the grid could have with
     eight. All entries but four have no slot; inputs are one row for all of them."""
     B, T, G, N = 65536, 45, 129, 8
     C = 40 * G
