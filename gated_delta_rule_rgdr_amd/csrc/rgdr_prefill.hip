@@ -333,7 +333,10 @@ __global__ __launch_bounds__(256, RGDR_PREFILL_MIN_WAVES) void prefill_kernel(
         it = (rest / sg.nseg) * a.ntiles + tl;
     }
     const Item m = resolve(a, x, it);
-    const int L = m.L, n = m.n;
+    // A skipped entry has no tokens (L = 0) and must have no segments either, whatever its count: one that
+    // took [0, n) for its own would write there while the first segment clears the entry's rows. (Decoding and
+    // the single pass go by L alone, and need not wait for the slot before they use the count.)
+    const int L = m.L, n = SEG != 0 && !m.state ? 0 : m.n;
     // Tokens tbeg .. tend - 1 of the entry; the chunk holding ncut (the accepted prefix's
     // end) stops there. A segment is seg_len tokens of [0, n), or of [n, L) after the
     // ceil(n / seg_len) segments of the prefix.
