@@ -66,7 +66,7 @@ __device__ __forceinline__ float ssm_meet(float (&y)[WAYS]) {
 
 // The wave's priority by the quarter of the tokens that it still has before it. Of waves alike the oldest
 // goes first, so that the last workgroup of a compute unit would run the longer alone, at half of the vector units'
-// rate: B=16, T=1024, C=4096 257 us without and 240 with, ragged 191 and 183.
+// rate. (This change alone: B=16, T=1024, C=4096 257 us without it and 240 with it, ragged 191 and 183.)
 __device__ __forceinline__ void ssm_priority(int now, int &quarter) {
     if (now == quarter) return;
     quarter = now;
@@ -87,11 +87,12 @@ __device__ __forceinline__ void ssm_priority(int now, int &quarter) {
 // tokens. d, d x and the sums over the states pass between the two through LDS, as do B and C in fp32.
 //
 // A workgroup's four waves do both in turn, and waves of other workgroups fill in: with four on a compute
-// unit the vector units are busy for 90 to 97% of the time (B=16, T=1024, C=4096, N=16, bf16: 236 us; ragged
+// unit the vector units are busy for 90 to 97% of the time (B=16, T=1024, C=4096, N=16, bf16: 240 us; ragged
 // 164). Where a compute unit has one workgroup at most (ROLES), four waves do the one and four others the other,
-// a chunk apart, in two sets of buffers: B=1, T=8192, C=512 199 us, and 276 with both in the same waves;
-// C=4096, T=300 14.0 and 17.0; with two workgroups there it is the other way round, 443 and 381 (C=8192). Workgroups
-// of 16 channels that share lines run on one XCD: C=4096 211 us, and 233 when they go round the XCDs.
+// a chunk apart, in two sets of buffers (in one pass, with roles and without: B=1, T=8192, C=512 194 us and 257;
+// C=4096 203 and 264; T=300 14.0 and 17.0; with two workgroups there it is the other way round, 443 and 381 for
+// C=8192). Workgroups of 16 channels that share lines run on one XCD (C=4096 211 us, and 233 when they go round the
+// XCDs, before the first chunk's loads were moved ahead of the barrier).
 template <typename E, int N, int WAYS, int PASS, bool ROLES>
 __global__ __launch_bounds__(ROLES ? 512 : 256, WAYS == 4 && N <= 16 ? (sizeof(E) == 4 ? 3 : 4) : 2)
 void ssm_prefill_kernel(const SsmArgs a, const SsmPlan p, const bool state_f32) {

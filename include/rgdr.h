@@ -572,8 +572,8 @@ enum {
  * la_rope -- rotary positions. Pair i < R / 2 of each query and key row's first R columns is turned
  * by its token's angle a = position * inv_freq[i]:
  *     (u, v) -> factor (u cos a - v sin a, u sin a + v cos a);
- * the other D - R columns are copied. The angle is a 64-bit product, so that far positions lose
- * nothing; the rest is fp32, rounded once.
+ * the other D - R columns are copied. The angle is a 64-bit product (off by at most 2^-51 of its
+ * value), taken to 2^-26 of a turn; the rest is fp32, rounded once.
  *
  *   query      [B, H_q, T, D], key [B, H_k, T, D] of dtype (RGDR_F32, RGDR_F16 or RGDR_BF16) with
  *              their strides (NULL: contiguous), the layout of la_decode's. key may be NULL if

@@ -1,5 +1,6 @@
 """Every row of an output is written, whatever the buffer held before: entries without a slot that have lengths and
-counts, empty ones, short ones; each form of the convolution, rotary positions and the state space scan."""
+counts, empty ones, short ones; each form of the convolution, rotary positions, the state space scan, linear attention
+and the gated delta rule."""
 import pytest
 import torch
 
@@ -106,3 +107,47 @@ def test_the_scan_s_forms():
     seen = {prefill_form(B, T, C, N, G)[:2] + (prefill_form(B, T, C, N, G)[2] > 1,)
             for fn, B, T, C, N, G in SCANS if fn == "ssm_prefill"}
     assert seen >= {(4, False, False), (4, False, True), (16, False, False), (16, True, False), (8, True, False)}, seen
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("fn,T,D", [("la_decode", 1, 64), ("la_decode", 5, 128), ("la_prefill", 70, 64),
+                                    ("la_prefill", 900, 128)])
+def test_linear_attention(rg, fn, T, D, state):
+    B = 6
+    lens, idx, acc = entries(B, T)
+    r = torch.Generator(device="cuda").manual_seed(T)
+    q, k = (torch.nn.functional.normalize(torch.randn(B, 2, T, D, generator=r, device="cuda"), dim=-1).bfloat16()
+            for _ in range(2))
+    v, g = torch.randn(B, 4, T, 96, generator=r, device="cuda").bfloat16(), -torch.rand(B, 4, T, generator=r, device="cuda")
+    pool, scales = torch.randn(B + 2, 4, D, 96, generator=r, device="cuda"), None
+    if state == "bf16":
+        pool = pool.bfloat16()
+    if state == "i8":
+        pool, scales = rg.la_state_quantize(pool)
+
+    def make(out):
+        return getattr(rg, fn)(q, k, v, g, pool.clone(), ints(lens), ints(idx), ints(acc), out=out,
+                               state_scales=None if scales is None else scales.clone())[0]
+    both(make, v.shape, torch.bfloat16, valid_rows(lens, idx, T, B + 2)[:, None].expand(B, 4, T))
+
+
+@pytest.mark.parametrize("fn,T,Dk,Dv", [
+    ("rgdr_decode", 1, 128, 128), ("rgdr_decode", 1, 64, 512), ("rgdr_decode", 2, 64, 64), ("rgdr_decode", 8, 128, 128),
+    ("rgdr_decode", 8, 64, 512), ("rgdr_prefill", 40, 128, 128), ("rgdr_prefill", 40, 64, 256),
+    ("rgdr_prefill_ws", 900, 128, 128), ("rgdr_prefill_ws", 900, 64, 256), ("rgdr_prefill_noalloc", 900, 128, 64)])
+def test_gated_delta_rule(rg, fn, T, Dk, Dv):
+    B = 6
+    lens, idx, acc = entries(B, T)
+    r = torch.Generator(device="cuda").manual_seed(T)
+    q, k = (torch.nn.functional.normalize(torch.randn(B, 2, T, Dk, generator=r, device="cuda"), dim=-1).bfloat16()
+            for _ in range(2))
+    v = torch.randn(B, 4, T, Dv, generator=r, device="cuda").bfloat16()
+    beta = torch.rand(B, 4, T, generator=r, device="cuda").bfloat16()
+    g, gk = -torch.rand(B, 4, T, generator=r, device="cuda"), -0.1 * torch.rand(B, 4, T, Dk, generator=r, device="cuda")
+    pool = torch.randn(B + 2, 4, Dk, Dv, generator=r, device="cuda").bfloat16()
+    if fn in ("rgdr_prefill_ws", "rgdr_prefill_noalloc"):
+        assert rg.rgdr_prefill_workspace_size(B, 4, T, Dk, Dv) > 0
+
+    def make(out):
+        return getattr(rg, fn)(q, k, v, beta, pool.clone(), ints(lens), ints(idx), g, gk, ints(acc), out=out)[0]
+    both(make, v.shape, torch.bfloat16, valid_rows(lens, idx, T, B + 2)[:, None].expand(B, 4, T))
