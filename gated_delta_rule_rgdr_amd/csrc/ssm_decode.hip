@@ -278,7 +278,7 @@ rgdr_status ssm_check(SsmArgs &a, int max_t, const void *x, const la_strides *x_
     if (!x || !dt || !A || !Bm || !Cm || !state_pool || !out || !state_out) return RGDR_ERR_NULL;
     a.sx = la_strides_or(x_strides, (long long)T * C, 0, C);
     a.sdt = la_strides_or(dt_strides, (long long)T * C, 0, C);
-    a.sz = la_strides_or(z_strides, (long long)T * C, 0, C);
+    a.sz = la_strides_or(z ? z_strides : nullptr, (long long)T * C, 0, C);
     a.so = la_strides_or(out_strides, (long long)T * C, 0, C);
     a.sB = la_strides_or(Bm_strides, (long long)T * G * N, N, (long long)G * N);
     a.sC = la_strides_or(Cm_strides, (long long)T * G * N, N, (long long)G * N);

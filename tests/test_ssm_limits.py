@@ -3,7 +3,7 @@ made-up addresses are never used)."""
 import pytest
 
 from ssm_form import prefill_form
-from test_ssm_abi import BF16, SHAPE, lib, scan  # noqa: F401  (lib is a fixture)
+from test_ssm_abi import ALIGN, BF16, SHAPE, lib, scan  # noqa: F401  (lib is a fixture)
 
 MOST = (1 << 31) - 8  # the most channels that an int32 holds
 
@@ -55,3 +55,11 @@ def test_the_workspace_does_not_go_by_the_type():
                 for N in (8, 16, 32):
                     a, b = (prefill_form(B, T, C, N, 1, f32=f) for f in (False, True))
                     assert a[2:] == b[2:]
+
+
+@pytest.mark.parametrize("fn", ["ssm_decode", "ssm_prefill"])
+@pytest.mark.parametrize("strides", [(-1, 0, 64), (256, 0, 68), (1 << 61, 0, 64)], ids=str)
+def test_strides_of_no_gate_say_nothing(lib, fn, strides):  # noqa: F811
+    """Without z its strides are not looked at: the call is refused for what follows in the checks."""
+    assert scan(lib, fn, z=None, zs=strides, lens=0x100002) == ALIGN
+    assert scan(lib, fn, zs=strides, lens=0x100002) in (SHAPE, ALIGN)
