@@ -31,7 +31,7 @@ it finds that a call does not fit, the checks here say why. It is loaded by the 
 A non-OK status from the library raises ``RuntimeError`` (the page's error behaviour).
 
 Calls run on the current stream, or on the one given as ``stream``: what they read has to be ready
-there, and their results are (tensors may be dropped as soon as a call returns).
+there, and what they write is ready there behind them. Tensors may be dropped when a call returns.
 
 With ``RGDR_VALIDATE=1`` in the environment (read at import; ``VALIDATE`` holds it), every
 call that takes lengths, accepted counts or slots of entries first checks them with

@@ -135,3 +135,51 @@ def test_dropped_tensors(rg, beside, fn, foreign):
         if waited:
             return
     pytest.skip("the work before the call was over too soon")
+
+
+POOL = {"ssm_prefill": 5, "la_conv": 2, "la_rope": None, "la_prefill": 4, "rgdr_prefill_ws": 4}  # the states' argument
+
+
+@pytest.mark.parametrize("fn", POOL)
+def test_captured_on_its_own_stream(rg, fn):
+    """The stream given is the one that captures: tensors made and dropped within the capture, four replays with
+    eager work between them."""
+    args, kw = inputs(fn)
+
+    def gpu(t):
+        return t.cuda() if isinstance(t, torch.Tensor) else t
+    fixed, kw = [gpu(t) for t in args], {k: gpu(v) for k, v in kw.items()}
+    pool_at = POOL[fn]
+
+    def call(stream, pool):
+        now = list(fixed)
+        if pool_at is not None:
+            now[pool_at] = pool
+        now[0] = now[0] + 0  # a tensor of the capture's own
+        out = getattr(rg, fn)(*now, **kw, stream=stream)
+        return [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+    first = fixed[pool_at].clone() if pool_at is not None else None
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pool = first.clone() if first is not None else None
+    with torch.cuda.stream(s):
+        want = [t.clone() for t in call(s, pool)]
+    torch.cuda.synchronize()
+    if pool is not None:
+        pool.copy_(first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = call(s, pool)
+    for k in range(4):
+        if pool is not None:
+            pool.copy_(first)
+        for t in got:
+            if pool is None or t.data_ptr() != pool.data_ptr():
+                t.zero_()
+        torch.ones(1 << 20, device="cuda").sum()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), k
